@@ -319,6 +319,110 @@ int qdq_llama_launches(const qdq_llama *model);
 void qdq_llama_destroy(qdq_llama *model);
 
 /* ---------------------------------------------------------------------------
+ * Serving several sequences: a paged key/value cache, the append of new tokens
+ * to it, attention of a chunk of new tokens over it, and sampling. No
+ * counterpart on the pages: the same step as qdq_rope_attention and the head's
+ * argmax ("S21 The Capstone: picoLM, in Python", section 4) for a batch of
+ * sequences of any lengths, prompts and single tokens alike.
+ *
+ * The cache is two pools of pages owned by the caller, keys and values, each
+ * [n_layers][n_pages][page_size][n_kv_heads][head_dim] of fp16 or bf16. Which
+ * page holds which positions is the caller's to decide: position j of a
+ * sequence lives in row j % page_size of page page_table[seq][j / page_size].
+ * A handle keeps the geometry, the rotation's frequency table and the attention's
+ * workspace (all device memory it needs: the calls allocate nothing).
+ *
+ * A step's batch (all arrays int32 on the device, 4-byte aligned, read when the
+ * kernels run, so a captured graph replays with their new contents):
+ *   q_start[n_seqs + 1]  the new tokens of sequence s are rows q_start[s] ..
+ *                        q_start[s+1] - 1 of q, k, v; starts at 0, never falls
+ *                        and never exceeds n_tokens. Rows from q_start[n_seqs]
+ *                        on belong to no sequence: their outputs are not written.
+ *   kv_len[n_seqs]       positions of the sequence, the new tokens included: its
+ *                        token i of n is at position kv_len - n + i.
+ *   page_table[n_seqs][max_pages]  page numbers; a position whose entry is not in
+ *                        [0, n_pages), or is past max_pages pages, is absent: it
+ *                        is not written and not attended to.
+ * n_seqs <= 1024, max_pages * page_size <= 2^30 (QDQ_ERR_LIMIT).
+ * ------------------------------------------------------------------------- */
+enum qdq_float_type { QDQ_F32 = 1, QDQ_F16 = 2, QDQ_BF16 = 3 };
+
+typedef struct qdq_paged_config {
+    int32_t type;             /* of the pools: QDQ_F16 or QDQ_BF16 */
+    int32_t n_layers, n_pages;
+    int32_t page_size;        /* 16, 32, 64, 128 or 256 positions */
+    int32_t n_heads, n_kv_heads; /* n_heads a multiple of n_kv_heads, at most 32 times it */
+    int32_t head_dim;         /* 64 or 128 */
+    int32_t rope_dim;         /* leading dims of a head that turn: a multiple of 8 in 0..head_dim */
+    int32_t rope_interleaved; /* 1: pairs (2i, 2i+1); 0: pairs (i, i + rope_dim/2) */
+    float rope_base;          /* pair i turns by position * rope_base^(-2i/rope_dim) */
+} qdq_paged_config;
+typedef struct qdq_paged_batch {
+    int32_t n_seqs, n_tokens, max_pages, reserved;
+    const int32_t *q_start, *kv_len, *page_table;
+} qdq_paged_batch;
+typedef struct qdq_paged qdq_paged;
+/* The pools must outlive the handle. Calls of one handle must not overlap on the
+ * GPU (they share the workspace); use one handle per stream otherwise. */
+int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, qdq_paged **out);
+void qdq_paged_destroy(qdq_paged *cache);
+
+/* qdq_paged_append: one pass over the new tokens' q, k and v rows.
+ *   y = x / sqrt(mean(x^2) + eps) * w over each head (q_norm, k_norm: fp32
+ *       [head_dim], or NULL for none),
+ *   q and k turned at their token's position (angles reduced exactly, so far
+ *   positions lose nothing), all arithmetic in fp32,
+ *   q_out[n_tokens][n_heads * head_dim] = q in the pools' type; k and v rounded
+ *   to the pools' type and stored in `layer` of the pools (one rounding each).
+ * in_type: QDQ_F32 (a GEMV's output) or the pools' type. Row strides are in
+ * elements; every row 16-byte aligned. A token at a negative position (kv_len
+ * below its sequence's new tokens) gets a zero q_out row and is not stored. */
+int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, int in_type, const void *q,
+                     int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                     const float *q_norm, const float *k_norm, float eps, void *q_out, qdq_stream_t stream);
+
+/* qdq_paged_attention: for token t at position p of its sequence and query head h
+ * with kv head h / (n_heads / n_kv_heads),
+ *   out[t][h] = sum_j a_j v_j,  a = softmax_j(scale * q . k_j),
+ * over the sequence's positions j <= p, and j > p - window when window > 0.
+ * q: [n_tokens][n_heads * head_dim] of the pools' type (append's q_out), out: of
+ * the pools' type or QDQ_F32; row strides in elements, rows 16-byte aligned.
+ * lse (NULL or fp32 [n_tokens][n_heads]): log sum_j exp(scale * q . k_j).
+ * Scores, maxima, sums and the accumulator are fp32; the softmax weights are
+ * rounded to the pools' type before they meet v (as its matrix product takes
+ * them), so an fp32 out is accurate to about that rounding too. A token with
+ * nothing to attend to gets a zero row and lse = -inf. Keys and values of
+ * positions outside a sequence's range are never used, whatever they hold.
+ * One launch; results do not depend on timing (no floating-point atomics). */
+int qdq_paged_attention(qdq_paged *cache, int layer, const qdq_paged_batch *batch, const void *q, int64_t q_stride,
+                        int out_type, void *out, int64_t out_stride, float scale, int window, float *lse,
+                        qdq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * qdq_sample: the next token of each row of logits, from given random numbers.
+ * logits: rows x vocab of `type` (QDQ_F32, QDQ_F16, QDQ_BF16), row stride in
+ * elements. Per row (device arrays of `rows`, 4-byte aligned; NULL switches the
+ * filter off, a NULL temperature is 1):
+ *   weights w_i = exp((l_i - max l) * (1 / temperature)) in fp32, entries ordered
+ *   by logit, the lowest index first among equals;
+ *   top_k  keeps the first top_k entries (<= 0: all);
+ *   top_p  of those, keeps an entry while the mass before it is < top_p times
+ *          their mass (>= 1: all; the first is always kept);
+ *   min_p  of those, keeps entries with w_i >= min_p (min_p above 1 counts as 1);
+ *   tokens[row] = the first index, in index order, at which the running mass of
+ *   the kept entries exceeds u[row] times their whole mass (u in [0, 1); at u = 1
+ *   the last kept index).
+ * temperature <= 0 takes the largest logit, the lowest index on ties. Masses are
+ * summed in 64-bit fixed point (units of 2^-44 of the largest weight), so they do
+ * not depend on any order. NaN logits count as -inf; a row with nothing above
+ * -inf gives token -1 and log-probability -inf. logprobs (may be NULL): the log
+ * of the chosen entry's share of the kept mass. vocab <= 2^18 (QDQ_ERR_LIMIT).
+ * ------------------------------------------------------------------------- */
+int qdq_sample(int type, const void *logits, int64_t stride, int rows, int vocab, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int64_t *tokens,
+               float *logprobs, qdq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * qdq_quantize: fp32 values -> PETIT q8_0 or q4_0 blocks, the exporter's step
  * ("PETIT", What makes it fast & small; How the pieces match: q8_0 = fp32 scale
  * + 32 int8, q4_0 = fp16 scale + 16 nibble bytes read as (q - 8) * d, low

@@ -48,8 +48,8 @@ static bool main_type(int type) {
 }
 static int check_type(int type) { return (main_type(type) || is_more_type(type)) ? QDQ_OK : QDQ_ERR_TYPE; }
 
-// Device (or managed) memory of the current device, 16-byte aligned.
-static int check_dev_ptr(const void *p, int device) {
+// Device (or managed) memory of the current device, aligned.
+int check_dev_ptr(const void *p, int device, int align) {
     if (p == nullptr) return QDQ_ERR_PTR;
     cudaPointerAttributes attr;
     if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
@@ -58,7 +58,7 @@ static int check_dev_ptr(const void *p, int device) {
     }
     if (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) return QDQ_ERR_PTR;
     if (attr.type == cudaMemoryTypeDevice && attr.device != device) return QDQ_ERR_PTR;
-    if (((uintptr_t)p & 15) != 0) return QDQ_ERR_ALIGN;
+    if (((uintptr_t)p & (uintptr_t)(align - 1)) != 0) return QDQ_ERR_ALIGN;
     return QDQ_OK;
 }
 

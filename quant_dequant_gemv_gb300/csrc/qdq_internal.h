@@ -21,6 +21,8 @@ const DeviceInfo &current_device(int *status);
 // (qdq_api.cu): shapes and device pointers, and the plan level sequence.
 int check_descs(const qdq_gemv_desc *descs, int n, int batch, int device);
 int check_levels(const int *level, int n, int max_levels, int *nlevels);
+// Device (or managed) memory of `device` at a multiple of `align` bytes (qdq_api.cu).
+int check_dev_ptr(const void *p, int device, int align = 16);
 
 int launch_dequant(int type, const void *blocks, int64_t n, float *out, cudaStream_t stream, int sm_count);
 int launch_quantize(int type, const float *x, int64_t n, void *blocks, cudaStream_t stream, int sm_count);
@@ -68,6 +70,23 @@ int launch_wait_selftest(int64_t limit_ns, cudaStream_t stream);
 int launch_mma_gemv(int type, const void *W, int64_t rows, int64_t cols, const float *x, float *y,
                     int batch, cudaStream_t stream, int sm_count);
 int take_status_mma();
+
+// The paged cache's attention kernels (qdq_attend.cu); the handle and the append
+// are in qdq_paged.cu.
+struct AttendArgs {
+    int n_seqs, n_tokens, max_pages;
+    const int32_t *q_start, *kv_len, *page_table;
+    const void *q;      // [n_tokens][n_heads * head_dim] of the pools' type
+    void *out;          // of the pools' type, or fp32
+    float *lse;         // [n_tokens][n_heads], or NULL
+    const void *k_pages, *v_pages;  // one layer
+    int64_t q_stride, out_stride;   // elements
+    float scale;
+    int window;         // 0: none
+    int n_pages, page_size, n_heads, n_kv_heads, head_dim;
+    bool bf16, out_f32;
+};
+int launch_attend(const AttendArgs &a, cudaStream_t stream, int sm_count);
 
 // While a caller's stream is being captured into a CUDA graph, one-time setup calls
 // (kernel attributes, occupancy queries, memory-pool creation) would invalidate a

@@ -1,0 +1,335 @@
+// qdq_paged.cu -- the paged key/value cache: the handle, its argument checks, and
+// the append of a step's new tokens (head norms, rotation and the cache write in
+// one pass). The attention over the cache is in qdq_attend.cu.
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "qdq_internal.h"
+#include "qdq_paged.cuh"
+
+namespace qdq {
+namespace {
+
+struct AppendArgs {
+    int n_seqs, n_tokens, max_pages;
+    const int32_t *q_start, *kv_len, *page_table;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements
+    const float *q_norm, *k_norm;
+    const uint64_t *freq;  // turns per position of pair i, in units of 2^-64
+    void *q_out, *k_pages, *v_pages;
+    float eps;
+    int n_heads, n_kv_heads, rope_dim, n_pages, page_shift, rows_per_warp, splits;
+};
+
+// 8 consecutive values of the input type as floats.
+template <typename TI>
+QDQ_DEV void load4(const TI *p, float *x) {
+    if constexpr (sizeof(TI) == 4) {
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        const float2 a = Float16<TI>::unpack(v.x), b = Float16<TI>::unpack(v.y);
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    }
+}
+
+// A group of D/8 lanes takes one head row, eight values a lane. A lane's values are
+// whole rotation pairs: in the interleaved layout eight consecutive values, in the
+// split layout four from each half of the turning dims (lanes past the turning dims
+// hold eight consecutive values either way), so the rotation needs no exchange
+// between lanes, the norm's sum is log2(D/8) shuffles, and every load and store is a
+// vector. A warp takes `rows_per_warp` of one token's n_heads + 2 n_kv_heads rows: a
+// lane sits at the same place of every row, so the angles are formed once per warp.
+// Angles: position * frequency in turns, modulo one turn, is a 64-bit integer product
+// that wraps (the frequency is kept in units of 2^-64 turn), so its error is 2^-65
+// turn per position whatever the position; the fraction then goes through sincospi.
+template <typename TI, typename TC, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
+    constexpr int G = D / 8, RW = 32 / G;  // lanes per row, rows per warp step
+    const int lane = threadIdx.x & 31, u = lane % G, sub = lane / G;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int t = (int)(unit / a.splits);
+    if (t >= a.n_tokens) return;
+    const int rows = a.n_heads + 2 * a.n_kv_heads;
+    const int r0 = (int)(unit % a.splits) * a.rows_per_warp, r1 = min(r0 + a.rows_per_warp, rows);
+
+    const int s = find_seq(a.q_start, a.n_seqs, t);
+    if (s < 0) return;
+    int first, count;
+    seq_tokens(a.q_start, s, a.n_tokens, first, count);
+    if (t < first || t >= first + count) return;  // a row of no sequence
+    const int p = max(a.kv_len[s], 0) - count + (t - first);
+    int64_t slot = -1;
+    if (p >= 0 && (p >> a.page_shift) < a.max_pages) {
+        const int page = a.page_table[(int64_t)s * a.max_pages + (p >> a.page_shift)];
+        if (page >= 0 && page < a.n_pages) slot = ((int64_t)page << a.page_shift) + (p & ((1 << a.page_shift) - 1));
+    }
+
+    const bool turns = 8 * u < a.rope_dim;
+    // the lane's first four and last four values
+    const int c0 = !INTERLEAVED && turns ? 4 * u : 8 * u;
+    const int c1 = !INTERLEAVED && turns ? a.rope_dim / 2 + 4 * u : 8 * u + 4;
+    float cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        cs[i] = 1.0f, sn[i] = 0.0f;
+        if (turns) {
+            const int32_t frac = (int32_t)(uint32_t)((a.freq[4 * u + i] * (uint64_t)(uint32_t)p) >> 32);
+            sincospif((float)frac * 0x1p-31f, &sn[i], &cs[i]);
+        }
+    }
+    float wq[8], wk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = i < 4 ? c0 + i : c1 + i - 4;
+        wq[i] = a.q_norm ? a.q_norm[c] : 1.0f;
+        wk[i] = a.k_norm ? a.k_norm[c] : 1.0f;
+    }
+
+#pragma unroll 4
+    for (int rb = r0; rb < r1; rb += RW) {
+        const int r = rb + sub;
+        const bool live = r < r1, is_q = r < a.n_heads, is_k = !is_q && r < a.n_heads + a.n_kv_heads;
+        const int h = is_q ? r : is_k ? r - a.n_heads : r - a.n_heads - a.n_kv_heads;
+        float x[8];
+        if (live) {
+            const TI *src = is_q   ? (const TI *)a.q + (int64_t)t * a.q_stride
+                            : is_k ? (const TI *)a.k + (int64_t)t * a.k_stride
+                                   : (const TI *)a.v + (int64_t)t * a.v_stride;
+            load4(src + h * D + c0, x);
+            load4(src + h * D + c1, x + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+        }
+        if (a.q_norm || a.k_norm) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int o = G / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+            const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
+            if ((is_q && a.q_norm) || (is_k && a.k_norm)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (is_q ? wq[i] : wk[i]);
+            }
+        }
+        if (is_q || is_k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = INTERLEAVED ? 2 * i : i, o = INTERLEAVED ? 2 * i + 1 : i + 4;
+                const float xe = x[e], xo = x[o];
+                x[e] = xe * cs[i] - xo * sn[i];
+                x[o] = xe * sn[i] + xo * cs[i];
+            }
+            if (p < 0) {  // only q rows are written then
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+            }
+        }
+        if (!live || (!is_q && slot < 0)) continue;
+        TC *dst = is_q   ? (TC *)a.q_out + ((int64_t)t * a.n_heads + h) * D
+                  : is_k ? (TC *)a.k_pages + (slot * a.n_kv_heads + h) * D
+                         : (TC *)a.v_pages + (slot * a.n_kv_heads + h) * D;
+        // v's values were loaded from the same two places and are only rounded
+        const uint2 lo = make_uint2(Float16<TC>::pack(x[0], x[1]), Float16<TC>::pack(x[2], x[3]));
+        const uint2 hi = make_uint2(Float16<TC>::pack(x[4], x[5]), Float16<TC>::pack(x[6], x[7]));
+        if (INTERLEAVED) {
+            *reinterpret_cast<uint4 *>(dst + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+            *reinterpret_cast<uint2 *>(dst + c0) = lo;
+            *reinterpret_cast<uint2 *>(dst + c1) = hi;
+        }
+    }
+}
+
+template <typename TI, typename TC, int D>
+void launch_append_typed(const AppendArgs &a, bool interleaved, unsigned grid, cudaStream_t stream) {
+    if (interleaved) append_kernel<TI, TC, D, true><<<grid, 128, 0, stream>>>(a);
+    else append_kernel<TI, TC, D, false><<<grid, 128, 0, stream>>>(a);
+}
+
+int launch_append(AppendArgs a, bool in_f32, bool bf16, bool interleaved, int head_dim, cudaStream_t stream,
+                  int sm_count) {
+    // Few tokens: a token's rows are split over warps, down to one step of a warp
+    // each, until about 16 warps per SM have work; many tokens: one warp a token.
+    const int rows = a.n_heads + 2 * a.n_kv_heads, rw = 256 / head_dim;
+    const int steps = (rows + rw - 1) / rw;
+    const int64_t want = ((int64_t)sm_count * 16 + a.n_tokens - 1) / a.n_tokens;
+    const int splits = want < 1 ? 1 : want > steps ? steps : (int)want;
+    a.rows_per_warp = (steps + splits - 1) / splits * rw;
+    a.splits = (rows + a.rows_per_warp - 1) / a.rows_per_warp;
+    const int64_t grid = ((int64_t)a.n_tokens * a.splits + 3) / 4;
+    if (grid > 0x7FFFFFFF) return QDQ_ERR_LIMIT;
+    const unsigned g = (unsigned)grid;
+#define QDQ_APPEND(TI, TC)                                                          \
+    (head_dim == 64 ? launch_append_typed<TI, TC, 64>(a, interleaved, g, stream)    \
+                    : launch_append_typed<TI, TC, 128>(a, interleaved, g, stream))
+    if (in_f32) bf16 ? QDQ_APPEND(float, __nv_bfloat16) : QDQ_APPEND(float, __half);
+    else bf16 ? QDQ_APPEND(__nv_bfloat16, __nv_bfloat16) : QDQ_APPEND(__half, __half);
+#undef QDQ_APPEND
+    return cudaGetLastError() == cudaSuccess ? QDQ_OK : QDQ_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace qdq
+
+using namespace qdq;
+
+struct qdq_paged {
+    qdq_paged_config cfg{};
+    int device = -1, sm_count = 0;
+    char *k_pages = nullptr, *v_pages = nullptr;
+    int64_t layer_bytes = 0;
+    uint64_t *freq = nullptr;  // [rope_dim / 2]
+};
+
+namespace {
+
+int check_paged_config(const qdq_paged_config *c) {
+    if (c->type != QDQ_F16 && c->type != QDQ_BF16) return QDQ_ERR_TYPE;
+    if (c->n_layers < 1 || c->n_pages < 1 || c->n_heads < 1 || c->n_kv_heads < 1) return QDQ_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return QDQ_ERR_SHAPE;
+    if (c->head_dim != 64 && c->head_dim != 128) return QDQ_ERR_SHAPE;
+    if (c->n_heads % c->n_kv_heads || c->n_heads / c->n_kv_heads > 32) return QDQ_ERR_SHAPE;
+    if (c->rope_dim < 0 || c->rope_dim > c->head_dim || c->rope_dim % 8) return QDQ_ERR_SHAPE;
+    if (c->rope_interleaved != 0 && c->rope_interleaved != 1) return QDQ_ERR_SHAPE;
+    if (c->rope_dim && !(c->rope_base > 1.0f && std::isfinite(c->rope_base))) return QDQ_ERR_SHAPE;
+    if (c->n_kv_heads > 1024 || (int64_t)c->n_pages * c->page_size > ((int64_t)1 << 31) - 1) return QDQ_ERR_LIMIT;
+    return QDQ_OK;
+}
+
+// The checks that append and attention share; *work is false when nothing is to do.
+int check_paged_call(const qdq_paged *c, int layer, const qdq_paged_batch *b, bool *work) {
+    *work = false;
+    if (c == nullptr || b == nullptr) return QDQ_ERR_PTR;
+    if (layer < 0 || layer >= c->cfg.n_layers || b->n_seqs < 0 || b->n_tokens < 0 || b->max_pages < 0)
+        return QDQ_ERR_SHAPE;
+    if (b->n_seqs > kMaxSeqs || (int64_t)b->max_pages * c->cfg.page_size > ((int64_t)1 << 30)) return QDQ_ERR_LIMIT;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device) return QDQ_ERR_DEVICE;
+    if (b->n_seqs == 0 || b->n_tokens == 0) return QDQ_OK;
+    int rc = check_dev_ptr(b->q_start, dev, 4);
+    if (!rc) rc = check_dev_ptr(b->kv_len, dev, 4);
+    if (!rc && b->max_pages) rc = check_dev_ptr(b->page_table, dev, 4);
+    *work = rc == QDQ_OK;
+    return rc;
+}
+
+// A [n_tokens][heads * head_dim] operand: its pointer, and rows that are 16-byte
+// aligned and do not overlap.
+int check_rows(const void *p, int64_t stride, int64_t width, int size, int n_tokens, int device) {
+    const int rc = check_dev_ptr(p, device);
+    if (rc) return rc;
+    if (n_tokens > 1 && stride < width) return QDQ_ERR_SHAPE;
+    return n_tokens > 1 && (stride * size) % 16 ? QDQ_ERR_ALIGN : QDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, qdq_paged **out) {
+    if (out == nullptr || cfg == nullptr) return QDQ_ERR_PTR;
+    *out = nullptr;
+    int rc = check_paged_config(cfg);
+    if (rc) return rc;
+    const DeviceInfo &dev = current_device(&rc);
+    if (rc) return rc;
+    if ((rc = check_dev_ptr(k_pages, dev.device)) || (rc = check_dev_ptr(v_pages, dev.device))) return rc;
+    qdq_paged *c = new (std::nothrow) qdq_paged();
+    if (!c) return QDQ_ERR_CUDA;
+    c->cfg = *cfg;
+    c->device = dev.device;
+    c->sm_count = dev.sm_count;
+    c->k_pages = (char *)k_pages;
+    c->v_pages = (char *)v_pages;
+    c->layer_bytes = (int64_t)cfg->n_pages * cfg->page_size * cfg->n_kv_heads * cfg->head_dim * 2;
+    // pair i turns by base^(-2i/R) radians a position: that over 2 pi turns, in units of
+    // 2^-64 turn (below one sixth of a turn, so it fits; a double's 53 bits of it are kept)
+    uint64_t freq[64] = {};
+    for (int i = 0; i < cfg->rope_dim / 2; ++i)
+        freq[i] = (uint64_t)std::ldexp(std::pow((double)cfg->rope_base, -2.0 * i / cfg->rope_dim) / 6.283185307179586476925, 64);
+    if (cudaMalloc((void **)&c->freq, sizeof(freq)) != cudaSuccess ||
+        cudaMemcpy(c->freq, freq, sizeof(freq), cudaMemcpyHostToDevice) != cudaSuccess) {
+        cudaGetLastError();
+        qdq_paged_destroy(c);
+        return QDQ_ERR_CUDA;
+    }
+    *out = c;
+    return QDQ_OK;
+}
+
+void qdq_paged_destroy(qdq_paged *c) {
+    if (c == nullptr) return;
+    if (c->freq) cudaFree(c->freq);
+    delete c;
+}
+
+int qdq_paged_append(qdq_paged *c, int layer, const qdq_paged_batch *b, int in_type, const void *q, int64_t q_stride,
+                     const void *k, int64_t k_stride, const void *v, int64_t v_stride, const float *q_norm,
+                     const float *k_norm, float eps, void *q_out, qdq_stream_t stream) {
+    bool work;
+    int rc = check_paged_call(c, layer, b, &work);
+    if (rc) return rc;
+    const qdq_paged_config &g = c->cfg;
+    if (in_type != QDQ_F32 && in_type != g.type) return QDQ_ERR_TYPE;
+    if (!(eps >= 0.0f) || eps > 1.0f) return QDQ_ERR_SHAPE;
+    if (!work) return QDQ_OK;
+    const int size = in_type == QDQ_F32 ? 4 : 2, n = b->n_tokens, kv = g.n_kv_heads * g.head_dim;
+    if ((rc = check_rows(q, q_stride, (int64_t)g.n_heads * g.head_dim, size, n, c->device)) ||
+        (rc = check_rows(k, k_stride, kv, size, n, c->device)) ||
+        (rc = check_rows(v, v_stride, kv, size, n, c->device)) || (rc = check_dev_ptr(q_out, c->device)) ||
+        (q_norm && (rc = check_dev_ptr(q_norm, c->device, 4))) || (k_norm && (rc = check_dev_ptr(k_norm, c->device, 4))))
+        return rc;
+    AppendArgs a = {};
+    a.n_seqs = b->n_seqs, a.n_tokens = n, a.max_pages = b->max_pages;
+    a.q_start = b->q_start, a.kv_len = b->kv_len, a.page_table = b->page_table;
+    a.q = q, a.k = k, a.v = v;
+    a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.q_norm = q_norm, a.k_norm = k_norm, a.eps = eps;
+    a.freq = c->freq;
+    a.q_out = q_out;
+    a.k_pages = c->k_pages + layer * c->layer_bytes;
+    a.v_pages = c->v_pages + layer * c->layer_bytes;
+    a.n_heads = g.n_heads, a.n_kv_heads = g.n_kv_heads, a.rope_dim = g.rope_dim, a.n_pages = g.n_pages;
+    a.page_shift = 0;
+    while ((1 << a.page_shift) < g.page_size) ++a.page_shift;
+    return launch_append(a, in_type == QDQ_F32, g.type == QDQ_BF16, g.rope_interleaved != 0, g.head_dim,
+                         (cudaStream_t)stream, c->sm_count);
+}
+
+int qdq_paged_attention(qdq_paged *c, int layer, const qdq_paged_batch *b, const void *q, int64_t q_stride,
+                        int out_type, void *out, int64_t out_stride, float scale, int window, float *lse,
+                        qdq_stream_t stream) {
+    bool work;
+    int rc = check_paged_call(c, layer, b, &work);
+    if (rc) return rc;
+    const qdq_paged_config &g = c->cfg;
+    if (out_type != QDQ_F32 && out_type != g.type) return QDQ_ERR_TYPE;
+    if (!std::isfinite(scale) || window < 0) return QDQ_ERR_SHAPE;
+    if (!work) return QDQ_OK;
+    const int n = b->n_tokens;
+    const int64_t width = (int64_t)g.n_heads * g.head_dim;
+    if ((rc = check_rows(q, q_stride, width, 2, n, c->device)) ||
+        (rc = check_rows(out, out_stride, width, out_type == QDQ_F32 ? 4 : 2, n, c->device)) ||
+        (lse && (rc = check_dev_ptr(lse, c->device, 4))))
+        return rc;
+    AttendArgs a = {};
+    a.n_seqs = b->n_seqs, a.n_tokens = n, a.max_pages = b->max_pages;
+    a.q_start = b->q_start, a.kv_len = b->kv_len, a.page_table = b->page_table;
+    a.q = q, a.out = out, a.lse = lse;
+    a.k_pages = c->k_pages + layer * c->layer_bytes;
+    a.v_pages = c->v_pages + layer * c->layer_bytes;
+    a.q_stride = q_stride, a.out_stride = out_stride;
+    a.scale = scale, a.window = window;
+    a.n_pages = g.n_pages, a.page_size = g.page_size;
+    a.n_heads = g.n_heads, a.n_kv_heads = g.n_kv_heads, a.head_dim = g.head_dim;
+    a.bf16 = g.type == QDQ_BF16, a.out_f32 = out_type == QDQ_F32;
+    return launch_attend(a, (cudaStream_t)stream, c->sm_count);
+}
+
+}  // extern "C"

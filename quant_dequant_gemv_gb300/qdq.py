@@ -54,6 +54,21 @@ class LlamaLayer(ctypes.Structure):
                 ("attn_norm", _P), ("ffn_norm", _P)]
 
 
+# qdq_float_type: element types of the serving calls
+F32, F16, BF16 = 1, 2, 3
+
+
+class PagedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("type", "n_layers", "n_pages", "page_size", "n_heads", "n_kv_heads",
+                                              "head_dim", "rope_dim", "rope_interleaved")] + \
+               [("rope_base", ctypes.c_float)]
+
+
+class PagedBatchDesc(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("q_start", _P), ("kv_len", _P), ("page_table", _P)]
+
+
 class GgufTensor(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 96), ("n_dims", ctypes.c_int32), ("ggml_type", ctypes.c_int32),
                 ("qdq_type", ctypes.c_int32), ("reserved", ctypes.c_int32), ("dims", _I64 * 4),
@@ -98,6 +113,12 @@ def lib() -> ctypes.CDLL:
                                          ctypes.POINTER(_P), ctypes.POINTER(_P)]),
             "qdq_llama_launches": (_INT, [_P]),
             "qdq_llama_destroy": (None, [_P]),
+            "qdq_paged_create": (_INT, [ctypes.POINTER(PagedConfig), _P, _P, ctypes.POINTER(_P)]),
+            "qdq_paged_destroy": (None, [_P]),
+            "qdq_paged_append": (_INT, [_P, _INT, _P, _INT, _P, _I64, _P, _I64, _P, _I64, _P, _P, ctypes.c_float,
+                                        _P, _P]),
+            "qdq_paged_attention": (_INT, [_P, _INT, _P, _P, _I64, _INT, _P, _I64, ctypes.c_float, _INT, _P, _P]),
+            "qdq_sample": (_INT, [_INT, _P, _I64, _INT, _INT, _P, _P, _P, _P, _P, _P, _P, _P]),
             "qdq_quantize": (_INT, [_INT, _P, _I64, _P, _P]),
             "qdq_gguf_parse": (_INT, [_P, _I64, ctypes.POINTER(GgufTensor), _INT, ctypes.POINTER(_INT),
                                       ctypes.POINTER(_I64), ctypes.POINTER(ctypes.c_uint32)]),
@@ -120,7 +141,8 @@ EXPORTS = ["qdq_block_bytes", "qdq_block_weights", "qdq_status_string", "qdq_dev
            "qdq_plan_launches", "qdq_get_device_status", "qdq_selftest_wait_timeout",
            "qdq_gemv_levels_noalloc", "qdq_rope_attention", "qdq_llama_create", "qdq_llama_forward",
            "qdq_llama_buffers", "qdq_llama_launches", "qdq_llama_destroy", "qdq_quantize", "qdq_gguf_parse",
-           "qdq_gguf_find_kv"]
+           "qdq_gguf_find_kv", "qdq_paged_create", "qdq_paged_destroy", "qdq_paged_append", "qdq_paged_attention",
+           "qdq_sample"]
 
 
 def _ptr(t) -> int:
@@ -322,6 +344,131 @@ class Llama:
             self.close()
         except Exception:
             pass
+
+
+def _float_type(t) -> int:
+    """The qdq_float_type of a torch tensor (0, which every call refuses, for another type)."""
+    import torch
+    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(t.dtype, 0)
+
+
+def _rows_of(t, what: str) -> int:
+    """The row stride of a [rows, n] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed")
+    return t.stride(0)
+
+
+def _vector(t, n: int, dtype: str, what: str) -> int:
+    """Address of a contiguous tensor of at least n elements of `dtype`; 0 for None."""
+    if t is None:
+        return 0
+    if str(t.dtype) != "torch." + dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of {n} elements is needed")
+    return int(t.data_ptr())
+
+
+class PagedBatch:
+    """The sequences of one step (qdq_paged_batch): q_start [n_seqs + 1], kv_len
+    [n_seqs] and page_table [n_seqs, max_pages], int32 on the device, and the
+    number of rows of q. The tensors are read when the kernels run."""
+
+    def __init__(self, q_start, kv_len, page_table, n_tokens: int):
+        n = kv_len.numel()
+        if page_table.dim() != 2 or page_table.shape[0] != n:
+            raise ValueError("page_table: [n_seqs, max_pages] is needed")
+        self._keep = (q_start, kv_len, page_table)
+        self.n_tokens = n_tokens
+        self.desc = PagedBatchDesc(n, n_tokens, page_table.shape[1], 0, _vector(q_start, n + 1, "int32", "q_start"),
+                                   _vector(kv_len, n, "int32", "kv_len"),
+                                   _vector(page_table, page_table.numel(), "int32", "page_table"))
+        self._ref = ctypes.addressof(self.desc)
+
+
+class PagedCache:
+    """A paged key/value cache (qdq_paged_*): k_pages and v_pages are fp16 or bf16
+    tensors [n_layers, n_pages, page_size, n_kv_heads, head_dim] of the caller's,
+    which must outlive the cache."""
+
+    def __init__(self, k_pages, v_pages, n_heads: int, rope_dim: int | None = None, interleaved: bool = True,
+                 rope_base: float = 10000.0):
+        if k_pages.dim() != 5 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or \
+                not k_pages.is_contiguous() or not v_pages.is_contiguous():
+            raise ValueError("k_pages, v_pages: two contiguous tensors [n_layers, n_pages, page_size, n_kv_heads, "
+                             "head_dim] of one type are needed")
+        layers, pages, page, kv, dim = k_pages.shape
+        self._keep = (k_pages, v_pages)
+        self.dtype = k_pages.dtype
+        self.n_heads, self.n_kv_heads, self.head_dim = n_heads, kv, dim
+        self.cfg = PagedConfig(_float_type(k_pages), layers, pages, page, n_heads, kv, dim,
+                               dim if rope_dim is None else rope_dim, int(interleaved), rope_base)
+        h = _P()
+        _check(lib().qdq_paged_create(ctypes.byref(self.cfg), _ptr(k_pages), _ptr(v_pages), ctypes.byref(h)),
+               "qdq_paged_create")
+        self._h = h
+
+    def _width(self, t, n_tokens: int, heads: int, what: str) -> int:
+        stride = _rows_of(t, what)
+        if t.shape[0] < n_tokens or t.shape[1] != heads * self.head_dim:
+            raise ValueError(f"{what}: {n_tokens} rows of {heads * self.head_dim} are needed")
+        return stride
+
+    def append(self, layer: int, batch: PagedBatch, q, k, v, q_out, q_norm=None, k_norm=None, eps: float = 1e-5,
+               stream=None) -> None:
+        """Head norms, rotation and the cache write of the batch's new tokens (qdq_paged_append).
+        q, k, v: [n_tokens, heads * head_dim] rows (views of a wider row are fine), fp32 or the
+        cache's type; q_out: contiguous, of the cache's type."""
+        n = batch.n_tokens
+        if k.dtype != q.dtype or v.dtype != q.dtype or q_out.dtype != self.dtype:
+            raise ValueError("q, k and v need one type, q_out the cache's")
+        if self._width(q_out, n, self.n_heads, "q_out") != self.n_heads * self.head_dim and n > 1:
+            raise ValueError("q_out: contiguous rows are needed")
+        _check(lib().qdq_paged_append(self._h, layer, batch._ref, _float_type(q), q.data_ptr(),
+                                      self._width(q, n, self.n_heads, "q"), k.data_ptr(),
+                                      self._width(k, n, self.n_kv_heads, "k"), v.data_ptr(),
+                                      self._width(v, n, self.n_kv_heads, "v"),
+                                      _vector(q_norm, self.head_dim, "float32", "q_norm"),
+                                      _vector(k_norm, self.head_dim, "float32", "k_norm"), eps, q_out.data_ptr(),
+                                      _stream(stream)), "qdq_paged_append")
+
+    def attention(self, layer: int, batch: PagedBatch, q, out, scale: float | None = None, window: int = 0, lse=None,
+                  stream=None) -> None:
+        """Causal attention of the batch's new tokens over the cache (qdq_paged_attention).
+        scale defaults to 1 / sqrt(head_dim); out: the cache's type or fp32."""
+        n = batch.n_tokens
+        if q.dtype != self.dtype:
+            raise ValueError("q: the cache's type is needed")
+        _check(lib().qdq_paged_attention(self._h, layer, batch._ref, q.data_ptr(),
+                                         self._width(q, n, self.n_heads, "q"), _float_type(out), out.data_ptr(),
+                                         self._width(out, n, self.n_heads, "out"),
+                                         self.head_dim ** -0.5 if scale is None else scale, window,
+                                         _vector(lse, n * self.n_heads, "float32", "lse"), _stream(stream)),
+               "qdq_paged_attention")
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) is not None and self._h.value:
+            lib().qdq_paged_destroy(self._h)
+            self._h = _P()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None,
+           stream=None) -> None:
+    """The next token of each row of logits from the random numbers u (qdq_sample). logits:
+    [rows, vocab] fp32, fp16 or bf16; per row u, temperature, top_p, min_p fp32, top_k int32
+    (None switches a filter off); tokens int64, logprobs fp32."""
+    stride, (rows, vocab) = _rows_of(logits, "logits"), logits.shape
+    _check(lib().qdq_sample(_float_type(logits), logits.data_ptr(), stride, rows, vocab,
+                            _vector(temperature, rows, "float32", "temperature"),
+                            _vector(top_k, rows, "int32", "top_k"), _vector(top_p, rows, "float32", "top_p"),
+                            _vector(min_p, rows, "float32", "min_p"), _vector(u, rows, "float32", "u"),
+                            _vector(tokens, rows, "int64", "tokens"), _vector(logprobs, rows, "float32", "logprobs"),
+                            _stream(stream)), "qdq_sample")
 
 
 def quantize(qtype: int, x, n: int, blocks, stream=None) -> None:
