@@ -1,72 +1,836 @@
-// qdq_attend.cu -- causal attention of a step's new tokens over the paged cache.
+// qdq_attend.cu -- causal attention of a step's new tokens over the paged cache, on the
+// tcgen05 tensor cores.
+//
+//   o = sum_j p_j v_j / l,  p_j = 2^(c s_j - m),  l = sum_j p_j,  c = scale * log2(e)
+// in one pass over the keys with a running maximum m and sum l (fp32). For a tile of 128
+// rows (tokens x the query heads that share a kv head) and a tile of 128 positions,
+// S = Q K^T goes to tensor memory, 128 threads take a row each, write P (16-bit) over S,
+// and O += P V accumulates in tensor memory. The maximum that p is taken against lags
+// the true one by up to 2^8, so that O is rescaled a few times a row and not every tile;
+// the factor cancels in o and in l.
+//
+// A CTA (one per SM) has ten working warps: two groups of four that each own one S/P/O set
+// (the softmax), one that issues the matrix instructions and one that issues the copies.
+// * Chunks: the two sets are two tiles of rows against the same keys, so that one
+//   group's exponentials run while the other's products do.
+// * Few rows (one tile, as in single-token steps): the two sets take alternate key tiles
+//   of the same rows, and their two states are joined at the end.
+// Keys and values arrive page by page through one ring of slots (4-D tensor copies with
+// the 128-byte swizzle: a slot is groups of 8 positions, each group head_dim / 64 blocks
+// of 8 x 128 bytes, which is the operand layout for K (K-major) and for V (N-major)).
+// A page that lies outside the block's positions is not read.
+//
+// The key tiles of all items are dealt to the CTAs in equal contiguous ranges
+// (qdq_attend_plan.h); the parts of an item that several CTAs hold are written to a
+// workspace, and the CTA that finishes last (an integer counter) joins them in CTA
+// order, so the result does not depend on which one that was. No CTA waits for another.
+//
+// Values in rows of V outside the block's positions are zeroed in shared memory before
+// their product (their weights are zero, but 0 x NaN is not), scores there are replaced
+// by -inf whatever K held.
 #include <cmath>
+#include <cuda.h>
+#include <mutex>
+#include <new>
 
+#include "qdq_attend_plan.h"
 #include "qdq_internal.h"
 #include "qdq_paged.cuh"
+#include "qdq_tcgen05.cuh"
 
 namespace qdq {
+
+// Host state of the attention of one cache: the tensor maps of the pools and the
+// workspace (partial results and the counters that the joins leave at zero).
+struct AttendState {
+    CUtensorMap k_map, v_map;
+    char *mem = nullptr;
+    float *part_o = nullptr, *part_m = nullptr, *part_l = nullptr;
+    unsigned *counters = nullptr;
+    int ctas = 0;
+};
+
 namespace {
 
-// One warp per (token, query head); the lanes hold D/32 dims each. Positions are
-// taken one by one with the running maximum and sum of an online softmax.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attend_kernel(const AttendArgs a) {
-    constexpr int E = D / 32;
+__device__ int g_attend_status;
+
+constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 320;
+constexpr float kLag = 8.0f;  // log2 of how far the running maximum may lag
+constexpr int kColO = 256;    // tensor memory: S/P of the two sets in columns 0..255, then O
+
+struct KernelArgs {
+    int n_seqs, n_tokens, max_pages;
+    const int32_t *q_start, *kv_len, *page_table;
+    void *out;
+    float *lse;
+    int64_t out_stride;
+    float scale_log2;  // |scale| * log2(e); a negative scale negates Q in the instruction
+    uint32_t idesc_qk, idesc_pv;
+    int n_pages, page_shift, row8_layer;  // row8_layer: first group of 8 rows of the layer
+    int n_heads;
+    bool out_f32;
+    AttendGeometry g;
+    float *part_o, *part_m, *part_l;
+    unsigned *counters;
+};
+
+template <int HD>
+struct Shape {
+    static constexpr int kHalves = HD / 64;
+    static constexpr uint32_t kQTile = 128u * HD * 2u;
+    static constexpr uint32_t kSlot = (uint32_t)kTileN * HD * 2u;
+    static constexpr int kSlots = HD == 128 ? 5 : 10;
+    static constexpr uint32_t kGroup8 = (uint32_t)kHalves * 1024u;  // 8 positions of a slot
+    static constexpr uint32_t kQ = 0, kRing = 2 * kQTile;
+    static constexpr uint32_t kBars = kRing + kSlots * kSlot;
+    static constexpr uint32_t kScratch = kBars + 256;        // joins: 2 groups x 128 x (maximum, 1 / sum)
+    static constexpr uint32_t kStart = kScratch + 2 * 128 * 8;  // the CTA's first piece, tensor-memory base
+    static constexpr uint32_t kTotal = kStart + 64;
+};
+// barriers (8 bytes each) at kBars
+constexpr int kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 21, kBarS = 22, kBarP = 24, kBarPv = 26,
+              kBarOFree = 28, kBarDrain = 30;
+
+struct Start {
+    long long pos, end;
+    int seq, block, head, off, ctas, live;
+};
+
+// A walk over the pieces of a CTA's range; every role walks it by itself.
+struct Walk {
+    long long pos;   // first key tile of the piece, in the order of all
+    long long left;  // key tiles of the range from there on
+    int seq, block, head, off;
+    int first, count, kv;
+    AttendBlock b;
+    QDQ_DEV void load_seq(const KernelArgs &a) {
+        seq_tokens(a.q_start, seq, a.n_tokens, first, count);
+        kv = max(a.kv_len[seq], 0);
+    }
+    QDQ_DEV Walk(const KernelArgs &a, const Start &s)
+        : pos(s.pos), left(s.end - s.pos), seq(s.seq), block(s.block), head(s.head), off(s.off) {
+        load_seq(a);
+        b = block_of(a.g, count, kv, block);
+    }
+    QDQ_DEV int t_beg() const { return b.t0 + off; }
+    QDQ_DEV int len() const { return (int)min((long long)(b.t1 - b.t0 - off), left); }
+    QDQ_DEV void next(const KernelArgs &a) {
+        const int n = len();
+        pos += n;
+        left -= n;
+        if (left == 0) return;
+        off = 0;
+        if (++head < a.g.kv_heads) return;
+        head = 0;
+        if (++block >= seq_blocks(a.g, count)) {
+            block = 0;
+            do {
+                if (++seq >= a.n_seqs) {  // (only if the batch changed under the kernel)
+                    left = 0;
+                    return;
+                }
+                load_seq(a);
+            } while (count == 0);
+        }
+        b = block_of(a.g, count, kv, block);
+    }
+};
+
+// The pages of key tile j that hold positions of [lo, hi): lane l's page number (the
+// tile's l-th run of min(page, 128) positions), or -1 where it has none or is absent.
+QDQ_DEV int tile_page(const KernelArgs &a, int seq, int j, int run_shift, int lo, int hi) {
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = (int)(unit / a.n_heads), h = (int)(unit % a.n_heads);
-    if (t >= a.n_tokens) return;
-    const int s = find_seq(a.q_start, a.n_seqs, t);
-    if (s < 0) return;
-    int first, count;
-    seq_tokens(a.q_start, s, a.n_tokens, first, count);
-    if (t < first || t >= first + count) return;
-    const int g = h / (a.n_heads / a.n_kv_heads);
-    const int p = max(a.kv_len[s], 0) - count + (t - first);
-    const int64_t last = min((int64_t)p, (int64_t)a.max_pages * a.page_size - 1);
-    const int lo = a.window && p >= a.window ? p - a.window + 1 : 0;
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) q[i] = (float)((const T *)a.q)[t * a.q_stride + h * D + lane * E + i] * a.scale;
-    for (int j = lo; j <= last; ++j) {
-        const int page = a.page_table[(int64_t)s * a.max_pages + j / a.page_size];
-        if (page < 0 || page >= a.n_pages) continue;
-        const int64_t row = (((int64_t)page * a.page_size + j % a.page_size) * a.n_kv_heads + g) * D + lane * E;
-        float x = 0.0f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) x = fmaf(q[i], (float)((const T *)a.k_pages)[row + i], x);
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, k);
-        const float mn = fmaxf(m, x), f = mn == -INFINITY ? 1.0f : expf(m - mn), w = mn == -INFINITY ? 0.0f : expf(x - mn);
-        m = mn;
-        l = l * f + w;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = o[i] * f + w * (float)((const T *)a.v_pages)[row + i];
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int64_t at = t * a.out_stride + h * D + lane * E + i;
-        if (a.out_f32) ((float *)a.out)[at] = o[i] * inv;
-        else ((T *)a.out)[at] = Float16<T>::one(o[i] * inv);
-    }
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.n_heads + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+    const int64_t p = (int64_t)j * kTileN + ((int64_t)lane << run_shift);
+    if (lane >= (kTileN >> run_shift) || p >= hi || p + (1 << run_shift) <= lo) return -1;
+    const int at = (int)(p >> a.page_shift);  // below max_pages: hi is within the table
+    const int page = a.page_table[(int64_t)seq * a.max_pages + at];
+    return page >= 0 && page < a.n_pages ? page : -1;
 }
+
+QDQ_DEV float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Where the CTA's range starts: sums of key tiles per sequence, a scan, and a search.
+template <int HD>
+QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
+    using L = Shape<HD>;
+    int *cnt = reinterpret_cast<int *>(smem + L::kRing), *kvs = cnt + kMaxSeqs;
+    long long *pre = reinterpret_cast<long long *>(smem + L::kRing + 8 * kMaxSeqs);  // [n_seqs + 1]
+    constexpr int kAlone = 8;  // blocks that one thread sums; longer sequences are summed by a warp
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int s = tid; s < a.n_seqs; s += kThreads) {
+        int first, count;
+        seq_tokens(a.q_start, s, a.n_tokens, first, count);
+        const int kv = max(a.kv_len[s], 0), nb = seq_blocks(a.g, count);
+        cnt[s] = count;
+        kvs[s] = kv;
+        long long sum = 0;
+        if (nb <= kAlone)
+            for (int b = 0; b < nb; ++b) {
+                const AttendBlock k = block_of(a.g, count, kv, b);
+                sum += k.t1 - k.t0;
+            }
+        pre[s] = sum * a.g.kv_heads;
+    }
+    __syncthreads();
+    for (int s = warp; s < a.n_seqs; s += kThreads / 32) {
+        const int nb = seq_blocks(a.g, cnt[s]);
+        if (nb <= kAlone) continue;
+        long long sum = 0;
+        for (int b = lane; b < nb; b += 32) {
+            const AttendBlock k = block_of(a.g, cnt[s], kvs[s], b);
+            sum += k.t1 - k.t0;
+        }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) pre[s] = sum * a.g.kv_heads;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        // a scan over lanes, each with a contiguous run of sequences
+        const int per = (a.n_seqs + 31) / 32, s0 = min(lane * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+        long long mine = 0;
+        for (int s = s0; s < s1; ++s) mine += pre[s];
+        long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long e = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += e;
+        }
+        const long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        const int ctas = (int)min((long long)gridDim.x, total);
+        const bool live = (int)blockIdx.x < ctas;
+        const long long x = live ? range_start(total, ctas, blockIdx.x) : 0;
+        const long long excl = incl - mine;
+        if (lane == 0) {
+            start->live = live;
+            start->ctas = ctas;
+            start->pos = x;
+            start->end = live ? range_start(total, ctas, blockIdx.x + 1) : 0;
+            // (the total is kept for the joins)
+            pre[a.n_seqs] = total;
+        }
+        // the lane whose run of sequences holds x walks it
+        const unsigned owner = __ballot_sync(0xFFFFFFFFu, live && mine > 0 && excl <= x && x < incl);
+        int s = 0;
+        long long rem = 0;
+        if (owner && lane == __ffs(owner) - 1) {
+            rem = x - excl;
+            s = s0;
+            while (rem >= pre[s]) rem -= pre[s++];
+        }
+        if (owner) {
+            const int src = __ffs(owner) - 1;
+            s = __shfl_sync(0xFFFFFFFFu, s, src);
+            rem = __shfl_sync(0xFFFFFFFFu, rem, src);
+            // the block: 32 at a time
+            const int nb = seq_blocks(a.g, cnt[s]);
+            for (int b0 = 0; b0 < nb; b0 += 32) {
+                int n = 0;
+                if (b0 + lane < nb) {
+                    const AttendBlock k = block_of(a.g, cnt[s], kvs[s], b0 + lane);
+                    n = k.t1 - k.t0;
+                }
+                long long run = (long long)n * a.g.kv_heads;
+                const long long own = run;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long e = __shfl_up_sync(0xFFFFFFFFu, run, o);
+                    if (lane >= o) run += e;
+                }
+                const unsigned m = __ballot_sync(0xFFFFFFFFu, rem < run);
+                if (m) {
+                    const int l = __ffs(m) - 1;
+                    if (lane == l) {
+                        const int r = (int)(rem - (run - own));
+                        start->seq = s;
+                        start->block = b0 + l;
+                        start->head = r / n;
+                        start->off = r % n;
+                    }
+                    break;
+                }
+                rem -= __shfl_sync(0xFFFFFFFFu, run, 31);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap q_map,
+                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using L = Shape<HD>;
+    extern __shared__ __align__(1024) char smem[];
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *status = &g_attend_status;
+    Start *start = reinterpret_cast<Start *>(smem + L::kStart);
+    auto bar = [&](int i) { return sb + L::kBars + 8u * i; };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(bar(kBarFull + i), 1);
+            mbar_init(bar(kBarEmpty + i), 1);
+        }
+        mbar_init(bar(kBarQFull), 1);
+        mbar_init(bar(kBarQEmpty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarS + i), 1);
+            mbar_init(bar(kBarP + i), 4);
+            mbar_init(bar(kBarPv + i), 1);
+            mbar_init(bar(kBarOFree + i), 4);
+        }
+        mbar_init(bar(kBarDrain), 1);
+        fence_mbar_init();
+    }
+    find_start<HD>(a, smem, start);
+    if (!start->live) return;
+    const long long total = *reinterpret_cast<long long *>(smem + L::kRing + 8 * kMaxSeqs + 8 * a.n_seqs);
+    const Start s0 = *start;
+    __syncthreads();
+    fence_async_smem();  // the ring's memory goes over to the copies
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kStart);
+    if (warp == kWarpMma) tc_alloc(smem_u32(tmem_slot), 512);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
+
+    const int run_shift = min(a.page_shift, 7), tq = tile_tokens(a.g);
+
+    if (warp == kWarpLoad) {
+        // ---- copies ---------------------------------------------------------------------
+        const uint32_t q_rows = (uint32_t)(tq * a.g.group), run_bytes = (L::kGroup8 << run_shift) >> 3;
+        uint32_t seq_no = 0, items = 0;
+        for (Walk w(a, s0); w.left > 0; w.next(a), ++items) {
+            const int n = w.len(), t0 = w.t_beg(), tiles = w.b.i1 - w.b.i0 > tq ? 2 : 1;
+            mbar_wait(bar(kBarQEmpty), (items & 1) ^ 1, status);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(kBarQFull), tiles * L::kHalves * q_rows * 128u);
+                for (int i = 0; i < tiles; ++i)
+                    for (int h = 0; h < L::kHalves; ++h)
+                        tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
+                                    w.first + w.b.i0 + i * tq, bar(kBarQFull));
+            }
+            int page = tile_page(a, w.seq, t0, run_shift, w.b.lo, w.b.hi);
+            for (int j = 0; j < n; ++j) {
+                const int here = page;
+                if (j + 1 < n) page = tile_page(a, w.seq, t0 + j + 1, run_shift, w.b.lo, w.b.hi);
+                const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0);
+                const uint32_t bytes = __popc(have) * run_bytes;
+                // the lane's run of positions: its first group of 8 rows in the pools
+                const int in_page = ((t0 + j) * kTileN + (lane << run_shift)) & ((1 << a.page_shift) - 1);
+                const int row8 = a.row8_layer + (int)((((int64_t)here << a.page_shift) + in_page) >> 3);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++seq_no) {
+                    const int slot = seq_no % L::kSlots;
+                    mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
+                    if (lane == 0) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
+                    __syncwarp();
+                    if (here >= 0)
+                        tma_load_4d(sb + L::kRing + slot * L::kSlot + (uint32_t)lane * run_bytes, kv ? &v_map : &k_map, 0,
+                                    0, w.head * L::kHalves, row8, bar(kBarFull + slot));
+                }
+            }
+        }
+        // every copy has landed before the CTA can end, also after a wait that ran out
+        for (uint32_t i = seq_no < (uint32_t)L::kSlots ? 0 : seq_no - L::kSlots; i < seq_no; ++i)
+            mbar_wait(bar(kBarFull + i % L::kSlots), (i / L::kSlots) & 1, status);
+        if (items) mbar_wait(bar(kBarQFull), (items - 1) & 1, status);
+    } else if (warp == kWarpMma) {
+        // ---- matrix instructions ----------------------------------------------------------
+        constexpr uint32_t q_hi = sdesc_hi(1024), kv_hi = sdesc_hi(L::kGroup8);
+        uint32_t seq_no = 0, items = 0, np[2] = {0, 0}, no[2] = {0, 0};
+        const uint32_t q_lo = sdesc_lo(16) | ((sb + L::kQ) >> 4);
+        const uint32_t k_lo = sdesc_lo(16) | ((sb + L::kRing) >> 4), v_lo = sdesc_lo(1024) | ((sb + L::kRing) >> 4);
+        auto full = [&](uint32_t s) { mbar_wait(bar(kBarFull + s % L::kSlots), (s / L::kSlots) & 1, status); };
+        // S_i = Q K^T with K in slot number s, rows of tile qi
+        auto qk = [&](int i, int qi, uint32_t s) {
+            const uint32_t kd = k_lo + (s % L::kSlots) * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
+            if (elect_lane()) {
+#pragma unroll
+                for (int k = 0; k < HD / 16; ++k)
+                    tc_mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
+                              desc64(kd + (k / 4) * 64u + (k % 4) * 2u, kv_hi), a.idesc_qk, k > 0);
+                tc_commit(bar(kBarS + i));
+            }
+            __syncwarp();
+        };
+        // O_i (+)= P_i V with V in slot number s
+        auto pv = [&](int i, uint32_t s, bool first) {
+            const uint32_t vd = v_lo + (s % L::kSlots) * (L::kSlot >> 4);
+            mbar_wait(bar(kBarP + i), np[i]++ & 1, status);
+            if (first) mbar_wait(bar(kBarOFree + i), (no[i]++ & 1) ^ 1, status);
+            full(s);
+            tc_after();
+            if (elect_lane()) {
+#pragma unroll
+                for (int k = 0; k < kTileN / 16; ++k)
+                    tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + 128u * i + 8u * k,
+                              desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
+                tc_commit(bar(kBarPv + i));
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t s) {
+            if (elect_lane()) tc_commit(bar(kBarEmpty + s % L::kSlots));
+            __syncwarp();
+        };
+        for (Walk w(a, s0); w.left > 0; w.next(a), ++items) {
+            const int n = w.len(), t0 = w.t_beg();
+            const uint32_t base = seq_no;
+            seq_no += 2 * n;
+            mbar_wait(bar(kBarQFull), items & 1, status);
+            if (block_alternates(a.g, w.b)) {
+                for (int k = 0; k < 2 && k < n; ++k) {
+                    full(base + 2 * k);
+                    qk(k, 0, base + 2 * k);
+                    release(base + 2 * k);
+                }
+                for (int k = 0; k < n; ++k) {
+                    pv(k & 1, base + 2 * k + 1, k < 2);
+                    release(base + 2 * k + 1);
+                    if (k + 2 < n) {
+                        full(base + 2 * k + 4);
+                        qk(k & 1, 0, base + 2 * k + 4);
+                        release(base + 2 * k + 4);
+                    }
+                }
+            } else {
+                bool begun[2] = {false, false};
+                auto on = [&](int i, int k) { return k < n && t0 + k >= w.b.tile_t0[i] && t0 + k < w.b.tile_t1[i]; };
+                full(base);
+                for (int i = 0; i < 2; ++i)
+                    if (on(i, 0)) qk(i, i, base);
+                release(base);
+                for (int k = 0; k < n; ++k) {
+                    full(base + 2 * k + 1);
+                    for (int i = 0; i < 2; ++i) {
+                        if (on(i, k)) {
+                            pv(i, base + 2 * k + 1, !begun[i]);
+                            begun[i] = true;
+                        }
+                        if (i == 0 && k + 1 < n) full(base + 2 * k + 2);
+                        if (on(i, k + 1)) qk(i, i, base + 2 * k + 2);
+                    }
+                    release(base + 2 * k + 1);
+                    if (k + 1 < n) release(base + 2 * k + 2);
+                }
+            }
+            if (elect_lane()) tc_commit(bar(kBarQEmpty));
+            __syncwarp();
+        }
+        if (elect_lane()) tc_commit(bar(kBarDrain));
+        __syncwarp();
+        mbar_wait(bar(kBarDrain), 0, status);
+    } else {
+        // ---- softmax, output ----------------------------------------------------------------
+        const int i = warp >> 2, r = threadIdx.x & 127;  // set; row = tensor-memory lane
+        const uint32_t t_s = tmem + ((uint32_t)(warp & 3) << 21) + 128u * i;
+        const uint32_t t_o = tmem + ((uint32_t)(warp & 3) << 21) + kColO + (uint32_t)HD * i;
+        const float c = a.scale_log2;
+        const uint64_t c2 = pack2(c, c);
+        float2 *scratch = reinterpret_cast<float2 *>(smem + L::kScratch) + i * 128;
+        uint32_t seq_no = 0, ns = 0, npv = 0;
+        for (Walk w(a, s0); w.left > 0; w.next(a)) {
+            const int n = w.len(), t0 = w.t_beg();
+            const uint32_t base = seq_no;
+            seq_no += 2 * n;
+            const bool alt = block_alternates(a.g, w.b);
+            // this set's rows and key tiles of the piece
+            const int qi = alt ? 0 : i, a0 = w.b.i0 + qi * tq, rows = min(tq, w.b.i1 - a0) * a.g.group;
+            if (rows <= 0) continue;
+            const int step = alt ? 2 : 1;
+            const int j0 = alt ? t0 + i : max(t0, w.b.tile_t0[qi]);
+            const int j1 = alt ? t0 + n : min(t0 + n, w.b.tile_t1[qi]);
+            const int token = a0 + min(r, rows - 1) / a.g.group;
+            int lo, hi, lo_last, hi_first, x;
+            span(a.g, w.kv - w.count + token, 1, lo, hi);
+            span(a.g, w.kv - w.count + a0, 1, x, hi_first);
+            span(a.g, w.kv - w.count + a0 + rows / a.g.group - 1, 1, lo_last, x);
+
+            float m = -INFINITY, l = 0.0f;
+            int page = j0 < j1 ? tile_page(a, w.seq, j0, run_shift, w.b.lo, w.b.hi) : -1;
+            for (int j = j0; j < j1; j += step) {
+                const unsigned have = __ballot_sync(0xFFFFFFFFu, page >= 0);
+                if (j + step < j1) page = tile_page(a, w.seq, j + step, run_shift, w.b.lo, w.b.hi);
+                const int p0 = j * kTileN;
+                const unsigned all = (1u << (kTileN >> run_shift)) - 1;
+                const bool dirty = have != all || p0 < w.b.lo || p0 + kTileN > w.b.hi;
+                const bool masked = dirty || p0 < lo_last || p0 + kTileN > hi_first;
+                // columns 32 k .. 32 k + 31 of a masked tile: those outside [lo, hi) and whole
+                // runs of absent pages become -inf
+                auto mask = [&](float *s, int k) {
+                    const int b = min(max(lo - p0 - 32 * k, 0), 32), e = min(max(hi - p0 - 32 * k, 0), 32);
+                    uint32_t keep = e > b ? (uint32_t)(((1ull << e) - 1) & ~((1ull << b) - 1)) : 0u;
+                    if (run_shift >= 5) keep = (have >> ((32 * k) >> run_shift)) & 1 ? keep : 0u;
+                    else keep &= ((have >> (2 * k)) & 1 ? 0xFFFFu : 0u) | ((have >> (2 * k + 1)) & 1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) s[y] = (keep >> y) & 1 ? s[y] : -INFINITY;
+                };
+                mbar_wait(bar(kBarS + i), ns++ & 1, status);
+                tc_after();
+                // The row's maximum, 64 columns at a time: the last 64 are read again when
+                // their turn comes, so that a thread holds 64 scores and not 128.
+                float s0[32], s1[32], mx[4];
+                tc_ld32(t_s + 64, s0);
+                tc_ld32(t_s + 96, s1);
+                tc_wait_ld<32>(s0);
+                tc_wait_ld<32>(s1);
+                if (masked) mask(s0, 2), mask(s1, 3);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s0[y], s1[y]);
+#pragma unroll
+                for (int y = 4; y < 32; ++y) mx[y & 3] = max3(mx[y & 3], s0[y], s1[y]);
+                tc_ld32(t_s, s0);
+                tc_ld32(t_s + 32, s1);
+                tc_wait_ld<32>(s0);
+                tc_wait_ld<32>(s1);
+                if (masked) mask(s0, 0), mask(s1, 1);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) mx[y & 3] = max3(mx[y & 3], s0[y], s1[y]);
+                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                if (j == j0) {
+                    m = mn;
+                } else if (__any_sync(0xFFFFFFFFu, (mn - m) * c > kLag)) {
+                    // raise the maximum of the warp's rows: O and l change units
+                    const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
+                    m = mn;
+                    l *= f;
+                    mbar_wait(bar(kBarPv + i), (npv - 1) & 1, status);
+                    tc_after();
+                    const uint64_t f2 = pack2(f, f);
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) {
+                        float o[16];
+                        tc_ld16(t_o + 16 * k, o);
+                        tc_wait_ld<16>(o);
+#pragma unroll
+                        for (int y = 0; y < 16; y += 2) {
+                            const uint64_t v = fmul2(pack2(o[y], o[y + 1]), f2);
+                            o[y] = lo_of(v);
+                            o[y + 1] = hi_of(v);
+                        }
+                        tc_st16(t_o + 16 * k, reinterpret_cast<uint32_t *>(o));
+                    }
+                    tc_wait_st();
+                }
+                const float mc = m == -INFINITY ? 0.0f : m * c;
+                const uint64_t mc2 = pack2(-mc, -mc);
+                uint64_t sum[2] = {};
+                uint32_t u[32];
+                auto weights = [&](const float *s, uint32_t *to) {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        const uint64_t e = ffma2(pack2(s[k], s[k + 1]), c2, mc2);
+                        const float p = ex2(lo_of(e)), q = ex2(hi_of(e));
+                        sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
+                        to[k / 2] = BF16 ? Float16<__nv_bfloat16>::pack(p, q) : Float16<__half>::pack(p, q);
+                    }
+                };
+                weights(s0, u);
+                tc_ld32(t_s + 64, s0);
+                weights(s1, u + 16);
+                tc_st32(t_s, u);
+                tc_ld32(t_s + 96, s1);
+                tc_wait_ld<32>(s0);
+                tc_wait_ld<32>(s1);
+                if (masked) mask(s0, 2), mask(s1, 3);
+                weights(s0, u);
+                weights(s1, u + 16);
+                tc_st32(t_s + 32, u);
+                const uint64_t t = fadd2(sum[0], sum[1]);
+                l += lo_of(t) + hi_of(t);
+                if (dirty) {
+                    // zero the rows of V that hold no position of the block (row r of the slot)
+                    const uint32_t vs = base + 2 * (j - t0) + 1;
+                    mbar_wait(bar(kBarFull + vs % L::kSlots), (vs / L::kSlots) & 1, status);
+                    if (p0 + r < w.b.lo || p0 + r >= w.b.hi || !((have >> (r >> run_shift)) & 1)) {
+                        char *row = smem + L::kRing + (vs % L::kSlots) * L::kSlot + (r / 8) * L::kGroup8 + (r % 8) * 128;
+#pragma unroll
+                        for (int k = 0; k < HD / 8; ++k)
+                            *reinterpret_cast<uint4 *>(row + (k / 8) * 1024 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                }
+                tc_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarP + i));
+                ++npv;
+            }
+
+            // ---- the piece's end ------------------------------------------------------------
+            const bool any = j1 > j0;
+            const float mc = m == -INFINITY ? -INFINITY : m * c;
+            if (any) {
+                mbar_wait(bar(kBarPv + i), (npv - 1) & 1, status);
+                tc_after();
+            }
+            auto o_read = [&] {  // the last read of O: the next piece may overwrite it
+                tc_before();
+                __syncwarp();
+                if (any && lane == 0) mbar_arrive(bar(kBarOFree + i));
+            };
+            const long long item = w.pos - w.off;
+            const int c_first = range_owner(total, s0.ctas, item);
+            const int c_last = range_owner(total, s0.ctas, item + (w.b.t1 - w.b.t0) - 1);
+            // outputs of row `row` of the set's tile: token and head
+            auto out_at = [&](int row) {
+                const int64_t t = w.first + a0 + row / a.g.group, h = (int64_t)w.head * a.g.group + row % a.g.group;
+                return t * a.out_stride + h * HD;
+            };
+            auto lse_at = [&](int row) {
+                return (int64_t)(w.first + a0 + row / a.g.group) * a.n_heads + w.head * a.g.group + row % a.g.group;
+            };
+            auto put4 = [&](int64_t at, float x, float y, float z, float v) {
+                if (a.out_f32) {
+                    *reinterpret_cast<float4 *>((float *)a.out + at) = make_float4(x, y, z, v);
+                } else {
+                    *reinterpret_cast<uint2 *>((uint16_t *)a.out + at) =
+                        BF16 ? make_uint2(Float16<__nv_bfloat16>::pack(x, y), Float16<__nv_bfloat16>::pack(z, v))
+                               : make_uint2(Float16<__half>::pack(x, y), Float16<__half>::pack(z, v));
+                }
+            };
+            if (c_first == c_last && !alt) {
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const int64_t at = out_at(min(r, rows - 1));
+#pragma unroll
+                for (int k = 0; k < HD / 32; ++k) {
+                    float o[32];
+                    if (any) {
+                        tc_ld32(t_o + 32 * k, o);
+                        tc_wait_ld<32>(o);
+                    }
+                    if (r < rows) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 4) {
+                            if (any && l > 0.0f) put4(at + 32 * k + y, o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv);
+                            else put4(at + 32 * k + y, 0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+                    }
+                }
+                o_read();
+                if (a.lse && r < rows) a.lse[lse_at(r)] = l > 0.0f ? (mc + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                continue;
+            }
+            // partial state: O as [column / 4][row][4], so that rows of a warp are contiguous
+            const int part = (blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0)) * 2 + i;
+            {
+                float4 *po = reinterpret_cast<float4 *>(a.part_o) + (int64_t)part * (HD / 4) * 128;
+                if (any) {
+#pragma unroll
+                    for (int k = 0; k < HD / 32; ++k) {
+                        float o[32];
+                        tc_ld32(t_o + 32 * k, o);
+                        tc_wait_ld<32>(o);
+                        if (r < rows) {
+#pragma unroll
+                            for (int y = 0; y < 32; y += 4)
+                                __stcg(po + (8 * k + y / 4) * 128 + r, make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]));
+                        }
+                    }
+                }
+                o_read();
+                if (r < rows) {
+                    __stcg(a.part_m + part * 128 + r, mc);
+                    __stcg(a.part_l + part * 128 + r, l);
+                }
+            }
+            // the last of the item's parts joins them all, in order
+            const int parts = (c_last - c_first + 1) * (alt ? 2 : 1);
+            int me = r, threads = 128;
+            if (c_first == c_last) {
+                // both parts are this CTA's: its two groups meet and join half each
+                __threadfence_block();
+                named_bar_sync(3, 256);
+                me = threadIdx.x;
+                threads = 256;
+            } else {
+                __threadfence();
+                named_bar_sync(1 + i, 128);
+                if (r == 0) {
+                    unsigned *ctr = a.counters + 2 * c_first + (alt ? 0 : i);
+                    const unsigned before = atomicAdd(ctr, 1u);
+                    const bool last = before == (unsigned)parts - 1;
+                    if (last) *ctr = 0;
+                    __threadfence();
+                    scratch[0] = make_float2(last ? 1.0f : 0.0f, 0.0f);
+                }
+                named_bar_sync(1 + i, 128);
+                const bool last = scratch[0].x != 0.0f;
+                named_bar_sync(1 + i, 128);
+                if (!last) continue;
+                __threadfence();
+            }
+            auto part_of = [&](int k) {
+                const int cta = c_first + (alt ? k >> 1 : k);
+                return (cta * 2 + (cta == c_first ? 1 : 0)) * 2 + (alt ? k & 1 : i);
+            };
+            if (r < rows) {
+                float M = -INFINITY, S = 0.0f;
+#pragma unroll 4
+                for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(a.part_m + part_of(k) * 128 + r));
+#pragma unroll 4
+                for (int k = 0; k < parts; ++k) {
+                    const float lk = __ldcg(a.part_l + part_of(k) * 128 + r), mk = __ldcg(a.part_m + part_of(k) * 128 + r);
+                    if (lk > 0.0f) S += lk * ex2(mk - M);
+                }
+                scratch[r] = make_float2(M, S > 0.0f ? 1.0f / S : 0.0f);
+                if (a.lse && (threads == 128 || i == 0)) a.lse[lse_at(r)] = S > 0.0f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
+            }
+            named_bar_sync(1 + i, 128);
+            for (int k = me; k < rows * (HD / 4); k += threads) {
+                const int row = k % rows, col = k / rows;
+                const float2 ml = scratch[row];
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (int y = 0; y < parts; ++y) {
+                    const int pt = part_of(y);
+                    const float lk = __ldcg(a.part_l + pt * 128 + row);
+                    if (!(lk > 0.0f)) continue;
+                    const float f = ex2(__ldcg(a.part_m + pt * 128 + row) - ml.x);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + ((int64_t)pt * (HD / 4) + col) * 128 + row);
+                    acc.x = fmaf(f, v.x, acc.x);
+                    acc.y = fmaf(f, v.y, acc.y);
+                    acc.z = fmaf(f, v.z, acc.z);
+                    acc.w = fmaf(f, v.w, acc.w);
+                }
+                put4(out_at(row) + 4 * col, acc.x * ml.y, acc.y * ml.y, acc.z * ml.y, acc.w * ml.y);
+            }
+            // (scratch, and the parts of a join within the CTA, are free again)
+            if (threads == 256) named_bar_sync(3, 256);
+            else named_bar_sync(1 + i, 128);
+        }
+    }
+
+    tc_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        tc_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+    static std::once_flag once;
+    static EncodeTiled fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(p);
+        else
+            cudaGetLastError();
+    });
+    return fn;
+}
+
+bool encode(CUtensorMap *map, bool bf16, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    EncodeTiled enc = encode_fn();
+    return enc && enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                      const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+using Kernel = void (*)(KernelArgs, CUtensorMap, CUtensorMap, CUtensorMap);
+Kernel kernel_of(int head_dim, bool bf16) {
+    if (head_dim == 64) return bf16 ? attend_kernel<64, true> : attend_kernel<64, false>;
+    return bf16 ? attend_kernel<128, true> : attend_kernel<128, false>;
+}
+uint32_t smem_of(int head_dim) { return head_dim == 64 ? Shape<64>::kTotal : Shape<128>::kTotal; }
 
 }  // namespace
 
-int launch_attend(const AttendArgs &a, cudaStream_t stream, int) {
-    const int64_t grid = ((int64_t)a.n_tokens * a.n_heads + 7) / 8;
-    if (grid > 0x7FFFFFFF) return QDQ_ERR_LIMIT;
-    const unsigned g = (unsigned)grid;
-    if (a.head_dim == 64) {
-        if (a.bf16) attend_kernel<__nv_bfloat16, 64><<<g, 256, 0, stream>>>(a);
-        else attend_kernel<__half, 64><<<g, 256, 0, stream>>>(a);
-    } else {
-        if (a.bf16) attend_kernel<__nv_bfloat16, 128><<<g, 256, 0, stream>>>(a);
-        else attend_kernel<__half, 128><<<g, 256, 0, stream>>>(a);
+int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
+    *out = nullptr;
+    AttendState *st = new (std::nothrow) AttendState();
+    if (!st) return QDQ_ERR_CUDA;
+    // the pools as [row / 8][64-wide block of a row][row % 8][64]: one box is a run of
+    // positions of one kv head, in the order that the matrix instructions read
+    const int run = p.page_size < 128 ? p.page_size : 128, blocks = p.n_kv_heads * p.head_dim / 64;
+    const cuuint64_t row = (cuuint64_t)p.n_kv_heads * p.head_dim * 2;
+    const cuuint64_t rows = (cuuint64_t)p.n_layers * p.n_pages * p.page_size;
+    const cuuint64_t dims[4] = {64, 8, (cuuint64_t)blocks, rows / 8}, strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)(p.head_dim / 64), (cuuint32_t)run / 8};
+    bool ok = encode(&st->k_map, p.bf16, 4, p.k_pages, dims, strides, box) &&
+              encode(&st->v_map, p.bf16, 4, p.v_pages, dims, strides, box);
+    st->ctas = sm_count;
+    // two parts per CTA and set: 128 rows of O, a maximum and a sum; the joins' counters
+    const size_t parts = (size_t)sm_count * 4, n_o = parts * 128 * p.head_dim * 4, n_s = parts * 128 * 4;
+    const size_t bytes = n_o + 2 * n_s + (size_t)sm_count * 2 * sizeof(unsigned);
+    ok = ok && cudaMalloc((void **)&st->mem, bytes) == cudaSuccess && cudaMemset(st->mem, 0, bytes) == cudaSuccess;
+    ok = ok && cudaFuncSetAttribute(kernel_of(p.head_dim, p.bf16), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    smem_of(p.head_dim)) == cudaSuccess;
+    if (!ok) {
+        cudaGetLastError();
+        attend_destroy(st);
+        return QDQ_ERR_CUDA;
     }
+    st->part_o = (float *)st->mem;
+    st->part_m = (float *)(st->mem + n_o);
+    st->part_l = (float *)(st->mem + n_o + n_s);
+    st->counters = (unsigned *)(st->mem + n_o + 2 * n_s);
+    *out = st;
+    return QDQ_OK;
+}
+
+void attend_destroy(AttendState *st) {
+    if (st == nullptr) return;
+    if (st->mem) cudaFree(st->mem);
+    delete st;
+}
+
+int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t stream) {
+    KernelArgs k = {};
+    const AttendPools &p = *a.pools;
+    k.n_seqs = a.n_seqs, k.n_tokens = a.n_tokens, k.max_pages = a.max_pages;
+    k.q_start = a.q_start, k.kv_len = a.kv_len, k.page_table = a.page_table;
+    k.out = a.out, k.lse = a.lse, k.out_stride = a.out_stride;
+    k.scale_log2 = (float)(std::fabs((double)a.scale) * 1.4426950408889634);
+    k.n_pages = p.n_pages;
+    while ((1 << k.page_shift) < p.page_size) ++k.page_shift;
+    k.row8_layer = (int)((int64_t)a.layer * p.n_pages * p.page_size / 8);
+    k.n_heads = p.n_heads;
+    k.out_f32 = a.out_f32;
+    k.g.group = p.n_heads / p.n_kv_heads;
+    k.g.kv_heads = p.n_kv_heads;
+    k.g.window = a.window < INT32_MAX - a.n_tokens ? a.window : INT32_MAX - a.n_tokens;
+    k.g.table_end = a.max_pages * p.page_size;
+    k.part_o = st->part_o, k.part_m = st->part_m, k.part_l = st->part_l, k.counters = st->counters;
+    // fp32 accumulators, both operands of the pools' type, M = 128; S: N = 128, both K-major
+    // (a negative scale negates Q); O: N = head_dim, V is N-major
+    const uint32_t common = (1u << 4) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTileM >> 4) << 24);
+    k.idesc_qk = common | ((uint32_t)(kTileN >> 3) << 17) | (a.scale < 0.0f ? 1u << 13 : 0u);
+    k.idesc_pv = common | ((uint32_t)(p.head_dim >> 3) << 17) | (1u << 16);
+    // Q as [token][head][dim]: a box is 64 dims of the group's heads of a tile's tokens
+    CUtensorMap q_map;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.n_heads, (cuuint64_t)a.n_tokens};
+    const cuuint64_t q_row = a.n_tokens > 1 ? (cuuint64_t)a.q_stride * 2 : (cuuint64_t)p.n_heads * p.head_dim * 2;
+    const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, q_row};
+    const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)tile_tokens(k.g)};
+    if (!encode(&q_map, p.bf16, 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
+    kernel_of(p.head_dim, p.bf16)<<<st->ctas, kThreads, smem_of(p.head_dim), stream>>>(k, q_map, st->k_map, st->v_map);
     return cudaGetLastError() == cudaSuccess ? QDQ_OK : QDQ_ERR_CUDA;
+}
+
+int take_status_attend() {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_attend_status, sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        return QDQ_ERR_CUDA;
+    }
+    if (v && cudaMemcpyToSymbol(g_attend_status, &zero, sizeof(int)) != cudaSuccess) {
+        cudaGetLastError();
+        return QDQ_ERR_CUDA;
+    }
+    return v;
 }
 
 }  // namespace qdq

@@ -71,22 +71,30 @@ int launch_mma_gemv(int type, const void *W, int64_t rows, int64_t cols, const f
                     int batch, cudaStream_t stream, int sm_count);
 int take_status_mma();
 
-// The paged cache's attention kernels (qdq_attend.cu); the handle and the append
-// are in qdq_paged.cu.
+// The attention over a paged cache (qdq_attend.cu); the handle and the append are in
+// qdq_paged.cu.
+struct AttendPools {
+    const void *k_pages, *v_pages;  // every layer
+    int n_layers, n_pages, page_size, n_heads, n_kv_heads, head_dim;
+    bool bf16;
+};
 struct AttendArgs {
-    int n_seqs, n_tokens, max_pages;
+    const AttendPools *pools;
+    int layer, n_seqs, n_tokens, max_pages;
     const int32_t *q_start, *kv_len, *page_table;
     const void *q;      // [n_tokens][n_heads * head_dim] of the pools' type
     void *out;          // of the pools' type, or fp32
     float *lse;         // [n_tokens][n_heads], or NULL
-    const void *k_pages, *v_pages;  // one layer
-    int64_t q_stride, out_stride;   // elements
+    int64_t q_stride, out_stride;  // elements
     float scale;
     int window;         // 0: none
-    int n_pages, page_size, n_heads, n_kv_heads, head_dim;
-    bool bf16, out_f32;
+    bool out_f32;
 };
-int launch_attend(const AttendArgs &a, cudaStream_t stream, int sm_count);
+struct AttendState;
+int attend_create(const AttendPools &p, int sm_count, AttendState **out);
+void attend_destroy(AttendState *st);
+int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t stream);
+int take_status_attend();
 
 // While a caller's stream is being captured into a CUDA graph, one-time setup calls
 // (kernel attributes, occupancy queries, memory-pool creation) would invalidate a

@@ -185,6 +185,8 @@ struct qdq_paged {
     char *k_pages = nullptr, *v_pages = nullptr;
     int64_t layer_bytes = 0;
     uint64_t *freq = nullptr;  // [rope_dim / 2]
+    AttendPools pools{};
+    AttendState *attend = nullptr;
 };
 
 namespace {
@@ -198,7 +200,10 @@ int check_paged_config(const qdq_paged_config *c) {
     if (c->rope_dim < 0 || c->rope_dim > c->head_dim || c->rope_dim % 8) return QDQ_ERR_SHAPE;
     if (c->rope_interleaved != 0 && c->rope_interleaved != 1) return QDQ_ERR_SHAPE;
     if (c->rope_dim && !(c->rope_base > 1.0f && std::isfinite(c->rope_base))) return QDQ_ERR_SHAPE;
-    if (c->n_kv_heads > 1024 || (int64_t)c->n_pages * c->page_size > ((int64_t)1 << 31) - 1) return QDQ_ERR_LIMIT;
+    // (rows of the whole pool are numbered in groups of 8 by 32-bit coordinates)
+    if (c->n_kv_heads > 1024 || (int64_t)c->n_pages * c->page_size > ((int64_t)1 << 30) ||
+        (int64_t)c->n_pages * c->page_size > ((int64_t)1 << 33) / c->n_layers)
+        return QDQ_ERR_LIMIT;
     return QDQ_OK;
 }
 
@@ -259,6 +264,12 @@ int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, 
         qdq_paged_destroy(c);
         return QDQ_ERR_CUDA;
     }
+    c->pools = {k_pages, v_pages, cfg->n_layers, cfg->n_pages, cfg->page_size, cfg->n_heads, cfg->n_kv_heads,
+                cfg->head_dim, cfg->type == QDQ_BF16};
+    if ((rc = attend_create(c->pools, c->sm_count, &c->attend))) {
+        qdq_paged_destroy(c);
+        return rc;
+    }
     *out = c;
     return QDQ_OK;
 }
@@ -266,6 +277,7 @@ int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, 
 void qdq_paged_destroy(qdq_paged *c) {
     if (c == nullptr) return;
     if (c->freq) cudaFree(c->freq);
+    attend_destroy(c->attend);
     delete c;
 }
 
@@ -319,17 +331,14 @@ int qdq_paged_attention(qdq_paged *c, int layer, const qdq_paged_batch *b, const
         (lse && (rc = check_dev_ptr(lse, c->device, 4))))
         return rc;
     AttendArgs a = {};
+    a.pools = &c->pools;
+    a.layer = layer;
     a.n_seqs = b->n_seqs, a.n_tokens = n, a.max_pages = b->max_pages;
     a.q_start = b->q_start, a.kv_len = b->kv_len, a.page_table = b->page_table;
     a.q = q, a.out = out, a.lse = lse;
-    a.k_pages = c->k_pages + layer * c->layer_bytes;
-    a.v_pages = c->v_pages + layer * c->layer_bytes;
     a.q_stride = q_stride, a.out_stride = out_stride;
-    a.scale = scale, a.window = window;
-    a.n_pages = g.n_pages, a.page_size = g.page_size;
-    a.n_heads = g.n_heads, a.n_kv_heads = g.n_kv_heads, a.head_dim = g.head_dim;
-    a.bf16 = g.type == QDQ_BF16, a.out_f32 = out_type == QDQ_F32;
-    return launch_attend(a, (cudaStream_t)stream, c->sm_count);
+    a.scale = scale, a.window = window, a.out_f32 = out_type == QDQ_F32;
+    return launch_attend(c->attend, a, (cudaStream_t)stream);
 }
 
 }  // extern "C"

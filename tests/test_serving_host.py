@@ -90,3 +90,15 @@ def test_oracle_sampling_ties_and_empty_rows():
     assert sv.sample(x, 0.999, top_p=1 / 3, top_k=3)[0] == 1    # the mass before the second is not below
     assert sv.sample(np.full(3, -np.inf), 0.5)[0] == -1 and sv.sample(np.full(3, np.nan), 0.5)[0] == -1
     assert sv.sample(x, 0.0, min_p=0.5)[0] == 1 and sv.sample(x, 1.0)[0] == 3
+
+
+def test_attention_work_split(tmp_path):
+    """The kernel's own work split, compiled for the host (tests/attend_plan_check.cpp)."""
+    import subprocess
+    from pathlib import Path
+    root = Path(__file__).resolve().parents[1]
+    exe = tmp_path / "attend_plan_check"
+    subprocess.run(["g++", "-O1", "-std=c++17", f"-I{root / 'quant_dequant_gemv_gb300' / 'csrc'}",
+                    str(root / "tests" / "attend_plan_check.cpp"), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
