@@ -458,3 +458,16 @@ def test_sample_follows_the_distribution(qdq):
     w[keep] = np.exp(row[keep].astype(np.float64))
     share = np.bincount(tokens.cpu().numpy(), minlength=V) / B
     assert np.abs(share - w / w.sum()).max() <= 1.5 / B
+
+
+def test_sample_extreme_parameters(qdq):
+    """Temperatures near the ends of fp32, random numbers outside [0, 1), a top-k far in the open bin."""
+    rng = np.random.default_rng(8)
+    B, V = 6, 20011
+    x = torch.from_numpy(rng.standard_normal((B, V)) * 3).float()
+    x[1, ::3] = float("-inf")
+    x = x.cuda()
+    u = rng.uniform(0, 1, B).astype(np.float32)
+    check_sample(qdq, x, u, temperature=[1e-30, 1e30, 0.02, 0.05, 50.0, 1.0], top_k=[0, 9000, 15000, 500, 19000, 20010])
+    check_sample(qdq, x, u, temperature=[1e30, 1e30, 1e6, 300.0, 50.0, 10.0], top_p=[0.5, 0.9, 0.99, 0.25, 0.999, 0.01])
+    check_sample(qdq, x, np.float32([-3.0, 1.5, 0.0, 1.0, -1e-9, 2.0]), top_k=40)
