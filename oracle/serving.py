@@ -101,4 +101,5 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     order = np.sort(order[w[order] >= min(min_p, 1.0)])
     mass = np.cumsum(w[order])
     at = min(int((mass <= u * mass[-1]).sum()), len(order) - 1)
-    return int(order[at]), float(np.log(w[order[at]] / mass[-1]))
+    share = w[order[at]] / mass[-1]
+    return int(order[at]), float(np.log(share)) if share > 0 else -np.inf

@@ -1,27 +1,30 @@
 // qdq_sample.cu -- sampling: temperature, top-k, top-p and min-p from given random
 // numbers.
 //
-// One pass over the logits: a cluster of up to eight CTAs holds a row in shared memory,
-// a contiguous slice each, and everything after the load works on that copy.
+// One pass over the logits: a cluster of up to eight CTAs holds a row's order-preserving
+// 32-bit keys in shared memory, a contiguous slice each, and everything after the load
+// works on those.
 //
 // The filters are cuts of one order (logit descending, index ascending), so nothing is
-// sorted. A cut is found by narrowing an interval of the logits' order-preserving 32-bit
-// keys: first 512 bins that are linear in the exponent (1/16 wide, the last one open;
-// counts only), then 512 equal parts of the interval at a time until it is one key; the
-// entries with exactly that key are then kept by index. Top-k narrows by count. Top-p
-// needs masses: the first level's bin is guessed from the counts (a bin's mass is close
-// to count x e^-middle) and checked with the exact mass above it, moving to the next bin
-// where the guess was off; below it the bins hold exact masses.
+// sorted. A cut is found by narrowing: 512 bins over an interval of keys, a scan, and the
+// bin that reaches the wanted count or mass becomes the next interval until it is one
+// key. The first bins are linear in the exponent (1/16 wide, the last one open) instead
+// of the key; the entries that share the cut's key are told apart by narrowing over their
+// indices, and so is the draw itself (an inverse CDF in index order).
+//
+// The first counts bound the kept set from above: all entries of a bin have weights
+// within a factor e^(1/16), so a prefix of bins whose estimated mass exceeds top-p's share
+// of the estimated whole by 1/15 is certain to hold the cut. If that prefix (or top-k's
+// bin) has at most kList entries, they are gathered in the first CTA, which finishes
+// alone while the others leave; otherwise the cluster narrows together.
 //
 // Masses are integers (weights in units of 2^-44 of the largest), so neither the order of
 // the additions nor the split over CTAs changes a sum. In the bins they are kept as three
 // 15-bit pieces, each added with a native 32-bit shared-memory atomic (at most 2^15
-// entries a slice, so a piece cannot overflow).
+// entries a CTA, so a piece cannot overflow).
 //
-// The draw is an inverse CDF in index order: kept mass per CTA, per warp, per entry.
-// CTAs of a cluster exchange sums by writing them to each other before a cluster barrier,
-// and read each other's bins after one; two sets of buffers take turns, so one barrier
-// per step is enough.
+// CTAs of a cluster send sums to each other before a cluster barrier and read each
+// other's bins after one; two sets of buffers take turns, so a step needs one barrier.
 #include <cmath>
 #include <mutex>
 
@@ -31,8 +34,9 @@
 namespace qdq {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 512, kMaxCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = kThreads, kMaxCluster = 8;
 constexpr int kSlice = 1 << 15;  // entries of a row that a CTA holds at most
+constexpr int kList = 2048;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr uint32_t kLowest = 0x00800000u;  // the key of the lowest finite logit (-inf is one below)
 typedef unsigned long long u64;
@@ -55,11 +59,12 @@ QDQ_DEV float value_of(uint32_t k) { return __uint_as_float(k ^ (k & 0x80000000u
 
 struct Shared {
     unsigned bins[2][3][kBins];
-    u64 sums[2][kMaxCluster][3];  // what the cluster's CTAs sent
-    u64 warp[kWarps][3];
+    u64 sums[2][kMaxCluster][2];  // what the cluster's CTAs sent
+    u64 warp[kWarps + 1][2];
     u64 found[2];                 // the bin a cut lies in, and the measure above it
     uint32_t edge[2];
-    float x[1];                   // the slice (slice entries)
+    u64 list[kList];              // key << 32 | index
+    uint32_t key[1];              // the slice (slice entries)
 };
 
 QDQ_DEV void cluster_sync() {
@@ -80,56 +85,75 @@ QDQ_DEV uint32_t remote(const void *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-QDQ_DEV u64 warp_sum(u64 v) {
+QDQ_DEV void store_remote(uint32_t at, u64 v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory"); }
+template <typename V>
+QDQ_DEV V warp_sum(V v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
 
-// One CTA's part in the work on one row.
+// One CTA's part in the work on one row. ALONE: the first CTA on the gathered list;
+// otherwise every CTA of the cluster on its slice, each with the same results.
 struct Row {
     Shared &sh;
-    const int n;  // entries of the slice
     const int tid, lane, warp;
     const uint32_t rank, ctas;
+    int n = 0, i_first = 0;  // the slice
     int turn_s = 0, turn_b = 0;
     float top = 0.0f, inv = 1.0f;
 
-    QDQ_DEV Row(Shared &s, int n_, uint32_t r, uint32_t c)
-        : sh(s), n(n_), tid(threadIdx.x), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), rank(r), ctas(c) {}
+    QDQ_DEV Row(Shared &s, uint32_t r, uint32_t c)
+        : sh(s), tid(threadIdx.x), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), rank(r), ctas(c) {}
 
-    QDQ_DEV float weight(float x) const { return x == top ? 1.0f : expf((x - top) * inv); }  // (-inf weighs 0)
+    QDQ_DEV float weight(uint32_t key) const {  // (-inf weighs 0)
+        const float x = value_of(key);
+        return x == top ? 1.0f : expf((x - top) * inv);
+    }
     static QDQ_DEV u64 fixed(float w) { return __float2ull_rn(w * 0x1p44f); }
     // The first level's bin: 1/16 of the exponent wide, falling logits, the last one open.
-    QDQ_DEV int bin_of(float x) const { return min((int)((top - x) * inv * 16.0f), kBins - 1); }
+    QDQ_DEV int bin_of(uint32_t key) const { return min((int)((top - value_of(key)) * inv * 16.0f), kBins - 1); }
 
-    // Every warp's sums (lane 0's arguments) to every CTA; after it, part(r, i) is CTA r's.
+    template <bool ALONE>
+    QDQ_DEV void sync() {
+        if (ALONE) __syncthreads();
+        else cluster_sync();
+    }
+    template <bool ALONE, typename F>
+    QDQ_DEV void each(F f) {  // f(key, index) over this CTA's entries
+        if (ALONE) {
+            for (int i = tid; i < n; i += kThreads) f((uint32_t)(sh.list[i] >> 32), (uint32_t)sh.list[i]);
+        } else {
+            for (int i = tid; i < n; i += kThreads) f(sh.key[i], (uint32_t)(i_first + i));
+        }
+    }
+
+    // The warps' values (maximum or sum of the first, sum of the second) to the CTAs below
+    // `to`; part(r, i) is CTA r's after the barrier that the caller passes next.
     template <bool MAX>
-    QDQ_DEV void send(u64 a, u64 b) {
+    QDQ_DEV void send(u64 a, u64 b, uint32_t to) {
         if (lane == 0) sh.warp[warp][0] = a, sh.warp[warp][1] = b;
         __syncthreads();
-        if (tid < (int)ctas) {
-            u64 x = 0, y = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                x = MAX ? (sh.warp[w][0] > x ? sh.warp[w][0] : x) : x + sh.warp[w][0];
-                y += sh.warp[w][1];
+        if (warp == 0) {
+            u64 x = lane < kWarps ? sh.warp[lane][0] : 0, y = lane < kWarps ? sh.warp[lane][1] : 0;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+                const u64 e = __shfl_xor_sync(kAll, x, o);
+                x = MAX ? (e > x ? e : x) : x + e;
+                y += __shfl_xor_sync(kAll, y, o);
             }
-            const uint32_t to = remote(&sh.sums[turn_s][rank][0], tid);
-            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(x) : "memory");
-            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + 8), "l"(y) : "memory");
+            if (lane < (int)to) {  // (lanes 0..15 hold the result)
+                const uint32_t at = remote(&sh.sums[turn_s][rank][0], lane);
+                store_remote(at, x);
+                store_remote(at + 8, y);
+            }
         }
-        cluster_sync();
         turn_s ^= 1;
     }
     QDQ_DEV u64 part(uint32_t r, int i) const { return sh.sums[turn_s ^ 1][r][i]; }
-    QDQ_DEV u64 all(int i) const {
-        u64 v = 0;
-        for (uint32_t r = 0; r < ctas; ++r) v += part(r, i);
-        return v;
-    }
 
     QDQ_DEV void clear_bins(int pieces) {
-        for (int i = tid; i < pieces * kBins; i += kThreads) (&sh.bins[turn_b][0][0])[i] = 0;
+        for (int i = 0; i < pieces; ++i) sh.bins[turn_b][i][tid] = 0;
         __syncthreads();
     }
     QDQ_DEV void add_mass(int b, u64 f) {
@@ -137,24 +161,34 @@ struct Row {
         atomicAdd(&sh.bins[turn_b][1][b], (unsigned)(f >> 15) & 0x7FFFu);
         atomicAdd(&sh.bins[turn_b][2][b], (unsigned)(f >> 30));
     }
-    // The cluster's sum of bin `tid` (each CTA reads all the others'); ends the turn.
-    template <int PIECES>
-    QDQ_DEV u64 gather_bins() {
-        cluster_sync();
-        u64 v = 0;
-        for (uint32_t r = 0; r < ctas; ++r)
+    // Bin `tid` over the whole cluster (each CTA reads all the others'), and over the CTAs
+    // below this one; ends the turn.
+    template <bool ALONE, int PIECES>
+    QDQ_DEV u64 gather_bins(u64 *below = nullptr) {
+        sync<ALONE>();
+        u64 v = 0, low = 0;
+        if (ALONE) {
 #pragma unroll
-            for (int i = 0; i < PIECES; ++i) {
-                unsigned x;
-                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(remote(&sh.bins[turn_b][i][tid], r)) : "memory");
-                v += (u64)x << (15 * i);
+            for (int i = 0; i < PIECES; ++i) v += (u64)sh.bins[turn_b][i][tid] << (15 * i);
+        } else {
+            unsigned x[PIECES];
+#pragma unroll 4
+            for (uint32_t r = 0; r < ctas; ++r) {
+                if (r == rank) low = v;
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i)
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x[i]) : "r"(remote(&sh.bins[turn_b][i][tid], r)));
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) v += (u64)x[i] << (15 * i);
             }
+        }
+        if (below) *below = low;
         turn_b ^= 1;
         return v;
     }
-    // Sum over the bins before this thread's.
+    // Sum over the bins before this thread's; *all: over every bin.
     template <typename V>
-    QDQ_DEV V before(V v) {
+    QDQ_DEV V before(V v, V *all) {
         V incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -162,37 +196,43 @@ struct Row {
             if (lane >= o) incl += e;
         }
         V *w = reinterpret_cast<V *>(&sh.warp[0][0]);
+        __syncthreads();
         if (lane == 31) w[warp] = incl;
         __syncthreads();
-        V sum = 0;
-        for (int i = 0; i < warp; ++i) sum += w[i];
+        V t = lane < kWarps ? w[lane] : 0, ti = t;
+#pragma unroll
+        for (int o = 1; o < kWarps; o <<= 1) {
+            const V e = __shfl_up_sync(kAll, ti, o);
+            if (lane >= o) ti += e;
+        }
+        *all = __shfl_sync(kAll, ti, kWarps - 1);
+        return __shfl_sync(kAll, ti - t, warp) + incl - v;
+    }
+    // The first bin whose sum (v in this thread's, excl before it) reaches the target: one
+    // thread's. found[] is set for every thread after the barrier.
+    QDQ_DEV void find(u64 v, u64 excl, u64 target) {
+        if (excl < target && excl + v >= target) sh.found[0] = tid, sh.found[1] = excl;
         __syncthreads();
-        return sum + incl - v;
     }
 
-    // The bin where above + its prefix first reaches the target (count or mass), and the
-    // prefix before it.
-    template <typename REACHED>
-    QDQ_DEV void find(u64 v, u64 above, REACHED reached, int &bin, u64 &ahead) {
-        const u64 excl = above + before(v);
-        if (v && !reached(excl) && reached(excl + v)) sh.found[0] = tid, sh.found[1] = excl;
-        __syncthreads();
-        bin = (int)sh.found[0];
-        ahead = sh.found[1];
-        __syncthreads();
-    }
-
-    // The keys whose first-level bin is b: [lo, hi]. Two warps search 32 probes at a time
-    // for the smallest key whose bin is at most b, and at most b - 1.
+    // The keys whose first-level bin is b: [lo, hi]. Two warps look for the smallest key
+    // whose bin is at most b, and at most b - 1: among the 32 keys around where it should
+    // be, then, if rounding put it elsewhere, 32 probes at a time from the whole range.
     QDQ_DEV void keys_of(int b, uint32_t &lo, uint32_t &hi) {
         if (warp < 2) {
             const int want = b - warp;
-            uint32_t first = kLowest, last = key_of(top);  // the answer lies in [first, last] (the top's bin is 0)
+            uint32_t first = kLowest, last = key_of(top);  // the answer is in [first, last] (the top's bin is 0)
             if (want >= kBins - 1) last = first;
+            if (want >= 0 && first < last) {
+                const uint32_t mid = key_of(top - (float)(want + 1) * 0.0625f / inv);
+                const uint32_t at = min(max(mid, first + 16) - 16 + lane, last);
+                const unsigned m = __ballot_sync(kAll, bin_of(at) <= want);
+                if (m && !(m & 1)) first = last = __shfl_sync(kAll, at, __ffs(m) - 1);
+            }
             while (first < last && want >= 0) {
                 const uint32_t step = (last - first) / 32 + 1;
                 const u64 at = (u64)first + (u64)step * lane;
-                const unsigned m = __ballot_sync(kAll, at >= last || bin_of(value_of((uint32_t)at)) <= want);
+                const unsigned m = __ballot_sync(kAll, at >= last || bin_of((uint32_t)at) <= want);
                 const int l = __ffs(m) - 1;  // the answer is at most lane l's probe, above lane l - 1's
                 if (m == 0) {
                     first = first + step * 31 + 1;
@@ -207,43 +247,120 @@ struct Row {
         __syncthreads();
         lo = sh.edge[0];
         hi = sh.edge[1] - 1;
-        __syncthreads();
     }
 
-    // Narrows [lo, hi], which holds the cut, to the cut's key. `ahead`: the measure above hi,
-    // and at the end above the key; returns the measure of the entries with that key.
-    template <bool MASS, typename REACHED>
-    QDQ_DEV u64 narrow(uint32_t lo, uint32_t hi, u64 &ahead, REACHED reached, uint32_t &key) {
+    // The largest key in [lo, hi] at which the measure from hi down (from `ahead` on)
+    // reaches the target; `ahead` becomes the measure above it; returns its own. get(key,
+    // index, k, f): whether an entry counts, under which key, with which mass. With SHARE
+    // the target is the share of the whole that `share` asks for, set at the first level.
+    template <bool ALONE, bool MASS, bool SHARE = false, typename GET>
+    QDQ_DEV u64 narrow(uint32_t lo, uint32_t hi, u64 &ahead, u64 &target, uint32_t &key, GET get, double share = 0.0,
+                       u64 *whole = nullptr) {
         for (int level = 0; level < 4; ++level) {  // 9 bits a level: 32 bits take four
-            int shift = 0;
-            while (((hi - lo) >> shift) >= kBins) ++shift;
+            const int shift = max(0, 32 - 9 - __clz(hi - lo));
             clear_bins(MASS ? 3 : 1);
-            for (int i = tid; i < n; i += kThreads) {
-                const float x = sh.x[i];
-                const uint32_t k = key_of(x);
-                if (k < lo || k > hi) continue;
+            each<ALONE>([&](uint32_t entry, uint32_t index) {
+                uint32_t k;
+                if (!get(entry, index, k) || k < lo || k > hi) return;
                 const int b = (int)((hi - k) >> shift);
-                if (MASS) add_mass(b, fixed(weight(x)));
+                if (MASS) add_mass(b, fixed(weight(entry)));
                 else atomicAdd(&sh.bins[turn_b][0][b], 1u);
+            });
+            const u64 v = gather_bins<ALONE, MASS ? 3 : 1>();
+            u64 all;
+            const u64 excl = ahead + before(v, &all);
+            if (SHARE && level == 0) {
+                *whole = all;
+                target = min((u64)(share * (double)all) + 1, all);
             }
-            const u64 v = gather_bins<MASS ? 3 : 1>();
-            int b;
-            find(v, ahead, reached, b, ahead);
-            const uint32_t top_key = hi - ((uint32_t)b << shift);
+            find(v, excl, target);
+            const uint32_t b = (uint32_t)sh.found[0] & (kBins - 1);
+            ahead = sh.found[1];
+            const uint32_t last = hi - (b << shift);
             if (shift == 0) {
-                key = top_key;
-                if (tid == b) sh.found[0] = v;
+                if (tid == (int)b) sh.warp[kWarps][0] = v;
                 __syncthreads();
-                const u64 here = sh.found[0];
-                __syncthreads();
-                return here;
+                key = last;
+                return sh.warp[kWarps][0];
             }
             const uint32_t wide = (1u << shift) - 1;
-            lo = top_key - lo > wide ? top_key - wide : lo;
-            hi = top_key;
+            lo = last - lo > wide ? last - wide : lo;
+            hi = last;
         }
         key = hi;  // not reached
         return 1;
+    }
+
+    // Everything after the first counts: the cuts, the ties, the draw. bin, ahead: top-k's
+    // first-level bin and the count above it.
+    template <bool ALONE>
+    QDQ_DEV void finish(const SampleArgs &a, int b, u64 top_k, int bin, u64 ahead, bool by_p, float top_p, float floor_w,
+                        u64 total) {
+        uint32_t cut = kLowest, lo, hi;
+        u64 ties = ~0ull, here = 0, target;  // entries above `cut` are kept, and the first `ties` at it
+        if (top_k) {
+            keys_of(bin, lo, hi);
+            target = top_k;
+            here = narrow<ALONE, false>(lo, hi, ahead, target, cut, [](uint32_t e, uint32_t, uint32_t &k) { return k = e, true; });
+            ties = top_k - ahead;
+        }
+        if (by_p) {
+            // exact masses of the first-level bins of what top-k left; their sum is the whole,
+            // but for a list, which holds part of it unless top-k chose it. The cut's own bin
+            // may hold more ties than top-k kept: none that the target reaches.
+            clear_bins(3);
+            u64 low = 0;  // mass of the ties that top-k dropped
+            each<ALONE>([&](uint32_t key, uint32_t) {
+                if (key >= cut) add_mass(bin_of(key), fixed(weight(key)));
+            });
+            if (top_k) low = (here - ties) * fixed(weight(cut));
+            const u64 v = gather_bins<ALONE, 3>();
+            u64 all;
+            const u64 excl = before(v, &all);
+            if (!ALONE || top_k) total = all - low;
+            // (at least one unit, so that the first entry is kept whatever top_p is)
+            const double share = (double)top_p * (double)total;
+            target = share < 1.0 ? 1 : (u64)ceil(share);
+            find(v, excl, target);
+            const int p_bin = (int)sh.found[0] & (kBins - 1);
+            u64 above = sh.found[1];
+            keys_of(p_bin, lo, hi);
+            uint32_t key;
+            const u64 mass = narrow<ALONE, true>(max(lo, cut), hi, above, target, key,
+                                                 [](uint32_t e, uint32_t, uint32_t &k) { return k = e, true; });
+            // the fewest of the entries at the key that reach the target
+            const u64 f = fixed(weight(key)), need = (target - above + f - 1) / f;
+            const u64 most = top_k && key == cut ? ties : mass / f;
+            here = mass / f;
+            cut = key;
+            ties = min(need, most);
+        }
+        // ties: the index of the last one kept (narrowing runs over inverted indices, so that
+        // the lowest come first)
+        uint32_t tie_last = 0xFFFFFFFFu;
+        if (ties < here) {
+            u64 none = 0;
+            uint32_t inverted;
+            narrow<ALONE, false>(0xFFFFFFFFu - (uint32_t)(a.vocab - 1), 0xFFFFFFFFu, none, ties, inverted,
+                                 [&](uint32_t e, uint32_t i, uint32_t &k) { return k = ~i, e == cut; });
+            tie_last = ~inverted;
+        }
+        // the draw: the first index at which the running mass of the kept entries exceeds u of
+        // the whole (at u = 1, reaches the whole)
+        uint32_t inverted;
+        u64 mass_ahead = 0, whole;
+        narrow<ALONE, true, true>(0xFFFFFFFFu - (uint32_t)(a.vocab - 1), 0xFFFFFFFFu, mass_ahead, target, inverted,
+                                  [&](uint32_t e, uint32_t i, uint32_t &k) {
+                                      k = ~i;
+                                      return (e > cut || (e == cut && i <= tie_last)) && weight(e) >= floor_w;
+                                  },
+                                  fmin(fmax((double)a.u[b], 0.0), 1.0), &whole);
+        const uint32_t token = ~inverted;
+        each<ALONE>([&](uint32_t key, uint32_t index) {
+            if (index != token) return;
+            a.tokens[b] = (int64_t)token;
+            if (a.logprobs) a.logprobs[b] = (float)log((double)weight(key) / ((double)whole * 0x1p-44));
+        });
     }
 };
 
@@ -251,11 +368,12 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) char smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
-    const uint32_t ctas = cluster_size(), rank = cluster_rank();
-    const int b = blockIdx.x / ctas, i_first = min((int)rank * a.slice, a.vocab);
-    Row r(sh, min(a.slice, a.vocab - i_first), rank, ctas);
-    const int tid = r.tid, lane = r.lane, warp = r.warp, n = r.n;
-    const T *src = (const T *)a.logits + (int64_t)b * a.stride + i_first;
+    Row r(sh, cluster_rank(), cluster_size());
+    const uint32_t ctas = r.ctas, rank = r.rank;
+    const int b = blockIdx.x / ctas, tid = r.tid, lane = r.lane;
+    r.i_first = min((int)rank * a.slice, a.vocab);
+    r.n = min(a.slice, a.vocab - r.i_first);
+    const T *src = (const T *)a.logits + (int64_t)b * a.stride + r.i_first;
     const float temp = a.temperature ? a.temperature[b] : 1.0f;
     const int top_k = a.top_k ? a.top_k[b] : 0;
     const float top_p = a.top_p ? a.top_p[b] : 1.0f;
@@ -268,23 +386,29 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     u64 best = 0;
     unsigned live = 0;
 #pragma unroll 8
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < r.n; i += kThreads) {
         float x = (float)src[i];
         x = x == x ? x + 0.0f : -INFINITY;
-        sh.x[i] = x;
-        live += x != -INFINITY;
-        const u64 e = ((u64)key_of(x) << 32) | (0xFFFFFFFFu - (unsigned)(i_first + i));
+        const uint32_t k = key_of(x);
+        sh.key[i] = k;
+        live += k >= kLowest;
+        const u64 e = ((u64)k << 32) | (0xFFFFFFFFu - (unsigned)(r.i_first + i));
         best = e > best ? e : best;
     }
+    sh.bins[0][0][tid] = 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const u64 e = __shfl_xor_sync(kAll, best, o);
         best = e > best ? e : best;
     }
-    r.send<true>(best, __reduce_add_sync(kAll, live));
+    r.send<true>(best, __reduce_add_sync(kAll, live), ctas);
+    cluster_sync();
     best = 0;
-    for (uint32_t c = 0; c < ctas; ++c) best = r.part(c, 0) > best ? r.part(c, 0) : best;
-    const u64 alive = r.all(1);
+    u64 alive = 0;
+    for (uint32_t c = 0; c < ctas; ++c) {
+        best = r.part(c, 0) > best ? r.part(c, 0) : best;
+        alive += r.part(c, 1);
+    }
     r.top = value_of((uint32_t)(best >> 32));
     if (alive == 0 || greedy) {
         if (rank == 0 && tid == 0) {
@@ -294,173 +418,88 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         return;
     }
 
-    // The cut: entries with a key above `cut` are kept, and the first `ties` with that key.
     const bool by_k = top_k > 0 && (u64)top_k < alive, by_p = top_p < 1.0f;
-    uint32_t cut = kLowest;
-    u64 ties = ~0ull;
-    if (by_k || by_p) {
-        // first level: counts (the open bin's is what the others leave)
-        r.clear_bins(1);
-        for (int i = tid; i < n; i += kThreads) {
-            const int k = r.bin_of(sh.x[i]);
-            if (k < kBins - 1) atomicAdd(&sh.bins[r.turn_b][0][k], 1u);
+    if (!by_k && !by_p) {
+        r.finish<false>(a, b, 0, 0, 0, false, top_p, floor_w, 0);
+        cluster_sync();  // (no CTA leaves while another reads its bins)
+        return;
+    }
+    // first level: counts (the open bin's is what the others leave)
+    for (int i = tid; i < r.n; i += kThreads) {
+        const int k = r.bin_of(sh.key[i]);
+        if (k < kBins - 1) atomicAdd(&sh.bins[0][0][k], 1u);
+    }
+    u64 below, all;
+    u64 count = r.gather_bins<false, 1>(&below);
+    const u64 count_before = r.before(count, &all);
+    if (tid == kBins - 1) count = alive - count_before;
+    int bin = 0;
+    u64 ahead = 0;
+    if (by_k) {
+        r.find(count, count_before, (u64)top_k);
+    } else {
+        // a prefix of bins that is certain to hold top-p's cut (the open bin weighs nothing
+        // next to the slack: 2^18 e^-32)
+        const float mid = expf(-((float)tid + 0.5f) * 0.0625f);
+        float sum;
+        const float est = tid == kBins - 1 ? 0.0f : (float)count * mid, est_before = r.before(est, &sum);
+        const float want = top_p * sum * 1.0667f + 1e-6f;
+        if (tid == 0) sh.found[0] = kBins - 1;
+        __syncthreads();
+        if (est > 0.0f && est_before + est >= want) atomicMin(&sh.found[0], (u64)tid);
+        __syncthreads();
+    }
+    bin = (int)sh.found[0];
+    ahead = sh.found[1];
+    // entries in the bins up to that one: in the cluster, and in the CTAs below this one
+    u64 listed, at;
+    {
+        const u64 both = ((tid <= bin ? count : 0) << 32) + (tid <= bin ? below : 0);
+        u64 sum;
+        r.before(both, &sum);
+        listed = sum >> 32;
+        at = sum & 0xFFFFFFFFu;
+    }
+    if (listed <= kList && bin < kBins - 1) {
+        // into the first CTA's list, this CTA's entries from `at` on; their order is of no
+        // consequence. With top-p alone the whole mass is needed too.
+        if (tid == 0) sh.edge[0] = 0;
+        __syncthreads();
+        const uint32_t to = remote(&sh.list[0], 0);
+        u64 mass = 0;
+        for (int i0 = 0; i0 < r.n; i0 += kThreads) {
+            const int i = i0 + tid;
+            const uint32_t k = i < r.n ? sh.key[i] : 0;
+            const bool take = i < r.n && r.bin_of(k) <= bin;
+            const unsigned m = __ballot_sync(kAll, take);
+            if (m) {
+                unsigned base = 0;
+                if (lane == 0) base = atomicAdd(&sh.edge[0], (unsigned)__popc(m));
+                base = __shfl_sync(kAll, base, 0) + __popc(m & ((1u << lane) - 1));
+                if (take && at + base < kList) store_remote(to + 8 * ((uint32_t)at + base), ((u64)k << 32) | (uint32_t)(r.i_first + i));
+            }
+            if (!by_k && i < r.n) mass += Row::fixed(r.weight(k));
         }
-        u64 count = r.gather_bins<1>();
-        const u64 count_before = r.before(count);
-        if (tid == kBins - 1) count = alive - count_before;
+        r.send<false>(warp_sum(mass), 0, 1);
+        cluster_sync();
+        if (rank) return;
         u64 total = 0;
-        if (by_k) {
-            const auto reached = [&](u64 v) { return v >= (u64)top_k; };
-            int bin;
-            u64 ahead;
-            r.find(count, 0, reached, bin, ahead);
-            uint32_t lo, hi;
-            r.keys_of(bin, lo, hi);
-            r.narrow<false>(lo, hi, ahead, reached, cut);
-            ties = (u64)top_k - ahead;
-            if (tid > bin) count = 0;
-            if (tid == bin) count = (u64)top_k - count_before;
-        }
-        if (by_p) {
-            // the mass that top-k left
-            u64 m = 0;
-            for (int i = tid; i < n; i += kThreads) {
-                const float x = sh.x[i];
-                if (by_k ? key_of(x) > cut : true) m += Row::fixed(r.weight(x));
-            }
-            r.send<false>(warp_sum(m), 0);
-            total = r.all(0) + (by_k ? ties * Row::fixed(r.weight(value_of(cut))) : 0);
-            // (at least one unit, so that the first entry is kept whatever top_p is)
-            const double target = fmax((double)top_p * (double)total, 1.0);
-            const auto reached = [&](u64 v) { return (double)v >= target; };
-            // a guess of the bin: mass close to count x e^-middle, in double
-            const double guess = (double)count * (double)expf(-((float)tid + 0.5f) * 0.0625f);
-            const double g0 = r.before(guess), share = target * 0x1p-44;
-            if (tid == 0) sh.found[0] = kBins;
-            __syncthreads();
-            if (count && g0 + guess >= share) atomicMin(&sh.found[0], (u64)tid);
-            __syncthreads();
-            int bin = (int)sh.found[0];
-            __syncthreads();
-            bin = min(bin, kBins - 1);
-            for (;;) {
-                // the exact mass above the bin and in it
-                u64 above = 0, in = 0;
-                for (int i = tid; i < n; i += kThreads) {
-                    const float x = sh.x[i];
-                    const int k = r.bin_of(x);
-                    if (k <= bin) {
-                        const u64 f = Row::fixed(r.weight(x));
-                        if (k < bin) above += f;
-                        else in += f;
-                    }
-                }
-                r.send<false>(warp_sum(above), warp_sum(in));
-                above = r.all(0);
-                in = r.all(1);
-                if (reached(above)) {
-                    --bin;
-                } else if (!reached(above + in) && bin < kBins - 1) {
-                    ++bin;
-                } else {
-                    uint32_t lo, hi, key;
-                    r.keys_of(bin, lo, hi);
-                    u64 ahead = above;
-                    const u64 here = r.narrow<true>(lo, hi, ahead, reached, key);
-                    const u64 f = Row::fixed(r.weight(value_of(key)));
-                    // the fewest ties that reach the target, out of those that top-k kept
-                    u64 most = here / f, need = 1;
-                    if (by_k && key == cut) most = min(most, ties);
-                    const double left = target - (double)ahead;
-                    if (left > (double)f) need = (u64)ceil(left / (double)f);
-                    while (need > 1 && reached(ahead + (need - 1) * f)) --need;
-                    while (need < most && !reached(ahead + need * f)) ++need;
-                    cut = key;
-                    ties = min(need, most);
-                    break;
-                }
-            }
-        }
+        for (uint32_t c = 0; c < ctas; ++c) total += r.part(c, 0);
+        r.n = (int)listed;
+        r.finish<true>(a, b, by_k ? (u64)top_k : 0, bin, ahead, by_p, top_p, floor_w, total);
+        return;
     }
-
-    // Kept mass, in index order: per warp's segment of the slice, per CTA. Ties are counted
-    // apart: they weigh the same, and how many of a segment's are kept follows from the
-    // ties ahead of it.
-    const bool all_ties = ties == ~0ull;  // nothing was cut: `cut` is the lowest key, and kept
-    const u64 tie_f = [&] {
-        const float w = r.weight(value_of(cut));
-        return w >= floor_w ? Row::fixed(w) : 0ull;
-    }();
-    const int per = (n + kWarps - 1) / kWarps, s0 = min(warp * per, n), s1 = min(s0 + per, n);
-    u64 mass = 0;
-    unsigned tied = 0;
-    for (int i = s0 + lane; i < s1; i += 32) {
-        const float x = sh.x[i];
-        const uint32_t k = key_of(x);
-        if (k > cut || (all_ties && k == cut)) {
-            const float w = r.weight(x);
-            mass += w >= floor_w ? Row::fixed(w) : 0ull;
-        }
-        tied += !all_ties && k == cut;
-    }
-    mass = warp_sum(mass);
-    tied = __reduce_add_sync(kAll, tied);
-    r.send<false>(mass, tied);
-    const auto clip = [&](u64 t0, u64 t) {  // of t ties after t0 others, how many are kept
-        return t0 >= ties ? 0ull : min(t, ties - t0);
-    };
-    u64 whole = 0, ahead = 0, t_ahead = 0, t_all = 0;
-    for (uint32_t c = 0; c < ctas; ++c) {
-        const u64 m = r.part(c, 0) + clip(t_all, r.part(c, 1)) * tie_f;
-        if (c == rank) ahead = whole, t_ahead = t_all;
-        whole += m;
-        t_all += r.part(c, 1);
-    }
-    // sums of the warps' segments ahead of this one (send() left them in place)
-    for (int w = 0; w < warp; ++w) {
-        ahead += sh.warp[w][0] + clip(t_ahead, sh.warp[w][1]) * tie_f;
-        t_ahead += sh.warp[w][1];
-    }
-    const u64 mine = mass + clip(t_ahead, tied) * tie_f;
-    const double target = fmax((double)a.u[b], 0.0) * (double)whole;
-    // u = 1 asks for the last kept entry: the segment that ends at the whole
-    const bool at_end = !((double)whole > target);
-    if (mine == 0 || !(at_end ? ahead + mine == whole : (double)ahead <= target && (double)(ahead + mine) > target)) return;
-    u64 sum = ahead, seen = t_ahead;
-    for (int i = s0; i < s1; i += 32) {
-        const float x = i + lane < s1 ? sh.x[i + lane] : -INFINITY;
-        const uint32_t k = key_of(x);
-        const bool tie = !all_ties && k == cut;
-        const unsigned m = __ballot_sync(kAll, tie);
-        const bool keep = k > cut || (all_ties && k == cut) || (tie && seen + __popc(m & ((1u << lane) - 1)) < ties);
-        const float w = keep ? r.weight(x) : 0.0f;
-        const u64 f = keep && w >= floor_w ? Row::fixed(w) : 0ull;
-        u64 incl = f;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 e = __shfl_up_sync(kAll, incl, o);
-            if (lane >= o) incl += e;
-        }
-        const unsigned hit = __ballot_sync(kAll, f && (at_end ? sum + incl == whole : (double)(sum + incl) > target));
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            if (lane == l) {
-                a.tokens[b] = i_first + i + l;
-                if (a.logprobs) a.logprobs[b] = (float)log((double)w / ((double)whole * 0x1p-44));
-            }
-            return;
-        }
-        sum += __shfl_sync(kAll, incl, 31);
-        seen += __popc(m);
-    }
+    r.finish<false>(a, b, by_k ? (u64)top_k : 0, bin, ahead, by_p, top_p, floor_w, 0);
+    cluster_sync();
 }
 
-// CTAs per row: enough to hold it (32768 entries each, half of that where it leaves two
-// CTAs an SM), and, with few rows, to give every SM two, down to slices of 2048 entries.
+// CTAs per row: enough to hold it (16384 entries each, which leaves room for two CTAs an
+// SM, 32768 above 2^17), and more while all of them still run at once, down to slices of
+// 2048 entries.
 int cluster_for(int rows, int vocab, int sm_count) {
     int c = 1;
     while (c < kMaxCluster && vocab > c * (kSlice / 2)) c *= 2;
-    while (c < kMaxCluster && rows * c < 2 * sm_count && vocab > c * 2048) c *= 2;
+    while (c < kMaxCluster && 2 * c * rows <= 2 * sm_count && vocab > c * 2048) c *= 2;
     return c;
 }
 

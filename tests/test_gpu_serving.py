@@ -460,6 +460,20 @@ def test_sample_follows_the_distribution(qdq):
     assert np.abs(share - w / w.sum()).max() <= 1.5 / B
 
 
+@pytest.mark.parametrize("dtype,vocab", [("f32", 50000), ("bf16", 200003)])
+def test_sample_wide_cuts(qdq, dtype, vocab):
+    """Kept sets from a handful of entries to most of the row: both sides of the gathered list's
+    length, cuts in the open bin, and 16-bit logits whose cuts fall among thousands of ties."""
+    rng = np.random.default_rng(vocab)
+    B = 10
+    x = torch.from_numpy(rng.standard_normal((B, vocab)) * np.linspace(0.3, 6, B)[:, None]).to(DT[dtype]).cuda()
+    for k in (1, 2, 1500, 2047, 2048, 2049, 2500, vocab // 2, vocab - 1):
+        check_sample(qdq, x, rng.uniform(0, 1, B).astype(np.float32), top_k=k, temperature=rng.uniform(0.2, 2, B))
+    for p in (0.01, 0.3, 0.6, 0.9, 0.96, 0.999, 0.999999):
+        check_sample(qdq, x, rng.uniform(0, 1, B).astype(np.float32), top_p=p, temperature=rng.uniform(0.2, 2, B))
+        check_sample(qdq, x, rng.uniform(0, 1, B).astype(np.float32), top_p=p, top_k=5000, min_p=0.02)
+
+
 def test_sample_extreme_parameters(qdq):
     """Temperatures near the ends of fp32, random numbers outside [0, 1), a top-k far in the open bin."""
     rng = np.random.default_rng(8)
