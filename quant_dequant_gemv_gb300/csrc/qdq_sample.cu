@@ -1,22 +1,19 @@
 // qdq_sample.cu -- sampling: temperature, top-k, top-p and min-p from given random
 // numbers.
 //
-// One pass over the logits: a cluster of up to eight CTAs holds a row's order-preserving
-// 32-bit keys in shared memory, a contiguous slice each, and everything after the load
-// works on those.
+// One pass over the logits: a cluster of up to eight CTAs holds a row in shared memory, a
+// contiguous slice each, and everything after the load works on those.
 //
 // The filters are cuts of one order (logit descending, index ascending), so nothing is
-// sorted. A cut is found by narrowing: 512 bins over an interval of keys, a scan, and the
-// bin that reaches the wanted count or mass becomes the next interval until it is one
-// key. The first bins are linear in the exponent (1/16 wide, the last one open) instead
-// of the key; the entries that share the cut's key are told apart by narrowing over their
-// indices, and so is the draw itself (an inverse CDF in index order).
-//
-// The first counts bound the kept set from above: all entries of a bin have weights
-// within a factor e^(1/16), so a prefix of bins whose estimated mass exceeds top-p's share
-// of the estimated whole by 1/15 is certain to hold the cut. If that prefix (or top-k's
-// bin) has at most kList entries, they are gathered in the first CTA, which finishes
-// alone while the others leave; otherwise the cluster narrows together.
+// sorted. A cut is found by narrowing: 512 bins over an interval of the logits' order-
+// preserving 32-bit keys, a scan, and the bin that reaches the wanted count or mass
+// becomes the next interval until it is one key. The first bins are linear in the
+// exponent (1/16 wide) instead of the key; the last of them is open, and its entries
+// weigh less than half a unit each. The entries that share the cut's key are told apart
+// by narrowing over their indices, and so is the draw itself (an inverse CDF in index
+// order). If the bins up to the one that holds the first cut have at most kList entries,
+// those are gathered in the first CTA, which finishes alone while the others leave;
+// otherwise the cluster narrows together.
 //
 // Masses are integers (weights in units of 2^-44 of the largest), so neither the order of
 // the additions nor the split over CTAs changes a sum. In the bins they are kept as three
@@ -58,13 +55,13 @@ QDQ_DEV uint32_t key_of(float x) {
 QDQ_DEV float value_of(uint32_t k) { return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu)); }
 
 struct Shared {
-    unsigned bins[2][3][kBins];
+    unsigned bins[2][4][kBins];   // three pieces of mass (or a count in the first), and a count
     u64 sums[2][kMaxCluster][2];  // what the cluster's CTAs sent
     u64 warp[kWarps + 1][2];
     u64 found[2];                 // the bin a cut lies in, and the measure above it
     uint32_t edge[2];
     u64 list[kList];              // key << 32 | index
-    uint32_t key[1];              // the slice (slice entries)
+    __align__(16) float x[4];     // the slice (slice entries)
 };
 
 QDQ_DEV void cluster_sync() {
@@ -106,25 +103,52 @@ struct Row {
     QDQ_DEV Row(Shared &s, uint32_t r, uint32_t c)
         : sh(s), tid(threadIdx.x), lane(threadIdx.x & 31), warp(threadIdx.x >> 5), rank(r), ctas(c) {}
 
-    QDQ_DEV float weight(uint32_t key) const {  // (-inf weighs 0)
-        const float x = value_of(key);
-        return x == top ? 1.0f : expf((x - top) * inv);
+    QDQ_DEV float weight(float x) const { return x == top ? 1.0f : expf((x - top) * inv); }  // (-inf weighs 0)
+    // A weight in units of 2^-44, as three pieces of 15 bits (the highest may be 2^14): adding
+    // 2^23 and rounding down leaves the whole part in the low mantissa bits.
+    static QDQ_DEV unsigned whole(float &v) {
+        const float t = __fadd_rz(v, 8388608.0f);
+        v -= t - 8388608.0f;
+        return __float_as_uint(t) & 0x7FFFFFu;
     }
-    static QDQ_DEV u64 fixed(float w) { return __float2ull_rn(w * 0x1p44f); }
+    static QDQ_DEV void pieces(float w, unsigned (&p)[3]) {
+        float v = w * 16384.0f;
+        p[2] = whole(v);
+        v *= 32768.0f;
+        p[1] = whole(v);
+        v = v * 32768.0f + 0.5f;
+        p[0] = whole(v);  // (2^15 where the half carries)
+    }
+    static QDQ_DEV u64 fixed(float w) {
+        unsigned p[3];
+        pieces(w, p);
+        return ((u64)p[2] << 30) + ((u64)p[1] << 15) + p[0];
+    }
     // The first level's bin: 1/16 of the exponent wide, falling logits, the last one open.
-    QDQ_DEV int bin_of(uint32_t key) const { return min((int)((top - value_of(key)) * inv * 16.0f), kBins - 1); }
+    QDQ_DEV int bin_of(float x) const {
+        const float v = (top - x) * inv * 16.0f;
+        if (!(v < (float)(kBins - 1))) return x == top ? 0 : kBins - 1;  // (inf - inf, 0 x inf)
+        return (int)(__float_as_uint(__fadd_rz(v, 8388608.0f)) & (kBins - 1));
+    }
 
     template <bool ALONE>
     QDQ_DEV void sync() {
         if (ALONE) __syncthreads();
         else cluster_sync();
     }
+    // f(logit, index) over this CTA's entries (and over the -inf that fill the slice up).
     template <bool ALONE, typename F>
-    QDQ_DEV void each(F f) {  // f(key, index) over this CTA's entries
+    QDQ_DEV void each(F f) {
         if (ALONE) {
-            for (int i = tid; i < n; i += kThreads) f((uint32_t)(sh.list[i] >> 32), (uint32_t)sh.list[i]);
+            for (int i = tid; i < n; i += kThreads) f(value_of((uint32_t)(sh.list[i] >> 32)), (uint32_t)sh.list[i]);
         } else {
-            for (int i = tid; i < n; i += kThreads) f(sh.key[i], (uint32_t)(i_first + i));
+            for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+                const float4 x = *reinterpret_cast<const float4 *>(sh.x + i);
+                f(x.x, (uint32_t)(i_first + i));
+                f(x.y, (uint32_t)(i_first + i + 1));
+                f(x.z, (uint32_t)(i_first + i + 2));
+                f(x.w, (uint32_t)(i_first + i + 3));
+            }
         }
     }
 
@@ -156,33 +180,37 @@ struct Row {
         for (int i = 0; i < pieces; ++i) sh.bins[turn_b][i][tid] = 0;
         __syncthreads();
     }
-    QDQ_DEV void add_mass(int b, u64 f) {
-        atomicAdd(&sh.bins[turn_b][0][b], (unsigned)f & 0x7FFFu);
-        atomicAdd(&sh.bins[turn_b][1][b], (unsigned)(f >> 15) & 0x7FFFu);
-        atomicAdd(&sh.bins[turn_b][2][b], (unsigned)(f >> 30));
+    QDQ_DEV void add_mass(int b, float w) {
+        unsigned p[3];
+        pieces(w, p);
+        for (int i = 0; i < 3; ++i) atomicAdd(&sh.bins[turn_b][i][b], p[i]);
     }
-    // Bin `tid` over the whole cluster (each CTA reads all the others'), and over the CTAs
-    // below this one; ends the turn.
+    // Bin `tid` over the whole cluster (each CTA reads all the others'): PIECES of mass, or a
+    // count with PIECES = 1. With a `below`: the fourth array too, as a count, over the whole
+    // cluster and over the CTAs below this one. Ends the turn.
     template <bool ALONE, int PIECES>
-    QDQ_DEV u64 gather_bins(u64 *below = nullptr) {
+    QDQ_DEV u64 gather_bins(unsigned *count = nullptr, unsigned *below = nullptr) {
         sync<ALONE>();
-        u64 v = 0, low = 0;
+        u64 v = 0;
         if (ALONE) {
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) v += (u64)sh.bins[turn_b][i][tid] << (15 * i);
         } else {
-            unsigned x[PIECES];
+            unsigned c = 0;
 #pragma unroll 4
             for (uint32_t r = 0; r < ctas; ++r) {
-                if (r == rank) low = v;
+                unsigned x[4] = {};
 #pragma unroll
-                for (int i = 0; i < PIECES; ++i)
-                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x[i]) : "r"(remote(&sh.bins[turn_b][i][tid], r)));
+                for (int i = 0; i < 4; ++i)
+                    if (i < PIECES || (i == 3 && below))
+                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x[i]) : "r"(remote(&sh.bins[turn_b][i][tid], r)));
+                if (below && r == rank) *below = c;
+                c += x[3];
 #pragma unroll
                 for (int i = 0; i < PIECES; ++i) v += (u64)x[i] << (15 * i);
             }
+            if (below) *count = c;
         }
-        if (below) *below = low;
         turn_b ^= 1;
         return v;
     }
@@ -226,13 +254,13 @@ struct Row {
             if (want >= 0 && first < last) {
                 const uint32_t mid = key_of(top - (float)(want + 1) * 0.0625f / inv);
                 const uint32_t at = min(max(mid, first + 16) - 16 + lane, last);
-                const unsigned m = __ballot_sync(kAll, bin_of(at) <= want);
+                const unsigned m = __ballot_sync(kAll, bin_of(value_of(at)) <= want);
                 if (m && !(m & 1)) first = last = __shfl_sync(kAll, at, __ffs(m) - 1);
             }
             while (first < last && want >= 0) {
                 const uint32_t step = (last - first) / 32 + 1;
                 const u64 at = (u64)first + (u64)step * lane;
-                const unsigned m = __ballot_sync(kAll, at >= last || bin_of((uint32_t)at) <= want);
+                const unsigned m = __ballot_sync(kAll, at >= last || bin_of(value_of((uint32_t)at)) <= want);
                 const int l = __ffs(m) - 1;  // the answer is at most lane l's probe, above lane l - 1's
                 if (m == 0) {
                     first = first + step * 31 + 1;
@@ -249,23 +277,62 @@ struct Row {
         hi = sh.edge[1] - 1;
     }
 
+    // Bins over the index: 128 neighbours share a bin of 128 or more, so a warp adds its sum
+    // once (their atomics would all meet at one address).
+    template <bool MASS, typename GET>
+    QDQ_DEV void bin_neighbours(int shift, GET get) {
+        for (int i0 = warp * 128; i0 < n; i0 += 4 * kThreads) {
+            const int i = i0 + 4 * lane;  // (the slice is filled up to a multiple of 128)
+            const float4 v = *reinterpret_cast<const float4 *>(sh.x + i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            unsigned sum[3] = {};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                uint32_t k;
+                if (!get(x[y], (uint32_t)(i_first + i + y), k)) continue;
+                if (MASS) {
+                    unsigned p[3];
+                    pieces(weight(x[y]), p);
+                    sum[0] += p[0], sum[1] += p[1], sum[2] += p[2];
+                } else {
+                    ++sum[0];
+                }
+            }
+            unsigned *at = &sh.bins[turn_b][0][(i_first + i0) >> shift];
+#pragma unroll
+            for (int y = 0; y < (MASS ? 3 : 1); ++y) {
+                const unsigned t = __reduce_add_sync(kAll, sum[y]);
+                if (lane == 0 && t) atomicAdd(at + y * kBins, t);
+            }
+        }
+    }
+
     // The largest key in [lo, hi] at which the measure from hi down (from `ahead` on)
     // reaches the target; `ahead` becomes the measure above it; returns its own. get(key,
     // index, k, f): whether an entry counts, under which key, with which mass. With SHARE
     // the target is the share of the whole that `share` asks for, set at the first level.
-    template <bool ALONE, bool MASS, bool SHARE = false, typename GET>
+    // INDEX: the keys are inverted indices, and [lo, hi] begins as all of them.
+    template <bool ALONE, bool MASS, bool INDEX = false, bool SHARE = false, typename GET>
     QDQ_DEV u64 narrow(uint32_t lo, uint32_t hi, u64 &ahead, u64 &target, uint32_t &key, GET get, double share = 0.0,
                        u64 *whole = nullptr) {
         for (int level = 0; level < 4; ++level) {  // 9 bits a level: 32 bits take four
-            const int shift = max(0, 32 - 9 - __clz(hi - lo));
+            // (a level over neighbours has bins of 128 at least)
+            const bool neighbours = INDEX && !ALONE && level == 0;
+            const int shift = max(neighbours ? 7 : 0, 32 - 9 - __clz(hi - lo));
             clear_bins(MASS ? 3 : 1);
-            each<ALONE>([&](uint32_t entry, uint32_t index) {
-                uint32_t k;
-                if (!get(entry, index, k) || k < lo || k > hi) return;
-                const int b = (int)((hi - k) >> shift);
-                if (MASS) add_mass(b, fixed(weight(entry)));
-                else atomicAdd(&sh.bins[turn_b][0][b], 1u);
-            });
+            if (neighbours) {
+                bin_neighbours<MASS>(shift, get);
+            } else {
+                const float x_lo = value_of(lo), x_hi = value_of(hi);
+                each<ALONE>([&](float x, uint32_t index) {
+                    if (!INDEX && !(x >= x_lo && x <= x_hi)) return;
+                    uint32_t k;
+                    if (!get(x, index, k) || k < lo || k > hi) return;
+                    const int b = (int)((hi - k) >> shift);
+                    if (MASS) add_mass(b, weight(x));
+                    else atomicAdd(&sh.bins[turn_b][0][b], 1u);
+                });
+            }
             const u64 v = gather_bins<ALONE, MASS ? 3 : 1>();
             u64 all;
             const u64 excl = ahead + before(v, &all);
@@ -291,76 +358,84 @@ struct Row {
         return 1;
     }
 
-    // Everything after the first counts: the cuts, the ties, the draw. bin, ahead: top-k's
-    // first-level bin and the count above it.
+    // Everything after the first level: the cuts, the ties, the draw. top_k: 0, or with the
+    // first-level bin of its cut and the count above that; top_p: below 1 if it is used, and
+    // without top-k with its cut's bin, the mass above that and the mass to reach.
+    struct First {
+        u64 top_k, ahead, target;
+        int bin;
+    };
     template <bool ALONE>
-    QDQ_DEV void finish(const SampleArgs &a, int b, u64 top_k, int bin, u64 ahead, bool by_p, float top_p, float floor_w,
-                        u64 total) {
+    QDQ_DEV void finish(const SampleArgs &a, int b, First first, float top_p, float floor_w) {
         uint32_t cut = kLowest, lo, hi;
-        u64 ties = ~0ull, here = 0, target;  // entries above `cut` are kept, and the first `ties` at it
-        if (top_k) {
-            keys_of(bin, lo, hi);
-            target = top_k;
-            here = narrow<ALONE, false>(lo, hi, ahead, target, cut, [](uint32_t e, uint32_t, uint32_t &k) { return k = e, true; });
-            ties = top_k - ahead;
+        u64 ties = ~0ull, here = 0;  // entries above `cut` are kept, and the first `ties` at it
+        const auto by_key = [](float x, uint32_t, uint32_t &k) { return k = key_of(x), true; };
+        if (first.top_k) {
+            keys_of(first.bin, lo, hi);
+            here = narrow<ALONE, false>(lo, hi, first.ahead, first.top_k, cut, by_key);
+            ties = first.top_k - first.ahead;
         }
-        if (by_p) {
-            // exact masses of the first-level bins of what top-k left; their sum is the whole,
-            // but for a list, which holds part of it unless top-k chose it. The cut's own bin
-            // may hold more ties than top-k kept: none that the target reaches.
-            clear_bins(3);
-            u64 low = 0;  // mass of the ties that top-k dropped
-            each<ALONE>([&](uint32_t key, uint32_t) {
-                if (key >= cut) add_mass(bin_of(key), fixed(weight(key)));
-            });
-            if (top_k) low = (here - ties) * fixed(weight(cut));
-            const u64 v = gather_bins<ALONE, 3>();
-            u64 all;
-            const u64 excl = before(v, &all);
-            if (!ALONE || top_k) total = all - low;
-            // (at least one unit, so that the first entry is kept whatever top_p is)
-            const double share = (double)top_p * (double)total;
-            target = share < 1.0 ? 1 : (u64)ceil(share);
-            find(v, excl, target);
-            const int p_bin = (int)sh.found[0] & (kBins - 1);
-            u64 above = sh.found[1];
-            keys_of(p_bin, lo, hi);
+        if (top_p < 1.0f) {
+            if (first.top_k) {
+                // exact masses of what top-k left, in the first level's bins. The cut's own bin may
+                // hold more ties than top-k kept: the lowest entries, none that the target needs.
+                clear_bins(3);
+                const float x_cut = value_of(cut);
+                each<ALONE>([&](float x, uint32_t) {
+                    if (!(x >= x_cut)) return;
+                    const int k = bin_of(x);
+                    if (k < kBins - 1) add_mass(k, weight(x));
+                });
+                const u64 v = gather_bins<ALONE, 3>();
+                u64 all;
+                const u64 excl = before(v, &all);
+                const u64 dropped = bin_of(x_cut) < kBins - 1 ? (here - ties) * fixed(weight(x_cut)) : 0;
+                first.target = reach(top_p, all - dropped);
+                find(v, excl, first.target);
+                first.bin = (int)sh.found[0] & (kBins - 1);
+                first.ahead = sh.found[1];
+            }
+            keys_of(first.bin, lo, hi);
             uint32_t key;
-            const u64 mass = narrow<ALONE, true>(max(lo, cut), hi, above, target, key,
-                                                 [](uint32_t e, uint32_t, uint32_t &k) { return k = e, true; });
+            const u64 mass = narrow<ALONE, true>(max(lo, cut), hi, first.ahead, first.target, key, by_key);
             // the fewest of the entries at the key that reach the target
-            const u64 f = fixed(weight(key)), need = (target - above + f - 1) / f;
-            const u64 most = top_k && key == cut ? ties : mass / f;
+            const u64 f = fixed(weight(value_of(key))), need = (first.target - first.ahead + f - 1) / f;
             here = mass / f;
+            ties = min(need, first.top_k && key == cut ? ties : here);
             cut = key;
-            ties = min(need, most);
         }
+        const float x_cut = value_of(cut);
         // ties: the index of the last one kept (narrowing runs over inverted indices, so that
         // the lowest come first)
         uint32_t tie_last = 0xFFFFFFFFu;
         if (ties < here) {
             u64 none = 0;
             uint32_t inverted;
-            narrow<ALONE, false>(0xFFFFFFFFu - (uint32_t)(a.vocab - 1), 0xFFFFFFFFu, none, ties, inverted,
-                                 [&](uint32_t e, uint32_t i, uint32_t &k) { return k = ~i, e == cut; });
+            narrow<ALONE, false, true>(0xFFFFFFFFu - (uint32_t)(a.vocab - 1), 0xFFFFFFFFu, none, ties, inverted,
+                                       [&](float x, uint32_t i, uint32_t &k) { return k = ~i, x == x_cut; });
             tie_last = ~inverted;
         }
         // the draw: the first index at which the running mass of the kept entries exceeds u of
         // the whole (at u = 1, reaches the whole)
         uint32_t inverted;
-        u64 mass_ahead = 0, whole;
-        narrow<ALONE, true, true>(0xFFFFFFFFu - (uint32_t)(a.vocab - 1), 0xFFFFFFFFu, mass_ahead, target, inverted,
-                                  [&](uint32_t e, uint32_t i, uint32_t &k) {
-                                      k = ~i;
-                                      return (e > cut || (e == cut && i <= tie_last)) && weight(e) >= floor_w;
-                                  },
-                                  fmin(fmax((double)a.u[b], 0.0), 1.0), &whole);
+        u64 mass_ahead = 0, whole_mass;
+        narrow<ALONE, true, true, true>(0xFFFFFFFFu - (uint32_t)(a.vocab - 1), 0xFFFFFFFFu, mass_ahead, first.target, inverted,
+                                        [&](float x, uint32_t i, uint32_t &k) {
+                                            k = ~i;
+                                            return (x > x_cut || (x == x_cut && i <= tie_last)) && weight(x) >= floor_w;
+                                        },
+                                        fmin(fmax((double)a.u[b], 0.0), 1.0), &whole_mass);
         const uint32_t token = ~inverted;
-        each<ALONE>([&](uint32_t key, uint32_t index) {
+        each<ALONE>([&](float x, uint32_t index) {
             if (index != token) return;
             a.tokens[b] = (int64_t)token;
-            if (a.logprobs) a.logprobs[b] = (float)log((double)weight(key) / ((double)whole * 0x1p-44));
+            if (a.logprobs) a.logprobs[b] = (float)log((double)weight(x) / ((double)whole_mass * 0x1p-44));
         });
+    }
+    // top-p's mass to reach: at least one unit, so that the first entry is kept whatever it is.
+    static QDQ_DEV u64 reach(float top_p, u64 whole_mass) {
+        const double share = (double)top_p * (double)whole_mass;
+        return share < 1.0 ? 1 : (u64)ceil(share);
     }
 };
 
@@ -370,7 +445,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     Row r(sh, cluster_rank(), cluster_size());
     const uint32_t ctas = r.ctas, rank = r.rank;
-    const int b = blockIdx.x / ctas, tid = r.tid, lane = r.lane;
+    const int b = blockIdx.x / ctas, tid = r.tid;
     r.i_first = min((int)rank * a.slice, a.vocab);
     r.n = min(a.slice, a.vocab - r.i_first);
     const T *src = (const T *)a.logits + (int64_t)b * a.stride + r.i_first;
@@ -389,13 +464,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     for (int i = tid; i < r.n; i += kThreads) {
         float x = (float)src[i];
         x = x == x ? x + 0.0f : -INFINITY;
-        const uint32_t k = key_of(x);
-        sh.key[i] = k;
-        live += k >= kLowest;
-        const u64 e = ((u64)k << 32) | (0xFFFFFFFFu - (unsigned)(r.i_first + i));
+        sh.x[i] = x;
+        live += x != -INFINITY;
+        const u64 e = ((u64)key_of(x) << 32) | (0xFFFFFFFFu - (unsigned)(r.i_first + i));
         best = e > best ? e : best;
     }
-    sh.bins[0][0][tid] = 0;
+    for (int i = r.n + tid; i < (r.n + 127) / 128 * 128; i += kThreads) sh.x[i] = -INFINITY;
+    for (int i = 0; i < 4; ++i) sh.bins[0][i][tid] = 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const u64 e = __shfl_xor_sync(kAll, best, o);
@@ -419,77 +494,58 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     }
 
     const bool by_k = top_k > 0 && (u64)top_k < alive, by_p = top_p < 1.0f;
+    Row::First first = {by_k ? (u64)top_k : 0, 0, 0, 0};
+    const float share = by_p ? top_p : 1.0f;
     if (!by_k && !by_p) {
-        r.finish<false>(a, b, 0, 0, 0, false, top_p, floor_w, 0);
+        r.finish<false>(a, b, first, share, floor_w);
         cluster_sync();  // (no CTA leaves while another reads its bins)
         return;
     }
-    // first level: counts (the open bin's is what the others leave)
-    for (int i = tid; i < r.n; i += kThreads) {
-        const int k = r.bin_of(sh.key[i]);
-        if (k < kBins - 1) atomicAdd(&sh.bins[0][0][k], 1u);
-    }
-    u64 below, all;
-    u64 count = r.gather_bins<false, 1>(&below);
-    const u64 count_before = r.before(count, &all);
-    if (tid == kBins - 1) count = alive - count_before;
-    int bin = 0;
-    u64 ahead = 0;
+    // first level: counts (the open bin's is what the others leave), and for top-p alone masses
+    r.each<false>([&](float x, uint32_t) {
+        const int k = r.bin_of(x);
+        if (k == kBins - 1) return;
+        atomicAdd(&sh.bins[0][3][k], 1u);
+        if (!by_k) r.add_mass(k, r.weight(x));
+    });
+    unsigned count, below;
     if (by_k) {
-        r.find(count, count_before, (u64)top_k);
+        r.gather_bins<false, 0>(&count, &below);
+        u64 all;
+        const u64 ahead = r.before((u64)count, &all);
+        r.find(tid == kBins - 1 ? alive - ahead : count, ahead, (u64)top_k);
     } else {
-        // a prefix of bins that is certain to hold top-p's cut (the open bin weighs nothing
-        // next to the slack: 2^18 e^-32)
-        const float mid = expf(-((float)tid + 0.5f) * 0.0625f);
-        float sum;
-        const float est = tid == kBins - 1 ? 0.0f : (float)count * mid, est_before = r.before(est, &sum);
-        const float want = top_p * sum * 1.0667f + 1e-6f;
-        if (tid == 0) sh.found[0] = kBins - 1;
-        __syncthreads();
-        if (est > 0.0f && est_before + est >= want) atomicMin(&sh.found[0], (u64)tid);
-        __syncthreads();
+        const u64 mass = r.gather_bins<false, 3>(&count, &below);
+        u64 all;
+        const u64 ahead = r.before(mass, &all);
+        first.target = Row::reach(top_p, all);
+        r.find(mass, ahead, first.target);
     }
-    bin = (int)sh.found[0];
-    ahead = sh.found[1];
-    // entries in the bins up to that one: in the cluster, and in the CTAs below this one
-    u64 listed, at;
-    {
-        const u64 both = ((tid <= bin ? count : 0) << 32) + (tid <= bin ? below : 0);
-        u64 sum;
-        r.before(both, &sum);
-        listed = sum >> 32;
-        at = sum & 0xFFFFFFFFu;
-    }
-    if (listed <= kList && bin < kBins - 1) {
-        // into the first CTA's list, this CTA's entries from `at` on; their order is of no
-        // consequence. With top-p alone the whole mass is needed too.
-        if (tid == 0) sh.edge[0] = 0;
-        __syncthreads();
-        const uint32_t to = remote(&sh.list[0], 0);
-        u64 mass = 0;
-        for (int i0 = 0; i0 < r.n; i0 += kThreads) {
-            const int i = i0 + tid;
-            const uint32_t k = i < r.n ? sh.key[i] : 0;
-            const bool take = i < r.n && r.bin_of(k) <= bin;
-            const unsigned m = __ballot_sync(kAll, take);
-            if (m) {
-                unsigned base = 0;
-                if (lane == 0) base = atomicAdd(&sh.edge[0], (unsigned)__popc(m));
-                base = __shfl_sync(kAll, base, 0) + __popc(m & ((1u << lane) - 1));
-                if (take && at + base < kList) store_remote(to + 8 * ((uint32_t)at + base), ((u64)k << 32) | (uint32_t)(r.i_first + i));
-            }
-            if (!by_k && i < r.n) mass += Row::fixed(r.weight(k));
+    first.bin = (int)sh.found[0] & (kBins - 1);
+    first.ahead = sh.found[1];
+    if (first.bin < kBins - 1) {
+        // entries in the bins up to that one: in the cluster, and in the CTAs below this one
+        u64 both;
+        r.before(tid <= first.bin ? ((u64)count << 32) + below : 0ull, &both);
+        const unsigned listed = (unsigned)(both >> 32), at = (unsigned)both;
+        if (listed <= kList) {
+            // into the first CTA's list, this CTA's from `at` on; their order there is of no consequence
+            if (tid == 0) sh.edge[0] = 0;
+            __syncthreads();
+            const uint32_t to = remote(&sh.list[0], 0);
+            r.each<false>([&](float x, uint32_t index) {
+                if (r.bin_of(x) > first.bin) return;
+                const unsigned i = at + atomicAdd(&sh.edge[0], 1u);
+                if (i < kList) store_remote(to + 8 * i, ((u64)key_of(x) << 32) | index);
+            });
+            cluster_sync();
+            if (rank) return;
+            r.n = (int)listed;
+            r.finish<true>(a, b, first, share, floor_w);
+            return;
         }
-        r.send<false>(warp_sum(mass), 0, 1);
-        cluster_sync();
-        if (rank) return;
-        u64 total = 0;
-        for (uint32_t c = 0; c < ctas; ++c) total += r.part(c, 0);
-        r.n = (int)listed;
-        r.finish<true>(a, b, by_k ? (u64)top_k : 0, bin, ahead, by_p, top_p, floor_w, total);
-        return;
     }
-    r.finish<false>(a, b, by_k ? (u64)top_k : 0, bin, ahead, by_p, top_p, floor_w, 0);
+    r.finish<false>(a, b, first, share, floor_w);
     cluster_sync();
 }
 
@@ -506,7 +562,7 @@ int cluster_for(int rows, int vocab, int sm_count) {
 template <typename T>
 int launch_sample(SampleArgs a, int sm_count, cudaStream_t stream) {
     const int c = cluster_for(a.rows, a.vocab, sm_count);
-    a.slice = ((a.vocab + c - 1) / c + 7) / 8 * 8;
+    a.slice = ((a.vocab + c - 1) / c + 127) / 128 * 128;  // (a warp's 128 neighbours share an index bin)
     const size_t smem = sizeof(Shared) + sizeof(float) * a.slice;
     static std::mutex mu;
     static bool attr_set[64] = {};
