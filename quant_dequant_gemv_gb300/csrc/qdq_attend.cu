@@ -92,15 +92,14 @@ constexpr int kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 21, kBa
               kBarOFree = 28, kBarDrain = 30;
 
 struct Start {
-    long long pos, end;
-    int seq, block, head, off, ctas, live;
+    long long total, item, pos, end;  // units: of all items, where the first one begins, the CTA's range
+    int seq, block, head, ctas, live;
 };
 
 // A walk over the pieces of a CTA's range; every role walks it by itself.
 struct Walk {
-    long long pos;   // first key tile of the piece, in the order of all
-    long long left;  // key tiles of the range from there on
-    int seq, block, head, off;
+    long long item, pos, end;  // units: where the item begins, the rest of the range
+    int seq, block, head, off, n;  // the piece: n key tiles from the item's off-th on
     int first, count, kv;
     AttendBlock b;
     QDQ_DEV void load_seq(const KernelArgs &a) {
@@ -108,31 +107,35 @@ struct Walk {
         kv = max(a.kv_len[seq], 0);
     }
     QDQ_DEV Walk(const KernelArgs &a, const Start &s)
-        : pos(s.pos), left(s.end - s.pos), seq(s.seq), block(s.block), head(s.head), off(s.off) {
+        : item(s.item), pos(s.pos), end(s.end), seq(s.seq), block(s.block), head(s.head) {
         load_seq(a);
         b = block_of(a.g, count, kv, block);
+        int last;
+        piece_of(b, item, pos, end, off, last);
+        n = last - off;
+        if (n == 0) next(a);  // (the range begins past the item's tiles or ends before them)
     }
+    QDQ_DEV bool more() const { return n > 0; }
     QDQ_DEV int t_beg() const { return b.t0 + off; }
-    QDQ_DEV int len() const { return (int)min((long long)(b.t1 - b.t0 - off), left); }
     QDQ_DEV void next(const KernelArgs &a) {
-        const int n = len();
-        pos += n;
-        left -= n;
-        if (left == 0) return;
-        off = 0;
-        if (++head < a.g.kv_heads) return;
-        head = 0;
-        if (++block >= seq_blocks(a.g, count)) {
-            block = 0;
-            do {
-                if (++seq >= a.n_seqs) {  // (only if the batch changed under the kernel)
-                    left = 0;
-                    return;
-                }
-                load_seq(a);
-            } while (count == 0);
+        item += item_units(b);
+        pos = item;
+        n = 0;
+        if (item >= end) return;
+        if (++head == a.g.kv_heads) {
+            head = 0;
+            if (++block >= seq_blocks(a.g, count)) {
+                block = 0;
+                do {
+                    if (++seq >= a.n_seqs) return;  // (only if the batch changed under the kernel)
+                    load_seq(a);
+                } while (count == 0);
+            }
+            b = block_of(a.g, count, kv, block);
         }
-        b = block_of(a.g, count, kv, block);
+        int last;
+        piece_of(b, item, pos, end, off, last);
+        n = last - off;  // 0 at the end of the range, where only the item's first units are left
     }
 };
 
@@ -154,7 +157,7 @@ template <int HD>
 QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
     using L = Shape<HD>;
     int *cnt = reinterpret_cast<int *>(smem + L::kRing), *kvs = cnt + kMaxSeqs;
-    long long *pre = reinterpret_cast<long long *>(smem + L::kRing + 8 * kMaxSeqs);  // [n_seqs + 1]
+    long long *pre = reinterpret_cast<long long *>(smem + L::kRing + 8 * kMaxSeqs);  // [n_seqs]
     constexpr int kAlone = 8;  // blocks that one thread sums; longer sequences are summed by a warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int s = tid; s < a.n_seqs; s += kThreads) {
@@ -166,8 +169,7 @@ QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
         long long sum = 0;
         if (nb <= kAlone)
             for (int b = 0; b < nb; ++b) {
-                const AttendBlock k = block_of(a.g, count, kv, b);
-                sum += k.t1 - k.t0;
+                sum += item_units(block_of(a.g, count, kv, b));
             }
         pre[s] = sum * a.g.kv_heads;
     }
@@ -177,8 +179,7 @@ QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
         if (nb <= kAlone) continue;
         long long sum = 0;
         for (int b = lane; b < nb; b += 32) {
-            const AttendBlock k = block_of(a.g, cnt[s], kvs[s], b);
-            sum += k.t1 - k.t0;
+            sum += item_units(block_of(a.g, cnt[s], kvs[s], b));
         }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (lane == 0) pre[s] = sum * a.g.kv_heads;
@@ -202,10 +203,9 @@ QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
         if (lane == 0) {
             start->live = live;
             start->ctas = ctas;
+            start->total = total;
             start->pos = x;
             start->end = live ? range_start(total, ctas, blockIdx.x + 1) : 0;
-            // (the total is kept for the joins)
-            pre[a.n_seqs] = total;
         }
         // the lane whose run of sequences holds x walks it
         const unsigned owner = __ballot_sync(0xFFFFFFFFu, live && mine > 0 && excl <= x && x < incl);
@@ -224,10 +224,7 @@ QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
             const int nb = seq_blocks(a.g, cnt[s]);
             for (int b0 = 0; b0 < nb; b0 += 32) {
                 int n = 0;
-                if (b0 + lane < nb) {
-                    const AttendBlock k = block_of(a.g, cnt[s], kvs[s], b0 + lane);
-                    n = k.t1 - k.t0;
-                }
+                if (b0 + lane < nb) n = item_units(block_of(a.g, cnt[s], kvs[s], b0 + lane));
                 long long run = (long long)n * a.g.kv_heads;
                 const long long own = run;
                 for (int o = 1; o < 32; o <<= 1) {
@@ -242,7 +239,7 @@ QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
                         start->seq = s;
                         start->block = b0 + l;
                         start->head = r / n;
-                        start->off = r % n;
+                        start->item = x - r % n;
                     }
                     break;
                 }
@@ -283,8 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     find_start<HD>(a, smem, start);
     if (!start->live) return;
-    const long long total = *reinterpret_cast<long long *>(smem + L::kRing + 8 * kMaxSeqs + 8 * a.n_seqs);
     const Start s0 = *start;
+    const long long total = s0.total;
     __syncthreads();
     fence_async_smem();  // the ring's memory goes over to the copies
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kStart);
@@ -300,8 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- copies ---------------------------------------------------------------------
         const uint32_t q_rows = (uint32_t)(tq * a.g.group), run_bytes = (L::kGroup8 << run_shift) >> 3;
         uint32_t seq_no = 0, items = 0;
-        for (Walk w(a, s0); w.left > 0; w.next(a), ++items) {
-            const int n = w.len(), t0 = w.t_beg(), tiles = w.b.i1 - w.b.i0 > tq ? 2 : 1;
+        for (Walk w(a, s0); w.more(); w.next(a), ++items) {
+            const int n = w.n, t0 = w.t_beg(), tiles = w.b.i1 - w.b.i0 > tq ? 2 : 1;
             mbar_wait(bar(kBarQEmpty), (items & 1) ^ 1, status);
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(kBarQFull), tiles * L::kHalves * q_rows * 128u);
@@ -357,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O_i (+)= P_i V with V in slot number s
         auto pv = [&](int i, uint32_t s, bool first) {
             const uint32_t vd = v_lo + (s % L::kSlots) * (L::kSlot >> 4);
-            mbar_wait(bar(kBarP + i), np[i]++ & 1, status);
+            mbar_wait_spin(bar(kBarP + i), np[i]++ & 1, status);
             if (first) mbar_wait(bar(kBarOFree + i), (no[i]++ & 1) ^ 1, status);
             full(s);
             tc_after();
@@ -374,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_lane()) tc_commit(bar(kBarEmpty + s % L::kSlots));
             __syncwarp();
         };
-        for (Walk w(a, s0); w.left > 0; w.next(a), ++items) {
-            const int n = w.len(), t0 = w.t_beg();
+        for (Walk w(a, s0); w.more(); w.next(a), ++items) {
+            const int n = w.n, t0 = w.t_beg();
             const uint32_t base = seq_no;
             seq_no += 2 * n;
             mbar_wait(bar(kBarQFull), items & 1, status);
@@ -430,8 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t c2 = pack2(c, c);
         float2 *scratch = reinterpret_cast<float2 *>(smem + L::kScratch) + i * 128;
         uint32_t seq_no = 0, ns = 0, npv = 0;
-        for (Walk w(a, s0); w.left > 0; w.next(a)) {
-            const int n = w.len(), t0 = w.t_beg();
+        for (Walk w(a, s0); w.more(); w.next(a)) {
+            const int n = w.n, t0 = w.t_beg();
             const uint32_t base = seq_no;
             seq_no += 2 * n;
             const bool alt = block_alternates(a.g, w.b);
@@ -466,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int y = 0; y < 32; ++y) s[y] = (keep >> y) & 1 ? s[y] : -INFINITY;
                 };
-                mbar_wait(bar(kBarS + i), ns++ & 1, status);
+                mbar_wait_spin(bar(kBarS + i), ns++ & 1, status);
                 tc_after();
                 // The row's maximum, 64 columns at a time: the last 64 are read again when
                 // their turn comes, so that a thread holds 64 scores and not 128.
@@ -495,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
                     m = mn;
                     l *= f;
-                    mbar_wait(bar(kBarPv + i), (npv - 1) & 1, status);
+                    mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
                     tc_after();
                     const uint64_t f2 = pack2(f, f);
 #pragma unroll
@@ -562,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = j1 > j0;
             const float mc = m == -INFINITY ? -INFINITY : m * c;
             if (any) {
-                mbar_wait(bar(kBarPv + i), (npv - 1) & 1, status);
+                mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
                 tc_after();
             }
             auto o_read = [&] {  // the last read of O: the next piece may overwrite it
@@ -570,9 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (any && lane == 0) mbar_arrive(bar(kBarOFree + i));
             };
-            const long long item = w.pos - w.off;
-            const int c_first = range_owner(total, s0.ctas, item);
-            const int c_last = range_owner(total, s0.ctas, item + (w.b.t1 - w.b.t0) - 1);
+            const int c_first = range_owner(total, s0.ctas, w.item + kItemUnits);
+            const int c_last = range_owner(total, s0.ctas, w.item + item_units(w.b) - 1);
             // outputs of row `row` of the set's tile: token and head
             auto out_at = [&](int row) {
                 const int64_t t = w.first + a0 + row / a.g.group, h = (int64_t)w.head * a.g.group + row % a.g.group;

@@ -5,10 +5,12 @@
 // kTileM rows holds kTileM / g whole tokens (row = token * g + head), a block two tiles.
 // Items. (sequence, block, kv head), in that order; an item's length is the number of
 // key tiles (kTileN positions) from the first one that any of its tokens attends to up
-// to the last. The items' key tiles, laid end to end, are dealt to the CTAs in equal
-// contiguous ranges, so whatever the lengths, every CTA has the same number of key
-// tiles; an item that crosses CTAs is joined from its parts afterwards. A CTA's range
-// can cut at most the item it starts in and the item it ends in.
+// to the last.
+// Work. An item is kItemUnits units (its queries, its output), then one for each key
+// tile. The items' units, laid end to end, are dealt to the CTAs in equal contiguous
+// ranges, so whatever the lengths, every CTA has the same work; a key tile belongs to the
+// CTA that holds its unit, and an item whose tiles belong to several is joined from its
+// parts. A CTA's range can cut at most the item it starts in and the item it ends in.
 #pragma once
 #include <cstdint>
 
@@ -21,6 +23,7 @@
 namespace qdq {
 
 constexpr int kTileM = 128, kTileN = 128;
+constexpr int kItemUnits = 4;
 
 struct AttendGeometry {
     int group;        // query heads per kv head
@@ -78,8 +81,16 @@ QDQ_PLAN_FN bool block_alternates(const AttendGeometry &g, const AttendBlock &b)
     return b.i1 - b.i0 <= tile_tokens(g) && b.t1 - b.t0 >= 2;
 }
 
-// CTA c of n takes key tiles range_start(c) .. range_start(c + 1) - 1 of `total`.
+// CTA c of n takes units range_start(c) .. range_start(c + 1) - 1 of `total`.
 QDQ_PLAN_FN int64_t range_start(int64_t total, int n, int c) { return total * c / n; }
 QDQ_PLAN_FN int range_owner(int64_t total, int n, int64_t x) { return (int)(((x + 1) * n - 1) / total); }
+QDQ_PLAN_FN int item_units(const AttendBlock &b) { return kItemUnits + b.t1 - b.t0; }
+// Of an item whose units begin at `item`, the key tiles [first, last) of the range [x, end).
+QDQ_PLAN_FN void piece_of(const AttendBlock &b, int64_t item, int64_t x, int64_t end, int &first, int &last) {
+    const int64_t tile0 = item + kItemUnits, n = b.t1 - b.t0;
+    const int64_t f = x > tile0 ? x - tile0 : 0, l = end - tile0 < n ? end - tile0 : n;
+    first = (int)f;
+    last = l > f ? (int)l : (int)f;
+}
 
 }  // namespace qdq

@@ -65,7 +65,7 @@ static int one(std::mt19937 &rng) {
             for (int h = 0; h < g.kv_heads; ++h) {
                 items.push_back({s, b, h, k});
                 at.push_back(total);
-                total += k.t1 - k.t0;
+                total += item_units(k);
             }
         }
         CHECK(covered == count[s]);
@@ -73,33 +73,42 @@ static int one(std::mt19937 &rng) {
     if (total == 0) return 0;
     const int ctas = (int)std::min<int64_t>(ctas_most, total);
     std::map<std::pair<int, int>, int> slots;  // (cta, slot) -> item
-    std::vector<int64_t> dealt(items.size());
+    std::vector<std::vector<int>> owner(items.size());
+    for (size_t i = 0; i < items.size(); ++i) owner[i].assign(items[i].k.t1 - items[i].k.t0, -1);
     for (int c = 0; c < ctas; ++c) {
         const int64_t a = range_start(total, ctas, c), b = range_start(total, ctas, c + 1);
         CHECK(b > a && b - a >= total / ctas && b - a <= total / ctas + 1);
         int cut = 0;
         for (size_t i = 0; i < items.size(); ++i) {
-            const int64_t len = items[i].k.t1 - items[i].k.t0, x = std::max(a, at[i]), y = std::min(b, at[i] + len);
-            if (x >= y) continue;
-            dealt[i] += y - x;
-            const int first = range_owner(total, ctas, at[i]), last = range_owner(total, ctas, at[i] + len - 1);
-            CHECK(first <= c && c <= last);
-            if (first == last) continue;
-            CHECK(++cut <= 2);
-            const auto key = std::make_pair(c, c == first ? 1 : 0);
+            if (at[i] >= b || at[i] + item_units(items[i].k) <= a) continue;
+            int first, last;
+            piece_of(items[i].k, at[i], std::max(a, at[i]), b, first, last);
+            CHECK(first >= 0 && last >= first && last <= (int)owner[i].size());
+            for (int t = first; t < last; ++t) {
+                CHECK(owner[i][t] == -1);
+                owner[i][t] = c;
+                CHECK(range_owner(total, ctas, at[i] + kItemUnits + t) == c);
+            }
+            const int from = range_owner(total, ctas, at[i] + kItemUnits);
+            const int to = range_owner(total, ctas, at[i] + item_units(items[i].k) - 1);
+            if (last == first || from == to) continue;
+            CHECK(from <= c && c <= to && ++cut <= 2);
+            const auto key = std::make_pair(c, c == from ? 1 : 0);
             CHECK(!slots.count(key));
             slots[key] = (int)i;
         }
     }
     CHECK(range_start(total, ctas, 0) == 0 && range_start(total, ctas, ctas) == total);
-    for (size_t i = 0; i < items.size(); ++i) CHECK(dealt[i] == items[i].k.t1 - items[i].k.t0);
-    // a counter per (first CTA) serves one cut item at most
+    // every tile is dealt; every CTA from an item's first to its last holds a part of it, in
+    // the slot that the others look in; a counter per first CTA serves one cut item
     std::map<int, int> counters;
     for (size_t i = 0; i < items.size(); ++i) {
-        const int64_t len = items[i].k.t1 - items[i].k.t0;
-        const int first = range_owner(total, ctas, at[i]), last = range_owner(total, ctas, at[i] + len - 1);
-        if (first != last) CHECK(!counters.count(first) && (counters[first] = (int)i, true));
-        for (int c = first; c <= last && first != last; ++c) CHECK(slots.at({c, c == first ? 1 : 0}) == (int)i);
+        for (int t : owner[i]) CHECK(t >= 0);
+        const int from = owner[i].front(), to = owner[i].back();
+        if (from == to) continue;
+        CHECK(!counters.count(from));
+        counters[from] = (int)i;
+        for (int c = from; c <= to; ++c) CHECK(slots.at({c, c == from ? 1 : 0}) == (int)i);
     }
     return 0;
 }
