@@ -14,7 +14,7 @@
 // * Chunks: the two sets are two tiles of rows against the same keys, so that one
 //   group's exponentials run while the other's products do.
 // * Few rows (one tile, as in single-token steps): the two sets take alternate key tiles
-//   of the same rows, and their two states are joined at the end.
+//   of the same rows; the first joins both states, which lie in tensor memory.
 // Keys and values arrive page by page through one ring of slots (4-D tensor copies with
 // the 128-byte swizzle: a slot is groups of 8 positions, each group head_dim / 64 blocks
 // of 8 x 128 bytes, which is the operand layout for K (K-major) and for V (N-major)).
@@ -32,6 +32,7 @@
 #include <cuda.h>
 #include <mutex>
 #include <new>
+#include <type_traits>
 
 #include "qdq_attend_plan.h"
 #include "qdq_internal.h"
@@ -45,7 +46,8 @@ namespace qdq {
 struct AttendState {
     CUtensorMap k_map, v_map;
     char *mem = nullptr;
-    float *part_o = nullptr, *part_m = nullptr, *part_l = nullptr;
+    float *part_o = nullptr;
+    float2 *part_ml = nullptr;
     unsigned *counters = nullptr;
     int ctas = 0;
 };
@@ -70,7 +72,8 @@ struct KernelArgs {
     int n_heads;
     bool out_f32;
     AttendGeometry g;
-    float *part_o, *part_m, *part_l;
+    float *part_o;
+    float2 *part_ml;
     unsigned *counters;
 };
 
@@ -100,11 +103,14 @@ struct Start {
 struct Walk {
     long long item, pos, end;  // units: where the item begins, the rest of the range
     int seq, block, head, off, n;  // the piece: n key tiles from the item's off-th on
-    int first, count, kv;
+    int first, count, kv, blocks;
+    const int32_t *pages;  // the sequence's page table
     AttendBlock b;
     QDQ_DEV void load_seq(const KernelArgs &a) {
         seq_tokens(a.q_start, seq, a.n_tokens, first, count);
         kv = max(a.kv_len[seq], 0);
+        blocks = seq_blocks(a.g, count);
+        pages = a.page_table + (int64_t)seq * a.max_pages;
     }
     QDQ_DEV Walk(const KernelArgs &a, const Start &s)
         : item(s.item), pos(s.pos), end(s.end), seq(s.seq), block(s.block), head(s.head) {
@@ -117,6 +123,7 @@ struct Walk {
     }
     QDQ_DEV bool more() const { return n > 0; }
     QDQ_DEV int t_beg() const { return b.t0 + off; }
+    QDQ_DEV bool whole() const { return n == b.t1 - b.t0; }
     QDQ_DEV void next(const KernelArgs &a) {
         item += item_units(b);
         pos = item;
@@ -124,7 +131,7 @@ struct Walk {
         if (item >= end) return;
         if (++head == a.g.kv_heads) {
             head = 0;
-            if (++block >= seq_blocks(a.g, count)) {
+            if (++block >= blocks) {
                 block = 0;
                 do {
                     if (++seq >= a.n_seqs) return;  // (only if the batch changed under the kernel)
@@ -139,18 +146,23 @@ struct Walk {
     }
 };
 
-// The pages of key tile j that hold positions of [lo, hi): lane l's page number (the
-// tile's l-th run of min(page, 128) positions), or -1 where it has none or is absent.
-QDQ_DEV int tile_page(const KernelArgs &a, int seq, int j, int run_shift, int lo, int hi) {
+// The pages of key tile j that hold positions of [lo, hi): lane l's entry of the page
+// table (for the tile's l-th run of min(page, 128) positions), or -1 where there is none.
+// The entry is checked where it is used, a tile later, so that nothing waits for the load.
+QDQ_DEV int tile_page(const KernelArgs &a, const Walk &w, int j, int run_shift) {
     const int lane = threadIdx.x & 31;
-    const int64_t p = (int64_t)j * kTileN + ((int64_t)lane << run_shift);
-    if (lane >= (kTileN >> run_shift) || p >= hi || p + (1 << run_shift) <= lo) return -1;
-    const int at = (int)(p >> a.page_shift);  // below max_pages: hi is within the table
-    const int page = a.page_table[(int64_t)seq * a.max_pages + at];
-    return page >= 0 && page < a.n_pages ? page : -1;
+    const int64_t p = (int64_t)j * kTileN + (lane << run_shift);
+    int page = -1;
+    if (lane < (kTileN >> run_shift) && p < w.b.hi && p + (1 << run_shift) > w.b.lo)
+        page = w.pages[(int)p >> a.page_shift];  // (inside the table: hi is)
+    return page;
 }
 
-QDQ_DEV float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+QDQ_DEV float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // Where the CTA's range starts: sums of key tiles per sequence, a scan, and a search.
 template <int HD>
@@ -291,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
 
-    const int run_shift = min(a.page_shift, 7), tq = tile_tokens(a.g);
+    const int run_shift = min(a.page_shift, 7), tq = a.g.tokens;
 
     if (warp == kWarpLoad) {
         // ---- copies ---------------------------------------------------------------------
@@ -307,10 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
                                     w.first + w.b.i0 + i * tq, bar(kBarQFull));
             }
-            int page = tile_page(a, w.seq, t0, run_shift, w.b.lo, w.b.hi);
+            int page = tile_page(a, w, t0, run_shift);
             for (int j = 0; j < n; ++j) {
-                const int here = page;
-                if (j + 1 < n) page = tile_page(a, w.seq, t0 + j + 1, run_shift, w.b.lo, w.b.hi);
+                const int here = (unsigned)page < (unsigned)a.n_pages ? page : -1;
+                if (j + 1 < n) page = tile_page(a, w, t0 + j + 1, run_shift);
                 const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0);
                 const uint32_t bytes = __popc(have) * run_bytes;
                 // the lane's run of positions: its first group of 8 rows in the pools
@@ -334,14 +346,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (items) mbar_wait(bar(kBarQFull), (items - 1) & 1, status);
     } else if (warp == kWarpMma) {
         // ---- matrix instructions ----------------------------------------------------------
+        // Everything that an instruction's operands depend on is kept known to be the same in
+        // every lane (values out of memory go through a shuffle), or each operand costs moves.
         constexpr uint32_t q_hi = sdesc_hi(1024), kv_hi = sdesc_hi(L::kGroup8);
-        uint32_t seq_no = 0, items = 0, np[2] = {0, 0}, no[2] = {0, 0};
+        uint32_t items = 0, np = 0, no = 0;  // np, no: bit i is the phase of set i's barrier
         const uint32_t q_lo = sdesc_lo(16) | ((sb + L::kQ) >> 4);
         const uint32_t k_lo = sdesc_lo(16) | ((sb + L::kRing) >> 4), v_lo = sdesc_lo(1024) | ((sb + L::kRing) >> 4);
-        auto full = [&](uint32_t s) { mbar_wait(bar(kBarFull + s % L::kSlots), (s / L::kSlots) & 1, status); };
-        // S_i = Q K^T with K in slot number s, rows of tile qi
-        auto qk = [&](int i, int qi, uint32_t s) {
-            const uint32_t kd = k_lo + (s % L::kSlots) * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
+        auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+        // A place in the ring; keys and values alternate, so the next of a kind is two on.
+        struct Place {
+            int slot;
+            uint32_t phase;
+            QDQ_DEV void step(int by) {
+                slot += by;
+                if (slot >= L::kSlots) slot -= L::kSlots, phase ^= 1;
+            }
+        };
+        auto full = [&](const Place &p) { mbar_wait(bar(kBarFull + p.slot), p.phase, status); };
+        auto release = [&](const Place &p) {
+            if (elect_lane()) tc_commit(bar(kBarEmpty + p.slot));
+            __syncwarp();
+        };
+        // S_i = Q K^T with rows of tile qi
+        auto qk = [&](int i, int qi, const Place &p) {
+            const uint32_t kd = k_lo + (uint32_t)p.slot * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
             if (elect_lane()) {
 #pragma unroll
                 for (int k = 0; k < HD / 16; ++k)
@@ -351,12 +379,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        // O_i (+)= P_i V with V in slot number s
-        auto pv = [&](int i, uint32_t s, bool first) {
-            const uint32_t vd = v_lo + (s % L::kSlots) * (L::kSlot >> 4);
-            mbar_wait_spin(bar(kBarP + i), np[i]++ & 1, status);
-            if (first) mbar_wait(bar(kBarOFree + i), (no[i]++ & 1) ^ 1, status);
-            full(s);
+        // O_i (+)= P_i V
+        auto pv = [&](int i, const Place &p, bool first) {
+            const uint32_t vd = v_lo + (uint32_t)p.slot * (L::kSlot >> 4);
+            mbar_wait_spin(bar(kBarP + i), (np >> i) & 1, status);
+            np ^= 1u << i;
+            if (first) {
+                mbar_wait(bar(kBarOFree + i), ((no >> i) & 1) ^ 1, status);
+                no ^= 1u << i;
+            }
             tc_after();
             if (elect_lane()) {
 #pragma unroll
@@ -367,49 +398,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        auto release = [&](uint32_t s) {
-            if (elect_lane()) tc_commit(bar(kBarEmpty + s % L::kSlots));
-            __syncwarp();
-        };
+        Place kp = {0, 0}, vp = {1, 0};
         for (Walk w(a, s0); w.more(); w.next(a), ++items) {
-            const int n = w.n, t0 = w.t_beg();
-            const uint32_t base = seq_no;
-            seq_no += 2 * n;
+            const int n = uniform(w.n), t0 = w.t_beg();
             mbar_wait(bar(kBarQFull), items & 1, status);
-            if (block_alternates(a.g, w.b)) {
-                for (int k = 0; k < 2 && k < n; ++k) {
-                    full(base + 2 * k);
-                    qk(k, 0, base + 2 * k);
-                    release(base + 2 * k);
+            if (uniform(block_alternates(a.g, w.b))) {
+                for (int k = 0; k < 2 && k < n; ++k, kp.step(2)) {
+                    full(kp);
+                    qk(k, 0, kp);
+                    release(kp);
                 }
-                for (int k = 0; k < n; ++k) {
-                    pv(k & 1, base + 2 * k + 1, k < 2);
-                    release(base + 2 * k + 1);
+                for (int k = 0; k < n; ++k, vp.step(2)) {
+                    full(vp);
+                    pv(k & 1, vp, k < 2);
+                    release(vp);
                     if (k + 2 < n) {
-                        full(base + 2 * k + 4);
-                        qk(k & 1, 0, base + 2 * k + 4);
-                        release(base + 2 * k + 4);
+                        full(kp);
+                        qk(k & 1, 0, kp);
+                        release(kp);
+                        kp.step(2);
                     }
                 }
             } else {
-                bool begun[2] = {false, false};
-                auto on = [&](int i, int k) { return k < n && t0 + k >= w.b.tile_t0[i] && t0 + k < w.b.tile_t1[i]; };
-                full(base);
-                for (int i = 0; i < 2; ++i)
-                    if (on(i, 0)) qk(i, i, base);
-                release(base);
-                for (int k = 0; k < n; ++k) {
-                    full(base + 2 * k + 1);
-                    for (int i = 0; i < 2; ++i) {
-                        if (on(i, k)) {
-                            pv(i, base + 2 * k + 1, !begun[i]);
-                            begun[i] = true;
-                        }
-                        if (i == 0 && k + 1 < n) full(base + 2 * k + 2);
-                        if (on(i, k + 1)) qk(i, i, base + 2 * k + 2);
+                // the sets' key tiles, counted from the piece's first
+                const int b0 = uniform(w.b.tile_t0[0] - t0), e0 = uniform(min(w.b.tile_t1[0] - t0, n));
+                const int b1 = uniform(w.b.tile_t0[1] - t0), e1 = uniform(min(w.b.tile_t1[1] - t0, n));
+                bool begun0 = false, begun1 = false;
+                full(kp);
+                if (b0 <= 0 && 0 < e0) qk(0, 0, kp);
+                if (b1 <= 0 && 0 < e1) qk(1, 1, kp);
+                release(kp);
+                kp.step(2);
+                for (int k = 0; k < n; ++k, vp.step(2)) {
+                    const bool more = k + 1 < n;
+                    full(vp);
+                    if (b0 <= k && k < e0) {
+                        pv(0, vp, !begun0);
+                        begun0 = true;
                     }
-                    release(base + 2 * k + 1);
-                    if (k + 1 < n) release(base + 2 * k + 2);
+                    if (more) full(kp);
+                    if (b0 <= k + 1 && k + 1 < e0) qk(0, 0, kp);
+                    if (b1 <= k && k < e1) {
+                        pv(1, vp, !begun1);
+                        begun1 = true;
+                    }
+                    release(vp);
+                    if (b1 <= k + 1 && k + 1 < e1) qk(1, 1, kp);
+                    if (more) {
+                        release(kp);
+                        kp.step(2);
+                    }
                 }
             }
             if (elect_lane()) tc_commit(bar(kBarQEmpty));
@@ -421,34 +459,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---- softmax, output ----------------------------------------------------------------
         const int i = warp >> 2, r = threadIdx.x & 127;  // set; row = tensor-memory lane
-        const uint32_t t_s = tmem + ((uint32_t)(warp & 3) << 21) + 128u * i;
-        const uint32_t t_o = tmem + ((uint32_t)(warp & 3) << 21) + kColO + (uint32_t)HD * i;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t t_s = tmem + lanes + 128u * i, t_o = tmem + lanes + kColO + (uint32_t)HD * i;
         const float c = a.scale_log2;
         const uint64_t c2 = pack2(c, c);
         float2 *scratch = reinterpret_cast<float2 *>(smem + L::kScratch) + i * 128;
+        const int r_token = r / a.g.group, r_head = r - r_token * a.g.group;
         uint32_t seq_no = 0, ns = 0, npv = 0;
+        bool lent = false;  // the second set's scratch holds a state that the first may not have read
         for (Walk w(a, s0); w.more(); w.next(a)) {
             const int n = w.n, t0 = w.t_beg();
             const uint32_t base = seq_no;
             seq_no += 2 * n;
             const bool alt = block_alternates(a.g, w.b);
             // this set's rows and key tiles of the piece
-            const int qi = alt ? 0 : i, a0 = w.b.i0 + qi * tq, rows = min(tq, w.b.i1 - a0) * a.g.group;
+            const int qi = alt ? 0 : i, a0 = w.b.i0 + qi * tq, tokens = min(tq, w.b.i1 - a0), rows = tokens * a.g.group;
             if (rows <= 0) continue;
+            const bool idle = (warp & 3) * 32 >= rows;  // no row of the warp's lanes is one
             const int step = alt ? 2 : 1;
-            const int j0 = alt ? t0 + i : max(t0, w.b.tile_t0[qi]);
-            const int j1 = alt ? t0 + n : min(t0 + n, w.b.tile_t1[qi]);
-            const int token = a0 + min(r, rows - 1) / a.g.group;
+            const int j0 = alt ? t0 + i : max(t0, qi ? w.b.tile_t0[1] : w.b.tile_t0[0]);
+            const int j1 = alt ? t0 + n : min(t0 + n, qi ? w.b.tile_t1[1] : w.b.tile_t1[0]);
+            const int p_first = w.kv - w.count + a0;
             int lo, hi, lo_last, hi_first, x;
-            span(a.g, w.kv - w.count + token, 1, lo, hi);
-            span(a.g, w.kv - w.count + a0, 1, x, hi_first);
-            span(a.g, w.kv - w.count + a0 + rows / a.g.group - 1, 1, lo_last, x);
+            span(a.g, p_first + min(r_token, tokens - 1), 1, lo, hi);
+            span(a.g, p_first, 1, x, hi_first);
+            span(a.g, p_first + tokens - 1, 1, lo_last, x);
 
             float m = -INFINITY, l = 0.0f;
-            int page = j0 < j1 ? tile_page(a, w.seq, j0, run_shift, w.b.lo, w.b.hi) : -1;
+            int page = j0 < j1 ? tile_page(a, w, j0, run_shift) : -1;
             for (int j = j0; j < j1; j += step) {
-                const unsigned have = __ballot_sync(0xFFFFFFFFu, page >= 0);
-                if (j + step < j1) page = tile_page(a, w.seq, j + step, run_shift, w.b.lo, w.b.hi);
+                const unsigned have = __ballot_sync(0xFFFFFFFFu, (unsigned)page < (unsigned)a.n_pages);
+                if (j + step < j1) page = tile_page(a, w, j + step, run_shift);
                 const int p0 = j * kTileN;
                 const unsigned all = (1u << (kTileN >> run_shift)) - 1;
                 const bool dirty = have != all || p0 < w.b.lo || p0 + kTileN > w.b.hi;
@@ -465,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 mbar_wait_spin(bar(kBarS + i), ns++ & 1, status);
                 tc_after();
+                if (!idle) {
                 // The row's maximum, 64 columns at a time: the last 64 are read again when
                 // their turn comes, so that a thread holds 64 scores and not 128.
                 float s0[32], s1[32], mx[4];
@@ -536,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_st32(t_s + 32, u);
                 const uint64_t t = fadd2(sum[0], sum[1]);
                 l += lo_of(t) + hi_of(t);
+                }
                 if (dirty) {
                     // zero the rows of V that hold no position of the block (row r of the slot)
                     const uint32_t vs = base + 2 * (j - t0) + 1;
@@ -557,67 +600,102 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---- the piece's end ------------------------------------------------------------
             const bool any = j1 > j0;
-            const float mc = m == -INFINITY ? -INFINITY : m * c;
+            float mc = m == -INFINITY ? -INFINITY : m * c, f0 = 1.0f, f1 = 0.0f;
             if (any) {
                 mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
                 tc_after();
             }
-            auto o_read = [&] {  // the last read of O: the next piece may overwrite it
+            const bool both = alt && n >= 2;  // two states of the same rows
+            if (alt && i == 1) {
+                if (lent) named_bar_sync(4, 256);
+                lent = both;
+                if (!both) continue;
+                scratch[r] = make_float2(mc, l);
+                tc_before();
+                named_bar_arrive(3, 256);
+                continue;
+            }
+            if (both) {
+                named_bar_sync(3, 256);
+                tc_after();
+                const float2 o = scratch[128 + r];
+                named_bar_arrive(4, 256);
+                const float M = fmaxf(mc, o.x);
+                f0 = l > 0.0f ? ex2(mc - M) : 0.0f;
+                f1 = o.y > 0.0f ? ex2(o.x - M) : 0.0f;
+                l = l * f0 + o.y * f1;
+                mc = M;
+            }
+            // 32 columns of the row's accumulator (both sets' where they share the rows)
+            auto read = [&](int k, float *o) {
+                if (!any) {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = 0.0f;
+                    return;
+                }
+                tc_ld32(t_o + 32 * k, o);
+                tc_wait_ld<32>(o);
+                if (both) {
+                    float e[32];
+                    tc_ld32(t_o + HD + 32 * k, e);
+                    tc_wait_ld<32>(e);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = fmaf(e[y], f1, o[y] * f0);
+                }
+            };
+            auto read_done = [&] {  // the next piece may overwrite the accumulators
                 tc_before();
                 __syncwarp();
-                if (any && lane == 0) mbar_arrive(bar(kBarOFree + i));
+                if (any && lane == 0) {
+                    mbar_arrive(bar(kBarOFree + i));
+                    if (both) mbar_arrive(bar(kBarOFree + 1));
+                }
             };
-            const int c_first = range_owner(total, s0.ctas, w.item + kItemUnits);
-            const int c_last = range_owner(total, s0.ctas, w.item + item_units(w.b) - 1);
-            // outputs of row `row` of the set's tile: token and head
-            auto out_at = [&](int row) {
-                const int64_t t = w.first + a0 + row / a.g.group, h = (int64_t)w.head * a.g.group + row % a.g.group;
-                return t * a.out_stride + h * HD;
-            };
-            auto lse_at = [&](int row) {
-                return (int64_t)(w.first + a0 + row / a.g.group) * a.n_heads + w.head * a.g.group + row % a.g.group;
-            };
+            const int64_t first_token = w.first + a0, first_head = (int64_t)w.head * a.g.group;
             auto put4 = [&](int64_t at, float x, float y, float z, float v) {
                 if (a.out_f32) {
                     *reinterpret_cast<float4 *>((float *)a.out + at) = make_float4(x, y, z, v);
                 } else {
-                    *reinterpret_cast<uint2 *>((uint16_t *)a.out + at) =
-                        BF16 ? make_uint2(Float16<__nv_bfloat16>::pack(x, y), Float16<__nv_bfloat16>::pack(z, v))
-                               : make_uint2(Float16<__half>::pack(x, y), Float16<__half>::pack(z, v));
+                    using F = Float16<typename std::conditional<BF16, __nv_bfloat16, __half>::type>;
+                    *reinterpret_cast<uint2 *>((uint16_t *)a.out + at) = make_uint2(F::pack(x, y), F::pack(z, v));
                 }
             };
-            if (c_first == c_last && !alt) {
+            const float ln2 = 0.6931471805599453f;
+            if (w.whole()) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-                const int64_t at = out_at(min(r, rows - 1));
-#pragma unroll
-                for (int k = 0; k < HD / 32; ++k) {
-                    float o[32];
-                    if (any) {
-                        tc_ld32(t_o + 32 * k, o);
-                        tc_wait_ld<32>(o);
-                    }
-                    if (r < rows) {
-#pragma unroll
-                        for (int y = 0; y < 32; y += 4) {
-                            if (any && l > 0.0f) put4(at + 32 * k + y, o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv);
-                            else put4(at + 32 * k + y, 0.0f, 0.0f, 0.0f, 0.0f);
-                        }
-                    }
-                }
-                o_read();
-                if (a.lse && r < rows) a.lse[lse_at(r)] = l > 0.0f ? (mc + log2f(l)) * 0.6931471805599453f : -INFINITY;
-                continue;
-            }
-            // partial state: O as [column / 4][row][4], so that rows of a warp are contiguous
-            const int part = (blockIdx.x * 2 + ((int)blockIdx.x == c_first ? 1 : 0)) * 2 + i;
-            {
-                float4 *po = reinterpret_cast<float4 *>(a.part_o) + (int64_t)part * (HD / 4) * 128;
-                if (any) {
+                const int64_t token = first_token + r_token, head = first_head + r_head;
+                const int64_t at = token * a.out_stride + head * HD;
+                if (!idle) {
 #pragma unroll
                     for (int k = 0; k < HD / 32; ++k) {
                         float o[32];
-                        tc_ld32(t_o + 32 * k, o);
-                        tc_wait_ld<32>(o);
+                        read(k, o);
+                        if (r < rows) {
+#pragma unroll
+                            for (int y = 0; y < 32; y += 4) {
+                                // (a row with nothing to attend to: its accumulator is 0 x its values' finite rows)
+                                if (l > 0.0f) put4(at + 32 * k + y, o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv);
+                                else put4(at + 32 * k + y, 0.0f, 0.0f, 0.0f, 0.0f);
+                            }
+                        }
+                    }
+                }
+                read_done();
+                if (a.lse && r < rows) a.lse[token * a.n_heads + head] = l > 0.0f ? (mc + log2f(l)) * ln2 : -INFINITY;
+                continue;
+            }
+            // partial state: O as [column / 4][row][4], so that rows of a warp are contiguous
+            const int c_first = range_owner(total, s0.ctas, w.item + kItemUnits);
+            const int c_last = range_owner(total, s0.ctas, w.item + item_units(w.b) - 1);
+            auto part_of = [&](int cta) { return (cta * 2 + (cta == c_first ? 1 : 0)) * 2 + i; };
+            {
+                const int part = part_of(blockIdx.x);
+                float4 *po = reinterpret_cast<float4 *>(a.part_o) + (int64_t)part * (HD / 4) * 128;
+                if (!idle) {
+#pragma unroll
+                    for (int k = 0; k < HD / 32; ++k) {
+                        float o[32];
+                        read(k, o);
                         if (r < rows) {
 #pragma unroll
                             for (int y = 0; y < 32; y += 4)
@@ -625,77 +703,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                o_read();
-                if (r < rows) {
-                    __stcg(a.part_m + part * 128 + r, mc);
-                    __stcg(a.part_l + part * 128 + r, l);
-                }
+                read_done();
+                if (r < rows) __stcg(a.part_ml + part * 128 + r, make_float2(mc, l));
             }
             // the last of the item's parts joins them all, in order
-            const int parts = (c_last - c_first + 1) * (alt ? 2 : 1);
-            int me = r, threads = 128;
-            if (c_first == c_last) {
-                // both parts are this CTA's: its two groups meet and join half each
-                __threadfence_block();
-                named_bar_sync(3, 256);
-                me = threadIdx.x;
-                threads = 256;
-            } else {
-                __threadfence();
-                named_bar_sync(1 + i, 128);
-                if (r == 0) {
-                    unsigned *ctr = a.counters + 2 * c_first + (alt ? 0 : i);
-                    const unsigned before = atomicAdd(ctr, 1u);
-                    const bool last = before == (unsigned)parts - 1;
-                    if (last) *ctr = 0;
-                    __threadfence();
-                    scratch[0] = make_float2(last ? 1.0f : 0.0f, 0.0f);
-                }
-                named_bar_sync(1 + i, 128);
-                const bool last = scratch[0].x != 0.0f;
-                named_bar_sync(1 + i, 128);
-                if (!last) continue;
-                __threadfence();
+            if (lent) {
+                named_bar_sync(4, 256);
+                lent = false;
             }
-            auto part_of = [&](int k) {
-                const int cta = c_first + (alt ? k >> 1 : k);
-                return (cta * 2 + (cta == c_first ? 1 : 0)) * 2 + (alt ? k & 1 : i);
-            };
-            if (r < rows) {
-                float M = -INFINITY, S = 0.0f;
-#pragma unroll 4
-                for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(a.part_m + part_of(k) * 128 + r));
-#pragma unroll 4
-                for (int k = 0; k < parts; ++k) {
-                    const float lk = __ldcg(a.part_l + part_of(k) * 128 + r), mk = __ldcg(a.part_m + part_of(k) * 128 + r);
-                    if (lk > 0.0f) S += lk * ex2(mk - M);
-                }
-                scratch[r] = make_float2(M, S > 0.0f ? 1.0f / S : 0.0f);
-                if (a.lse && (threads == 128 || i == 0)) a.lse[lse_at(r)] = S > 0.0f ? (M + log2f(S)) * 0.6931471805599453f : -INFINITY;
+            __threadfence();
+            named_bar_sync(1 + i, 128);
+            if (r == 0) {
+                unsigned *ctr = a.counters + 2 * c_first + i;
+                const bool last = atomicAdd(ctr, 1u) == (unsigned)(c_last - c_first);
+                if (last) *ctr = 0;
+                __threadfence();
+                scratch[0].x = last ? 1.0f : 0.0f;
             }
             named_bar_sync(1 + i, 128);
-            for (int k = me; k < rows * (HD / 4); k += threads) {
+            const bool last = scratch[0].x != 0.0f;
+            named_bar_sync(1 + i, 128);
+            if (!last) continue;
+            if (r < rows) {
+                float M = -INFINITY, S = 0.0f;
+                for (int cta = c_first; cta <= c_last; cta += 8) {
+                    float2 ml[8];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) ml[y] = cta + y <= c_last ? __ldcg(a.part_ml + part_of(cta + y) * 128 + r) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const float mn = fmaxf(M, ml[y].x);
+                        if (ml[y].y > 0.0f) S = (S > 0.0f ? S * ex2(M - mn) : 0.0f) + ml[y].y * ex2(ml[y].x - mn);
+                        M = mn;
+                    }
+                }
+                scratch[r] = make_float2(M, S > 0.0f ? 1.0f / S : 0.0f);
+                if (a.lse) a.lse[(first_token + r_token) * a.n_heads + first_head + r_head] = S > 0.0f ? (M + log2f(S)) * ln2 : -INFINITY;
+            }
+            named_bar_sync(1 + i, 128);
+            for (int k = r; k < rows * (HD / 4); k += 128) {
                 const int row = k % rows, col = k / rows;
                 const float2 ml = scratch[row];
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-                for (int y = 0; y < parts; ++y) {
-                    const int pt = part_of(y);
-                    const float lk = __ldcg(a.part_l + pt * 128 + row);
-                    if (!(lk > 0.0f)) continue;
-                    const float f = ex2(__ldcg(a.part_m + pt * 128 + row) - ml.x);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + ((int64_t)pt * (HD / 4) + col) * 128 + row);
-                    acc.x = fmaf(f, v.x, acc.x);
-                    acc.y = fmaf(f, v.y, acc.y);
-                    acc.z = fmaf(f, v.z, acc.z);
-                    acc.w = fmaf(f, v.w, acc.w);
+                for (int cta = c_first; cta <= c_last; cta += 4) {
+                    float2 p[4];
+                    float4 v[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int pt = part_of(min(cta + y, c_last));
+                        p[y] = __ldcg(a.part_ml + pt * 128 + row);
+                        v[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + ((int64_t)pt * (HD / 4) + col) * 128 + row);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        if (cta + y > c_last || !(p[y].y > 0.0f)) continue;
+                        const float f = ex2(p[y].x - ml.x);
+                        acc.x = fmaf(f, v[y].x, acc.x);
+                        acc.y = fmaf(f, v[y].y, acc.y);
+                        acc.z = fmaf(f, v[y].z, acc.z);
+                        acc.w = fmaf(f, v[y].w, acc.w);
+                    }
                 }
-                put4(out_at(row) + 4 * col, acc.x * ml.y, acc.y * ml.y, acc.z * ml.y, acc.w * ml.y);
+                const int64_t token = first_token + row / a.g.group, head = first_head + row % a.g.group;
+                put4(token * a.out_stride + head * HD + 4 * col, acc.x * ml.y, acc.y * ml.y, acc.z * ml.y, acc.w * ml.y);
             }
-            // (scratch, and the parts of a join within the CTA, are free again)
-            if (threads == 256) named_bar_sync(3, 256);
-            else named_bar_sync(1 + i, 128);
+            named_bar_sync(1 + i, 128);  // (scratch is free again)
         }
+        if (lent) named_bar_sync(4, 256);
     }
 
     tc_before();
@@ -759,8 +833,8 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
               encode(&st->v_map, p.bf16, 4, p.v_pages, dims, strides, box);
     st->ctas = sm_count;
     // two parts per CTA and set: 128 rows of O, a maximum and a sum; the joins' counters
-    const size_t parts = (size_t)sm_count * 4, n_o = parts * 128 * p.head_dim * 4, n_s = parts * 128 * 4;
-    const size_t bytes = n_o + 2 * n_s + (size_t)sm_count * 2 * sizeof(unsigned);
+    const size_t parts = (size_t)sm_count * 4, n_o = parts * 128 * p.head_dim * 4, n_s = parts * 128 * 8;
+    const size_t bytes = n_o + n_s + (size_t)sm_count * 2 * sizeof(unsigned);
     ok = ok && cudaMalloc((void **)&st->mem, bytes) == cudaSuccess && cudaMemset(st->mem, 0, bytes) == cudaSuccess;
     ok = ok && cudaFuncSetAttribute(kernel_of(p.head_dim, p.bf16), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     smem_of(p.head_dim)) == cudaSuccess;
@@ -770,9 +844,8 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
         return QDQ_ERR_CUDA;
     }
     st->part_o = (float *)st->mem;
-    st->part_m = (float *)(st->mem + n_o);
-    st->part_l = (float *)(st->mem + n_o + n_s);
-    st->counters = (unsigned *)(st->mem + n_o + 2 * n_s);
+    st->part_ml = (float2 *)(st->mem + n_o);
+    st->counters = (unsigned *)(st->mem + n_o + n_s);
     *out = st;
     return QDQ_OK;
 }
@@ -796,10 +869,11 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     k.n_heads = p.n_heads;
     k.out_f32 = a.out_f32;
     k.g.group = p.n_heads / p.n_kv_heads;
+    k.g.tokens = kTileM / k.g.group;
     k.g.kv_heads = p.n_kv_heads;
     k.g.window = a.window < INT32_MAX - a.n_tokens ? a.window : INT32_MAX - a.n_tokens;
     k.g.table_end = a.max_pages * p.page_size;
-    k.part_o = st->part_o, k.part_m = st->part_m, k.part_l = st->part_l, k.counters = st->counters;
+    k.part_o = st->part_o, k.part_ml = st->part_ml, k.counters = st->counters;
     // fp32 accumulators, both operands of the pools' type, M = 128; S: N = 128, both K-major
     // (a negative scale negates Q); O: N = head_dim, V is N-major
     const uint32_t common = (1u << 4) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTileM >> 4) << 24);
@@ -810,7 +884,7 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     const cuuint64_t dims[3] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.n_heads, (cuuint64_t)a.n_tokens};
     const cuuint64_t q_row = a.n_tokens > 1 ? (cuuint64_t)a.q_stride * 2 : (cuuint64_t)p.n_heads * p.head_dim * 2;
     const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, q_row};
-    const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)tile_tokens(k.g)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)k.g.tokens};
     if (!encode(&q_map, p.bf16, 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
     kernel_of(p.head_dim, p.bf16)<<<st->ctas, kThreads, smem_of(p.head_dim), stream>>>(k, q_map, st->k_map, st->v_map);
     return cudaGetLastError() == cudaSuccess ? QDQ_OK : QDQ_ERR_CUDA;

@@ -27,6 +27,7 @@ constexpr int kItemUnits = 4;
 
 struct AttendGeometry {
     int group;        // query heads per kv head
+    int tokens;       // whole tokens of a tile: kTileM / group
     int kv_heads;
     int window;       // 0: none
     int table_end;    // positions that the page table covers
@@ -41,9 +42,8 @@ struct AttendBlock {
 
 QDQ_PLAN_FN int plan_min(int a, int b) { return a < b ? a : b; }
 QDQ_PLAN_FN int plan_max(int a, int b) { return a > b ? a : b; }
-QDQ_PLAN_FN int tile_tokens(const AttendGeometry &g) { return kTileM / g.group; }
 QDQ_PLAN_FN int seq_blocks(const AttendGeometry &g, int count) {
-    const int b = 2 * tile_tokens(g);
+    const int b = 2 * g.tokens;
     return (count + b - 1) / b;
 }
 
@@ -55,7 +55,7 @@ QDQ_PLAN_FN void span(const AttendGeometry &g, int p0, int n, int &lo, int &hi) 
 
 // Block b of a sequence with `count` new tokens and kv positions in all.
 QDQ_PLAN_FN AttendBlock block_of(const AttendGeometry &g, int count, int kv, int b) {
-    const int tq = tile_tokens(g), base = kv - count;
+    const int tq = g.tokens, base = kv - count;
     AttendBlock r;
     r.i0 = b * 2 * tq;
     r.i1 = plan_min(r.i0 + 2 * tq, count);
@@ -78,7 +78,7 @@ QDQ_PLAN_FN AttendBlock block_of(const AttendGeometry &g, int count, int kv, int
 // Item of one tile of rows and two key tiles or more: its two softmax groups take
 // alternate key tiles of the same rows.
 QDQ_PLAN_FN bool block_alternates(const AttendGeometry &g, const AttendBlock &b) {
-    return b.i1 - b.i0 <= tile_tokens(g) && b.t1 - b.t0 >= 2;
+    return b.i1 - b.i0 <= g.tokens && b.t1 - b.t0 >= 2;
 }
 
 // CTA c of n takes units range_start(c) .. range_start(c + 1) - 1 of `total`.

@@ -128,6 +128,11 @@ QDQ_DEV void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int
         : "memory");
 }
 
+// Arrives at a named barrier without waiting there.
+QDQ_DEV void named_bar_arrive(int id, int nthreads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 QDQ_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

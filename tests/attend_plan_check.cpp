@@ -24,6 +24,7 @@ static int one(std::mt19937 &rng) {
     auto pick = [&](int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); };
     AttendGeometry g;
     g.group = pick(1, 32);
+    g.tokens = kTileM / g.group;
     g.kv_heads = pick(1, 8);
     g.window = pick(0, 2) ? 0 : pick(1, 700);
     const int page = 16 << pick(0, 4), max_pages = pick(0, 40);
@@ -56,7 +57,7 @@ static int one(std::mt19937 &rng) {
                 for (int j = lo; j < hi; ++j) CHECK(j <= p && (!g.window || j > p - g.window) && j < g.table_end);
                 if (hi <= lo) continue;
                 CHECK(lo >= k.lo && hi <= k.hi && k.t0 * kTileN <= lo && k.t1 * kTileN >= hi);
-                const int q = (i - k.i0) / tile_tokens(g);
+                const int q = (i - k.i0) / g.tokens;
                 CHECK(q < 2 && k.tile_t0[q] * kTileN <= lo && k.tile_t1[q] * kTileN >= hi);
                 CHECK(k.tile_t0[q] >= k.t0 && k.tile_t1[q] <= k.t1);
             }
