@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using L = Shape<HD>;
+    using F16 = Float16<typename std::conditional<BF16, __nv_bfloat16, __half>::type>;
     extern __shared__ __align__(1024) char smem[];
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -367,27 +368,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_lane()) tc_commit(bar(kBarEmpty + p.slot));
             __syncwarp();
         };
-        // S_i = Q K^T with rows of tile qi
+        // S_i = Q K^T with rows of tile qi (in an elected lane)
         auto qk = [&](int i, int qi, const Place &p) {
             const uint32_t kd = k_lo + (uint32_t)p.slot * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
-            if (elect_lane()) {
 #pragma unroll
-                for (int k = 0; k < HD / 16; ++k)
-                    tc_mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
-                              desc64(kd + (k / 4) * 64u + (k % 4) * 2u, kv_hi), a.idesc_qk, k > 0);
-                tc_commit(bar(kBarS + i));
-            }
+            for (int k = 0; k < HD / 16; ++k)
+                tc_mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
+                          desc64(kd + (k / 4) * 64u + (k % 4) * 2u, kv_hi), a.idesc_qk, k > 0);
+            tc_commit(bar(kBarS + i));
+        };
+        auto begin = [&](int i, int qi, const Place &p) {
+            if (elect_lane()) qk(i, qi, p);
             __syncwarp();
         };
-        // O_i (+)= P_i V
-        auto pv = [&](int i, const Place &p, bool first) {
-            const uint32_t vd = v_lo + (uint32_t)p.slot * (L::kSlot >> 4);
-            mbar_wait_spin(bar(kBarP + i), (np >> i) & 1, status);
-            np ^= 1u << i;
+        // O_i (+)= P_i V, and, if there is a next tile, its S_i right behind (over P_i, which the
+        // instructions before it have read)
+        auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more) {
+            const uint32_t vd = v_lo + (uint32_t)v.slot * (L::kSlot >> 4);
             if (first) {
                 mbar_wait(bar(kBarOFree + i), ((no >> i) & 1) ^ 1, status);
                 no ^= 1u << i;
             }
+            mbar_wait_spin(bar(kBarP + i), (np >> i) & 1, status);
+            np ^= 1u << i;
             tc_after();
             if (elect_lane()) {
 #pragma unroll
@@ -395,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + 128u * i + 8u * k,
                               desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
                 tc_commit(bar(kBarPv + i));
+                if (more) qk(i, qi, k_next);
             }
             __syncwarp();
         };
@@ -405,16 +409,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (uniform(block_alternates(a.g, w.b))) {
                 for (int k = 0; k < 2 && k < n; ++k, kp.step(2)) {
                     full(kp);
-                    qk(k, 0, kp);
+                    begin(k, 0, kp);
                     release(kp);
                 }
                 for (int k = 0; k < n; ++k, vp.step(2)) {
+                    // (few rows wait for memory: no key is waited for ahead of a product that could run)
                     full(vp);
-                    pv(k & 1, vp, k < 2);
+                    turn(k & 1, 0, vp, k < 2, kp, false);
                     release(vp);
                     if (k + 2 < n) {
                         full(kp);
-                        qk(k & 1, 0, kp);
+                        begin(k & 1, 0, kp);
                         release(kp);
                         kp.step(2);
                     }
@@ -425,25 +430,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int b1 = uniform(w.b.tile_t0[1] - t0), e1 = uniform(min(w.b.tile_t1[1] - t0, n));
                 bool begun0 = false, begun1 = false;
                 full(kp);
-                if (b0 <= 0 && 0 < e0) qk(0, 0, kp);
-                if (b1 <= 0 && 0 < e1) qk(1, 1, kp);
+                if (b0 <= 0 && 0 < e0) begin(0, 0, kp);
+                if (b1 <= 0 && 0 < e1) begin(1, 1, kp);
                 release(kp);
                 kp.step(2);
                 for (int k = 0; k < n; ++k, vp.step(2)) {
                     const bool more = k + 1 < n;
+                    const bool on0 = b0 <= k && k < e0, next0 = b0 <= k + 1 && k + 1 < e0;
+                    const bool on1 = b1 <= k && k < e1, next1 = b1 <= k + 1 && k + 1 < e1;
                     full(vp);
-                    if (b0 <= k && k < e0) {
-                        pv(0, vp, !begun0);
-                        begun0 = true;
-                    }
                     if (more) full(kp);
-                    if (b0 <= k + 1 && k + 1 < e0) qk(0, 0, kp);
-                    if (b1 <= k && k < e1) {
-                        pv(1, vp, !begun1);
+                    if (on0) {
+                        turn(0, 0, vp, !begun0, kp, next0);
+                        begun0 = true;
+                    } else if (next0) {
+                        begin(0, 0, kp);
+                    }
+                    if (on1) {
+                        turn(1, 1, vp, !begun1, kp, next1);
                         begun1 = true;
+                    } else if (next1) {
+                        begin(1, 1, kp);
                     }
                     release(vp);
-                    if (b1 <= k + 1 && k + 1 < e1) qk(1, 1, kp);
                     if (more) {
                         release(kp);
                         kp.step(2);
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t e = ffma2(pack2(s[k], s[k + 1]), c2, mc2);
                         const float p = ex2(lo_of(e)), q = ex2(hi_of(e));
                         sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
-                        to[k / 2] = BF16 ? Float16<__nv_bfloat16>::pack(p, q) : Float16<__half>::pack(p, q);
+                        to[k / 2] = F16::pack(p, q);
                     }
                 };
                 weights(s0, u);
@@ -652,12 +661,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             const int64_t first_token = w.first + a0, first_head = (int64_t)w.head * a.g.group;
-            auto put4 = [&](int64_t at, float x, float y, float z, float v) {
+            auto put8 = [&](int64_t at, const float *o, float f) {
                 if (a.out_f32) {
-                    *reinterpret_cast<float4 *>((float *)a.out + at) = make_float4(x, y, z, v);
+                    float4 *to = reinterpret_cast<float4 *>((float *)a.out + at);
+                    to[0] = make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
+                    to[1] = make_float4(o[4] * f, o[5] * f, o[6] * f, o[7] * f);
                 } else {
-                    using F = Float16<typename std::conditional<BF16, __nv_bfloat16, __half>::type>;
-                    *reinterpret_cast<uint2 *>((uint16_t *)a.out + at) = make_uint2(F::pack(x, y), F::pack(z, v));
+                    *reinterpret_cast<uint4 *>((uint16_t *)a.out + at) =
+                        make_uint4(F16::pack(o[0] * f, o[1] * f), F16::pack(o[2] * f, o[3] * f),
+                                   F16::pack(o[4] * f, o[5] * f), F16::pack(o[6] * f, o[7] * f));
                 }
             };
             const float ln2 = 0.6931471805599453f;
@@ -672,10 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         read(k, o);
                         if (r < rows) {
 #pragma unroll
-                            for (int y = 0; y < 32; y += 4) {
-                                // (a row with nothing to attend to: its accumulator is 0 x its values' finite rows)
-                                if (l > 0.0f) put4(at + 32 * k + y, o[y] * inv, o[y + 1] * inv, o[y + 2] * inv, o[y + 3] * inv);
-                                else put4(at + 32 * k + y, 0.0f, 0.0f, 0.0f, 0.0f);
+                            for (int y = 0; y < 32; y += 8) {
+                                if (!(l > 0.0f)) {
+#pragma unroll
+                                    for (int z = 0; z < 8; ++z) o[y + z] = 0.0f;  // (nothing to attend to)
+                                }
+                                put8(at + 32 * k + y, o + y, inv);
                             }
                         }
                     }
@@ -741,32 +755,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (a.lse) a.lse[(first_token + r_token) * a.n_heads + first_head + r_head] = S > 0.0f ? (M + log2f(S)) * ln2 : -INFINITY;
             }
             named_bar_sync(1 + i, 128);
-            for (int k = r; k < rows * (HD / 4); k += 128) {
-                const int row = k % rows, col = k / rows;
-                const float2 ml = scratch[row];
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int cta = c_first; cta <= c_last; cta += 4) {
-                    float2 p[4];
-                    float4 v[4];
+            // thread by thread eight columns of a row; many loads in flight: several such, or several parts
+            const int pieces = rows * (HD / 8);
+            auto join = [&](auto items_at_once, auto parts_at_once) {
+                constexpr int U = decltype(items_at_once)::value, P = decltype(parts_at_once)::value;
+                for (int k = r; k < pieces; k += 128 * U) {
+                    float acc[U][8] = {};
+                    int row[U], col[U];
+                    float M[U];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int pt = part_of(min(cta + y, c_last));
-                        p[y] = __ldcg(a.part_ml + pt * 128 + row);
-                        v[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o) + ((int64_t)pt * (HD / 4) + col) * 128 + row);
+                    for (int z = 0; z < U; ++z) {
+                        const int x = min(k + 128 * z, pieces - 1);
+                        col[z] = x / rows;
+                        row[z] = x - col[z] * rows;
+                        M[z] = scratch[row[z]].x;
+                    }
+                    for (int cta = c_first; cta <= c_last; cta += P) {
+                        float2 p[P][U];
+                        float4 v[P][U][2];
+#pragma unroll
+                        for (int y = 0; y < P; ++y)
+#pragma unroll
+                            for (int z = 0; z < U; ++z) {
+                                const int pt = part_of(min(cta + y, c_last));
+                                const float4 *src = reinterpret_cast<const float4 *>(a.part_o) + ((int64_t)pt * (HD / 4) + 2 * col[z]) * 128 + row[z];
+                                p[y][z] = __ldcg(a.part_ml + pt * 128 + row[z]);
+                                v[y][z][0] = __ldcg(src);
+                                v[y][z][1] = __ldcg(src + 128);
+                            }
+#pragma unroll
+                        for (int y = 0; y < P; ++y)
+#pragma unroll
+                            for (int z = 0; z < U; ++z) {
+                                if (cta + y > c_last || !(p[y][z].y > 0.0f)) continue;
+                                const float f = ex2(p[y][z].x - M[z]);
+                                const float e[8] = {v[y][z][0].x, v[y][z][0].y, v[y][z][0].z, v[y][z][0].w,
+                                                    v[y][z][1].x, v[y][z][1].y, v[y][z][1].z, v[y][z][1].w};
+#pragma unroll
+                                for (int t = 0; t < 8; ++t) acc[z][t] = fmaf(f, e[t], acc[z][t]);
+                            }
                     }
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        if (cta + y > c_last || !(p[y].y > 0.0f)) continue;
-                        const float f = ex2(p[y].x - ml.x);
-                        acc.x = fmaf(f, v[y].x, acc.x);
-                        acc.y = fmaf(f, v[y].y, acc.y);
-                        acc.z = fmaf(f, v[y].z, acc.z);
-                        acc.w = fmaf(f, v[y].w, acc.w);
+                    for (int z = 0; z < U; ++z) {
+                        if (k + 128 * z >= pieces) continue;
+                        const int64_t token = first_token + row[z] / a.g.group, head = first_head + row[z] % a.g.group;
+                        put8(token * a.out_stride + head * HD + 8 * col[z], acc[z], scratch[row[z]].y);
                     }
                 }
-                const int64_t token = first_token + row / a.g.group, head = first_head + row % a.g.group;
-                put4(token * a.out_stride + head * HD + 4 * col, acc.x * ml.y, acc.y * ml.y, acc.z * ml.y, acc.w * ml.y);
-            }
+            };
+            if (pieces > 256) join(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+            else join(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
             named_bar_sync(1 + i, 128);  // (scratch is free again)
         }
         if (lent) named_bar_sync(4, 256);
