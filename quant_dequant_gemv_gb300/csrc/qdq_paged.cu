@@ -23,19 +23,6 @@ struct AppendArgs {
     int n_heads, n_kv_heads, rope_dim, n_pages, page_shift, rows_per_warp, splits;
 };
 
-// 8 consecutive values of the input type as floats.
-template <typename TI>
-QDQ_DEV void load4(const TI *p, float *x) {
-    if constexpr (sizeof(TI) == 4) {
-        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-        const float2 a = Float16<TI>::unpack(v.x), b = Float16<TI>::unpack(v.y);
-        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-    }
-}
-
 // A group of D/8 lanes takes one head row, eight values a lane. A lane's values are
 // whole rotation pairs: in the interleaved layout eight consecutive values, in the
 // split layout four from each half of the turning dims (lanes past the turning dims

@@ -60,4 +60,17 @@ struct Float16<__nv_bfloat16> {
     static QDQ_DEV __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
 };
 
+// Four consecutive values, read once, as floats.
+template <typename TI>
+QDQ_DEV void load4(const TI *p, float *x) {
+    if constexpr (sizeof(TI) == 4) {
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        const float2 a = Float16<TI>::unpack(v.x), b = Float16<TI>::unpack(v.y);
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+    }
+}
+
 }  // namespace qdq

@@ -11,9 +11,15 @@
 // exponent (1/16 wide) instead of the key; the last of them is open, and its entries
 // weigh less than half a unit each. The entries that share the cut's key are told apart
 // by narrowing over their indices, and so is the draw itself (an inverse CDF in index
-// order). If the bins up to the one that holds the first cut have at most kList entries,
-// those are gathered in the first CTA, which finishes alone while the others leave;
-// otherwise the cluster narrows together.
+// order).
+//
+// Most cuts lie near the top. A bin that certainly holds top-k's is found from the largest
+// entry of each thread alone (the k-th largest of those is not above the k-th of all), top-
+// p's from the bins' masses. If the bins down to that one have at most kList entries, those
+// are gathered in the first CTA, which finishes alone while the others leave (with up to
+// kFew entries by comparing all pairs). Otherwise only the cut's own bin is gathered and
+// narrowed there, and the whole cluster draws; a bin with more than kList entries (ties,
+// as a rule) is narrowed by the whole cluster.
 //
 // Masses are integers (weights in units of 2^-44 of the largest), so neither the order of
 // the additions nor the split over CTAs changes a sum. In the bins they are kept as three
@@ -33,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = kThreads, kMaxCluster = 8;
 constexpr int kSlice = 1 << 15;  // entries of a row that a CTA holds at most
-constexpr int kList = 2048;
+constexpr int kList = 2048, kFew = kThreads / 4;
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr uint32_t kLowest = 0x00800000u;  // the key of the lowest finite logit (-inf is one below)
 typedef unsigned long long u64;
@@ -55,12 +61,13 @@ QDQ_DEV uint32_t key_of(float x) {
 QDQ_DEV float value_of(uint32_t k) { return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu)); }
 
 struct Shared {
-    unsigned bins[2][4][kBins];   // three pieces of mass (or a count in the first), and a count
+    unsigned bins[2][3][kBins];   // three pieces of mass, or a count in the first
     u64 sums[2][kMaxCluster][2];  // what the cluster's CTAs sent
     u64 warp[kWarps + 1][2];
     u64 found[2];                 // the bin a cut lies in, and the measure above it
     uint32_t edge[2];
-    u64 list[kList];              // key << 32 | index
+    u64 cut[3];                   // the first CTA's word on a cut: key, measure above it, measure at it
+    u64 list[kList];              // key << 32 | ~index: in the order of the cuts
     __align__(16) float x[4];     // the slice (slice entries)
 };
 
@@ -140,7 +147,7 @@ struct Row {
     template <bool ALONE, typename F>
     QDQ_DEV void each(F f) {
         if (ALONE) {
-            for (int i = tid; i < n; i += kThreads) f(value_of((uint32_t)(sh.list[i] >> 32)), (uint32_t)sh.list[i]);
+            for (int i = tid; i < n; i += kThreads) f(value_of((uint32_t)(sh.list[i] >> 32)), ~(uint32_t)sh.list[i]);
         } else {
             for (int i = 4 * tid; i < n; i += 4 * kThreads) {
                 const float4 x = *reinterpret_cast<const float4 *>(sh.x + i);
@@ -186,30 +193,24 @@ struct Row {
         for (int i = 0; i < 3; ++i) atomicAdd(&sh.bins[turn_b][i][b], p[i]);
     }
     // Bin `tid` over the whole cluster (each CTA reads all the others'): PIECES of mass, or a
-    // count with PIECES = 1. With a `below`: the fourth array too, as a count, over the whole
-    // cluster and over the CTAs below this one. Ends the turn.
+    // count with PIECES = 1. Ends the turn.
     template <bool ALONE, int PIECES>
-    QDQ_DEV u64 gather_bins(unsigned *count = nullptr, unsigned *below = nullptr) {
+    QDQ_DEV u64 gather_bins() {
         sync<ALONE>();
         u64 v = 0;
         if (ALONE) {
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) v += (u64)sh.bins[turn_b][i][tid] << (15 * i);
         } else {
-            unsigned c = 0;
 #pragma unroll 4
             for (uint32_t r = 0; r < ctas; ++r) {
-                unsigned x[4] = {};
+                unsigned x[PIECES];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < PIECES || (i == 3 && below))
-                        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x[i]) : "r"(remote(&sh.bins[turn_b][i][tid], r)));
-                if (below && r == rank) *below = c;
-                c += x[3];
+                for (int i = 0; i < PIECES; ++i)
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x[i]) : "r"(remote(&sh.bins[turn_b][i][tid], r)));
 #pragma unroll
                 for (int i = 0; i < PIECES; ++i) v += (u64)x[i] << (15 * i);
             }
-            if (below) *count = c;
         }
         turn_b ^= 1;
         return v;
@@ -277,51 +278,40 @@ struct Row {
         hi = sh.edge[1] - 1;
     }
 
-    // Bins over the index: 128 neighbours share a bin of 128 or more, so a warp adds its sum
+    // Counts over the index: 128 neighbours share a bin of 128 or more, so a warp adds its sum
     // once (their atomics would all meet at one address).
-    template <bool MASS, typename GET>
+    template <typename GET>
     QDQ_DEV void bin_neighbours(int shift, GET get) {
         for (int i0 = warp * 128; i0 < n; i0 += 4 * kThreads) {
             const int i = i0 + 4 * lane;  // (the slice is filled up to a multiple of 128)
             const float4 v = *reinterpret_cast<const float4 *>(sh.x + i);
             const float x[4] = {v.x, v.y, v.z, v.w};
-            unsigned sum[3] = {};
+            unsigned sum = 0;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 uint32_t k;
-                if (!get(x[y], (uint32_t)(i_first + i + y), k)) continue;
-                if (MASS) {
-                    unsigned p[3];
-                    pieces(weight(x[y]), p);
-                    sum[0] += p[0], sum[1] += p[1], sum[2] += p[2];
-                } else {
-                    ++sum[0];
-                }
+                sum += get(x[y], (uint32_t)(i_first + i + y), k);
             }
-            unsigned *at = &sh.bins[turn_b][0][(i_first + i0) >> shift];
-#pragma unroll
-            for (int y = 0; y < (MASS ? 3 : 1); ++y) {
-                const unsigned t = __reduce_add_sync(kAll, sum[y]);
-                if (lane == 0 && t) atomicAdd(at + y * kBins, t);
-            }
+            sum = __reduce_add_sync(kAll, sum);
+            if (lane == 0 && sum) atomicAdd(&sh.bins[turn_b][0][(i_first + i0) >> shift], sum);
         }
     }
 
     // The largest key in [lo, hi] at which the measure from hi down (from `ahead` on)
     // reaches the target; `ahead` becomes the measure above it; returns its own. get(key,
-    // index, k, f): whether an entry counts, under which key, with which mass. With SHARE
-    // the target is the share of the whole that `share` asks for, set at the first level.
+    // index, k): whether an entry counts, and under which key. With SHARE the target is the
+    // draw's mark in the whole, which the first level finds.
     // INDEX: the keys are inverted indices, and [lo, hi] begins as all of them.
     template <bool ALONE, bool MASS, bool INDEX = false, bool SHARE = false, typename GET>
-    QDQ_DEV u64 narrow(uint32_t lo, uint32_t hi, u64 &ahead, u64 &target, uint32_t &key, GET get, double share = 0.0,
-                       u64 *whole = nullptr) {
+    QDQ_DEV u64 narrow(uint32_t lo, uint32_t hi, u64 &ahead, u64 target, uint32_t &key, GET get, u64 *whole = nullptr,
+                       const SampleArgs *a = nullptr, int row = 0) {
         for (int level = 0; level < 4; ++level) {  // 9 bits a level: 32 bits take four
             // (a level over neighbours has bins of 128 at least)
-            const bool neighbours = INDEX && !ALONE && level == 0;
+            const bool neighbours = INDEX && !ALONE && !MASS && level == 0;
             const int shift = max(neighbours ? 7 : 0, 32 - 9 - __clz(hi - lo));
             clear_bins(MASS ? 3 : 1);
             if (neighbours) {
-                bin_neighbours<MASS>(shift, get);
+                bin_neighbours(shift, get);
             } else {
                 const float x_lo = value_of(lo), x_hi = value_of(hi);
                 each<ALONE>([&](float x, uint32_t index) {
@@ -338,7 +328,7 @@ struct Row {
             const u64 excl = ahead + before(v, &all);
             if (SHARE && level == 0) {
                 *whole = all;
-                target = min((u64)(share * (double)all) + 1, all);
+                target = mark(*a, row, all);
             }
             find(v, excl, target);
             const uint32_t b = (uint32_t)sh.found[0] & (kBins - 1);
@@ -358,6 +348,162 @@ struct Row {
         return 1;
     }
 
+    // Counts of the first level (without the open bin, which gets what the others leave of
+    // `total`), and the bin of the top_k-th entry with the count above it.
+    template <bool ALONE>
+    QDQ_DEV void first_counts(u64 top_k, u64 total, int &bin, u64 &ahead) {
+        clear_bins(1);
+        each<ALONE>([&](float x, uint32_t) {
+            const int k = bin_of(x);
+            if (k < kBins - 1) atomicAdd(&sh.bins[turn_b][0][k], 1u);
+        });
+        const u64 count = gather_bins<ALONE, 1>();
+        u64 all;
+        const u64 excl = before(count, &all);
+        find(tid == kBins - 1 ? total - excl : count, excl, top_k);
+        bin = (int)sh.found[0] & (kBins - 1);
+        ahead = sh.found[1];
+    }
+
+    // The key of a cut in first-level bin b (narrow(), which see, from `ahead` above the bin, not
+    // below `least`): alone, or by the first CTA for all, or by the cluster.
+    template <bool ALONE, bool MASS>
+    QDQ_DEV u64 resolve(int b, uint32_t least, u64 &ahead, u64 target, uint32_t &key) {
+        const auto by_key = [](float x, uint32_t, uint32_t &k) { return k = key_of(x), true; };
+        uint32_t lo, hi;
+        if (ALONE) {
+            keys_of(b, lo, hi);
+            return narrow<true, MASS>(max(lo, least), hi, ahead, target, key, by_key);
+        }
+        unsigned own = 0;
+        each<false>([&](float x, uint32_t) { own += bin_of(x) == b && x != -INFINITY; });
+        u64 listed, at;
+        if (!gather_list(own, listed, at, [&](float x) { return bin_of(x) == b && x != -INFINITY; })) {
+            keys_of(b, lo, hi);
+            return narrow<false, MASS>(max(lo, least), hi, ahead, target, key, by_key);
+        }
+        if (rank == 0) {
+            const int slice = n, turn = turn_b;  // (the bins' turns are the cluster's)
+            n = (int)listed;
+            keys_of(b, lo, hi);
+            const u64 here = narrow<true, MASS>(max(lo, least), hi, ahead, target, key, by_key);
+            n = slice;
+            turn_b = turn;
+            if (tid < (int)ctas) {
+                const uint32_t to = remote(&sh.cut[0], tid);
+                store_remote(to, key);
+                store_remote(to + 8, ahead);
+                store_remote(to + 16, here);
+            }
+        }
+        cluster_sync();
+        key = (uint32_t)sh.cut[0];
+        ahead = sh.cut[1];
+        return sh.cut[2];
+    }
+
+    // Entries that `take` names, `own` of them this thread's, into the first CTA's list; false,
+    // and nothing is moved, if they are more than it holds.
+    template <typename TAKE>
+    QDQ_DEV bool gather_list(unsigned own, u64 &listed, u64 &at, TAKE take) {
+        send<false>(__reduce_add_sync(kAll, own), 0, ctas);
+        cluster_sync();
+        listed = at = 0;
+        for (uint32_t c = 0; c < ctas; ++c) {
+            if (c == rank) at = listed;
+            listed += part(c, 0);
+        }
+        if (listed > kList) return false;
+        unsigned all;
+        uint32_t to = remote(&sh.list[0], 0) + 8 * ((uint32_t)at + before(own, &all));
+        if (own)
+            each<false>([&](float x, uint32_t index) {
+                if (!take(x)) return;
+                store_remote(to, ((u64)key_of(x) << 32) | (uint32_t)~index);
+                to += 8;
+            });
+        cluster_sync();
+        return true;
+    }
+
+    // The cluster's draw: the kept mass of each warp's segment of the slice, of each CTA, and
+    // then the warp whose segment holds the mark looks for it. keep(x, index) names the kept.
+    template <typename KEEP>
+    QDQ_DEV void draw(const SampleArgs &a, int b, float floor_w, KEEP keep) {
+        const int seg = (((n + kWarps - 1) / kWarps) + 127) / 128 * 128;
+        const int s0 = warp * seg, s1 = min(s0 + seg, n);
+        unsigned sum[3] = {};  // (at most 64 entries a thread)
+        const auto mass4 = [&](int i, unsigned (&p)[4][3], float (&w)[4]) {
+            const float4 v = *reinterpret_cast<const float4 *>(sh.x + i);
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                w[y] = keep(x[y], (uint32_t)(i_first + i + y)) ? weight(x[y]) : 0.0f;
+                if (!(w[y] >= floor_w)) w[y] = 0.0f;
+                pieces(w[y], p[y]);
+            }
+        };
+        for (int i = s0 + 4 * lane; i < s1; i += 128) {
+            unsigned p[4][3];
+            float w[4];
+            mass4(i, p, w);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                for (int z = 0; z < 3; ++z) sum[z] += p[y][z];
+        }
+        u64 mass = 0;
+        for (int z = 0; z < 3; ++z) mass += (u64)__reduce_add_sync(kAll, sum[z]) << (15 * z);
+        send<false>(mass, 0, ctas);
+        cluster_sync();
+        u64 whole = 0, ahead = 0;
+        for (uint32_t c = 0; c < ctas; ++c) {
+            if (c == rank) ahead = whole;
+            whole += part(c, 0);
+        }
+        const u64 target = mark(a, b, whole);
+        for (int w = 0; w < warp; ++w) ahead += sh.warp[w][0];
+        if (!(ahead < target && target <= ahead + mass)) return;
+        for (int i0 = s0; i0 < s1; i0 += 128) {
+            unsigned p[4][3];
+            float w[4];
+            mass4(i0 + 4 * lane, p, w);
+            u64 f[4], own = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                f[y] = ((u64)p[y][2] << 30) + ((u64)p[y][1] << 15) + p[y][0];
+                own += f[y];
+            }
+            u64 incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 e = __shfl_up_sync(kAll, incl, o);
+                if (lane >= o) incl += e;
+            }
+            const u64 all = __shfl_sync(kAll, incl, 31);
+            if (ahead + all < target) {
+                ahead += all;
+                continue;
+            }
+            u64 excl = ahead + incl - own;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                if (excl < target && target <= excl + f[y]) {
+                    a.tokens[b] = (int64_t)(i_first + i0 + 4 * lane + y);
+                    if (a.logprobs) a.logprobs[b] = share_log(w[y], whole);
+                }
+                excl += f[y];
+            }
+            return;
+        }
+    }
+    // The mass at which the draw stops: the first unit above u of the whole (at u = 1, the last).
+    static QDQ_DEV u64 mark(const SampleArgs &a, int b, u64 whole_mass) {
+        return min((u64)(fmin(fmax((double)a.u[b], 0.0), 1.0) * (double)whole_mass) + 1, whole_mass);
+    }
+    static QDQ_DEV float share_log(float w, u64 whole_mass) {
+        return (float)log((double)w / ((double)whole_mass * 0x1p-44));
+    }
+
     // Everything after the first level: the cuts, the ties, the draw. top_k: 0, or with the
     // first-level bin of its cut and the count above that; top_p: below 1 if it is used, and
     // without top-k with its cut's bin, the mass above that and the mass to reach.
@@ -367,12 +513,11 @@ struct Row {
     };
     template <bool ALONE>
     QDQ_DEV void finish(const SampleArgs &a, int b, First first, float top_p, float floor_w) {
-        uint32_t cut = kLowest, lo, hi;
+        uint32_t cut = kLowest;
         u64 ties = ~0ull, here = 0;  // entries above `cut` are kept, and the first `ties` at it
-        const auto by_key = [](float x, uint32_t, uint32_t &k) { return k = key_of(x), true; };
         if (first.top_k) {
-            keys_of(first.bin, lo, hi);
-            here = narrow<ALONE, false>(lo, hi, first.ahead, first.top_k, cut, by_key);
+            if (ALONE) first_counts<true>(first.top_k, n, first.bin, first.ahead);
+            here = resolve<ALONE, false>(first.bin, kLowest, first.ahead, first.top_k, cut);
             ties = first.top_k - first.ahead;
         }
         if (top_p < 1.0f) {
@@ -395,13 +540,18 @@ struct Row {
                 first.bin = (int)sh.found[0] & (kBins - 1);
                 first.ahead = sh.found[1];
             }
-            keys_of(first.bin, lo, hi);
             uint32_t key;
-            const u64 mass = narrow<ALONE, true>(max(lo, cut), hi, first.ahead, first.target, key, by_key);
-            // the fewest of the entries at the key that reach the target
-            const u64 f = fixed(weight(value_of(key))), need = (first.target - first.ahead + f - 1) / f;
-            here = mass / f;
-            ties = min(need, first.top_k && key == cut ? ties : here);
+            const u64 mass = resolve<ALONE, true>(first.bin, cut, first.ahead, first.target, key);
+            // the fewest of the entries at the key that reach the target (one alone, mostly)
+            const u64 f = fixed(weight(value_of(key)));
+            u64 need = 1;
+            const u64 most = first.top_k && key == cut ? ties : ~0ull;
+            here = 1;
+            if (mass != f) {
+                need = (first.target - first.ahead + f - 1) / f;
+                here = mass / f;
+            }
+            ties = min(need, most);
             cut = key;
         }
         const float x_cut = value_of(cut);
@@ -416,21 +566,83 @@ struct Row {
             tie_last = ~inverted;
         }
         // the draw: the first index at which the running mass of the kept entries exceeds u of
-        // the whole (at u = 1, reaches the whole)
+        // the whole
+        const auto keep = [&](float x, uint32_t i) { return x > x_cut || (x == x_cut && i <= tie_last); };
+        if (!ALONE) {
+            draw(a, b, floor_w, keep);
+            return;
+        }
         uint32_t inverted;
-        u64 mass_ahead = 0, whole_mass;
+        u64 mass_ahead = 0, whole_mass = 0;
         narrow<ALONE, true, true, true>(0xFFFFFFFFu - (uint32_t)(a.vocab - 1), 0xFFFFFFFFu, mass_ahead, first.target, inverted,
-                                        [&](float x, uint32_t i, uint32_t &k) {
-                                            k = ~i;
-                                            return (x > x_cut || (x == x_cut && i <= tie_last)) && weight(x) >= floor_w;
-                                        },
-                                        fmin(fmax((double)a.u[b], 0.0), 1.0), &whole_mass);
+                                        [&](float x, uint32_t i, uint32_t &k) { return k = ~i, keep(x, i) && weight(x) >= floor_w; },
+                                        &whole_mass, &a, b);
         const uint32_t token = ~inverted;
         each<ALONE>([&](float x, uint32_t index) {
             if (index != token) return;
             a.tokens[b] = (int64_t)token;
-            if (a.logprobs) a.logprobs[b] = (float)log((double)weight(x) / ((double)whole_mass * 0x1p-44));
+            if (a.logprobs) a.logprobs[b] = share_log(weight(x), whole_mass);
         });
+    }
+    // The same for a list of at most kFew entries: four threads to an entry. Its rank in the
+    // list, the cuts as positions in that order (one warp), then the kept mass up to its
+    // index, which is the draw.
+    QDQ_DEV void finish_few(const SampleArgs &a, int b, const First &first, float top_p, float floor_w) {
+        const int e = tid >> 2, q = tid & 3;
+        u64 *sorted = sh.list + kFew, *mass = sh.list + 2 * kFew;
+        const u64 mine = e < n ? sh.list[e] : 0;
+        int rank_e = 0;
+        for (int j = q; j < n; j += 4) rank_e += sh.list[j] > mine;
+        rank_e += __shfl_xor_sync(kAll, rank_e, 1);
+        rank_e += __shfl_xor_sync(kAll, rank_e, 2);
+        if (e < n && q == 0) {
+            sorted[rank_e] = mine;
+            mass[rank_e] = fixed(weight(value_of((uint32_t)(mine >> 32))));
+        }
+        __syncthreads();
+        if (warp == 0) {
+            u64 f[4], incl = 0, excl;
+            const int keep = first.top_k ? min((int)first.top_k, n) : n;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                f[y] = 4 * lane + y < keep ? mass[4 * lane + y] : 0;
+                incl += f[y];
+            }
+            u64 sum = incl;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const u64 t = __shfl_up_sync(kAll, sum, o);
+                if (lane >= o) sum += t;
+            }
+            excl = sum - incl;
+            // an entry is kept while the mass before it is below top-p's share
+            const u64 target = top_p >= 1.0f ? ~0ull : first.top_k ? reach(top_p, __shfl_sync(kAll, sum, 31)) : first.target;
+            u64 whole = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int at = 4 * lane + y;
+                const bool in = at < keep && excl < target && weight(value_of((uint32_t)(sorted[at] >> 32))) >= floor_w;
+                excl += f[y];
+                if (!in) f[y] = 0;
+                if (at < n) mass[at] = f[y];
+                whole += f[y];
+            }
+            whole = warp_sum(whole);
+            if (lane == 0) sh.found[0] = whole;
+        }
+        __syncthreads();
+        const u64 whole = sh.found[0];
+        const u64 target = mark(a, b, whole);
+        const u64 at = e < n ? sorted[e] : 0, f = e < n ? mass[e] : 0;
+        u64 sum = 0;
+        for (int j = q; j < n; j += 4)
+            if ((uint32_t)sorted[j] >= (uint32_t)at) sum += mass[j];  // (inverted: an index not above this one)
+        sum += __shfl_xor_sync(kAll, sum, 1);
+        sum += __shfl_xor_sync(kAll, sum, 2);
+        if (q == 0 && f && sum >= target && sum - f < target) {
+            a.tokens[b] = (int64_t)(uint32_t)~(uint32_t)at;
+            if (a.logprobs) a.logprobs[b] = share_log(weight(value_of((uint32_t)(at >> 32))), whole);
+        }
     }
     // top-p's mass to reach: at least one unit, so that the first entry is kept whatever it is.
     static QDQ_DEV u64 reach(float top_p, u64 whole_mass) {
@@ -458,19 +670,31 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
 
     // The slice, with the row's largest key and the lowest index that has it. NaN becomes
     // -inf and -0 becomes +0: equal logits have equal keys.
-    u64 best = 0;
+    float top_x = -INFINITY;
+    int top_i = -1;
     unsigned live = 0;
-#pragma unroll 8
-    for (int i = tid; i < r.n; i += kThreads) {
-        float x = (float)src[i];
+    const auto put = [&](float x, int i) {
         x = x == x ? x + 0.0f : -INFINITY;
-        sh.x[i] = x;
         live += x != -INFINITY;
-        const u64 e = ((u64)key_of(x) << 32) | (0xFFFFFFFFu - (unsigned)(r.i_first + i));
-        best = e > best ? e : best;
+        if (x > top_x) top_x = x, top_i = i;  // (a thread's indices rise)
+        return x;
+    };
+    int done = 0;
+    if (((uintptr_t)src & (4 * sizeof(T) - 1)) == 0) {  // four at a time where the row allows it
+        done = r.n & ~3;
+#pragma unroll 4
+        for (int i = 4 * tid; i < done; i += 4 * kThreads) {
+            float x[4];
+            load4(src + i, x);
+            *reinterpret_cast<float4 *>(sh.x + i) = make_float4(put(x[0], i), put(x[1], i + 1), put(x[2], i + 2), put(x[3], i + 3));
+        }
     }
+#pragma unroll 8
+    for (int i = done + tid; i < r.n; i += kThreads) sh.x[i] = put((float)src[i], i);
+    u64 best = top_i < 0 ? 0 : ((u64)key_of(top_x) << 32) | (0xFFFFFFFFu - (unsigned)(r.i_first + top_i));
     for (int i = r.n + tid; i < (r.n + 127) / 128 * 128; i += kThreads) sh.x[i] = -INFINITY;
-    for (int i = 0; i < 4; ++i) sh.bins[0][i][tid] = 0;
+    for (int i = 0; i < 3; ++i) sh.bins[0][i][tid] = 0;
+    const uint32_t mine = (uint32_t)(best >> 32);  // (0, which is no logit's, for a thread without any)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const u64 e = __shfl_xor_sync(kAll, best, o);
@@ -498,55 +722,48 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     const float share = by_p ? top_p : 1.0f;
     if (!by_k && !by_p) {
         r.finish<false>(a, b, first, share, floor_w);
-        cluster_sync();  // (no CTA leaves while another reads its bins)
         return;
     }
-    // first level: counts (the open bin's is what the others leave), and for top-p alone masses
-    r.each<false>([&](float x, uint32_t) {
-        const int k = r.bin_of(x);
-        if (k == kBins - 1) return;
-        atomicAdd(&sh.bins[0][3][k], 1u);
-        if (!by_k) r.add_mass(k, r.weight(x));
-    });
-    unsigned count, below;
-    if (by_k) {
-        r.gather_bins<false, 0>(&count, &below);
-        u64 all;
-        const u64 ahead = r.before((u64)count, &all);
-        r.find(tid == kBins - 1 ? alive - ahead : count, ahead, (u64)top_k);
+    // the first level: the bin down to which entries are gathered
+    const bool maxima = by_k && 4 * (int64_t)top_k <= min(a.vocab, kThreads * (int)ctas);
+    if (tid == 0) sh.found[0] = kBins - 1;
+    u64 all;
+    if (maxima) {
+        const int k = mine >= kLowest ? r.bin_of(value_of(mine)) : kBins - 1;
+        __syncthreads();
+        if (k < kBins - 1) atomicAdd(&sh.bins[0][0][k], 1u);
+        const u64 count = r.gather_bins<false, 1>();
+        const u64 ahead = r.before(count, &all);
+        r.find(count, ahead, (u64)top_k);  // (the open bin if there are not as many)
+        first.bin = (int)sh.found[0] & (kBins - 1);
+    } else if (by_k) {
+        r.first_counts<false>((u64)top_k, alive, first.bin, first.ahead);
     } else {
-        const u64 mass = r.gather_bins<false, 3>(&count, &below);
-        u64 all;
+        r.each<false>([&](float x, uint32_t) {
+            const int k = r.bin_of(x);
+            if (k < kBins - 1) r.add_mass(k, r.weight(x));
+        });
+        const u64 mass = r.gather_bins<false, 3>();
         const u64 ahead = r.before(mass, &all);
         first.target = Row::reach(top_p, all);
         r.find(mass, ahead, first.target);
+        first.bin = (int)sh.found[0] & (kBins - 1);
+        first.ahead = sh.found[1];
     }
-    first.bin = (int)sh.found[0] & (kBins - 1);
-    first.ahead = sh.found[1];
     if (first.bin < kBins - 1) {
-        // entries in the bins up to that one: in the cluster, and in the CTAs below this one
-        u64 both;
-        r.before(tid <= first.bin ? ((u64)count << 32) + below : 0ull, &both);
-        const unsigned listed = (unsigned)(both >> 32), at = (unsigned)both;
-        if (listed <= kList) {
-            // into the first CTA's list, this CTA's from `at` on; their order there is of no consequence
-            if (tid == 0) sh.edge[0] = 0;
-            __syncthreads();
-            const uint32_t to = remote(&sh.list[0], 0);
-            r.each<false>([&](float x, uint32_t index) {
-                if (r.bin_of(x) > first.bin) return;
-                const unsigned i = at + atomicAdd(&sh.edge[0], 1u);
-                if (i < kList) store_remote(to + 8 * i, ((u64)key_of(x) << 32) | index);
-            });
-            cluster_sync();
+        unsigned own = 0;
+        r.each<false>([&](float x, uint32_t) { own += r.bin_of(x) <= first.bin; });
+        u64 listed, at;
+        if (r.gather_list(own, listed, at, [&](float x) { return r.bin_of(x) <= first.bin; })) {
             if (rank) return;
             r.n = (int)listed;
-            r.finish<true>(a, b, first, share, floor_w);
+            if (listed <= kFew) r.finish_few(a, b, first, share, floor_w);
+            else r.finish<true>(a, b, first, share, floor_w);
             return;
         }
     }
+    if (maxima) r.first_counts<false>((u64)top_k, alive, first.bin, first.ahead);
     r.finish<false>(a, b, first, share, floor_w);
-    cluster_sync();
 }
 
 // CTAs per row: enough to hold it (16384 entries each, which leaves room for two CTAs an
