@@ -375,10 +375,20 @@ struct Row {
             keys_of(b, lo, hi);
             return narrow<true, MASS>(max(lo, least), hi, ahead, target, key, by_key);
         }
-        unsigned own = 0;
-        each<false>([&](float x, uint32_t) { own += bin_of(x) == b && x != -INFINITY; });
-        u64 listed, at;
-        if (!gather_list(own, listed, at, [&](float x) { return bin_of(x) == b && x != -INFINITY; })) {
+        u64 own = 0;
+        each_bit([&](float x, u64 bit) { own |= bin_of(x) == b && x != -INFINITY ? bit : 0; });
+        send<false>(__reduce_add_sync(kAll, __popcll(own)), 0, ctas);
+        cluster_sync();
+        return resolve_listed<MASS>(b, own, 0, least, ahead, target, key);
+    }
+    // The same for the cluster, from the threads' entries in the bin and, sent as value i, how
+    // many a CTA has.
+    template <bool MASS>
+    QDQ_DEV u64 resolve_listed(int b, u64 own, int i, uint32_t least, u64 &ahead, u64 target, uint32_t &key) {
+        const auto by_key = [](float x, uint32_t, uint32_t &k) { return k = key_of(x), true; };
+        uint32_t lo, hi;
+        u64 listed;
+        if (!gather_list(own, i, listed)) {
             keys_of(b, lo, hi);
             return narrow<false, MASS>(max(lo, least), hi, ahead, target, key, by_key);
         }
@@ -402,26 +412,34 @@ struct Row {
         return sh.cut[2];
     }
 
-    // Entries that `take` names, `own` of them this thread's, into the first CTA's list; false,
-    // and nothing is moved, if they are more than it holds.
-    template <typename TAKE>
-    QDQ_DEV bool gather_list(unsigned own, u64 &listed, u64 &at, TAKE take) {
-        send<false>(__reduce_add_sync(kAll, own), 0, ctas);
-        cluster_sync();
-        listed = at = 0;
+    // f(logit, bit) over the slice, for sets of a thread's entries (64 at most).
+    template <typename F>
+    QDQ_DEV void each_bit(F f) {
+        u64 bit = 1;
+        for (int i = 4 * tid; i < n; i += 4 * kThreads, bit <<= 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(sh.x + i);
+            f(x.x, bit);
+            f(x.y, bit << 1);
+            f(x.z, bit << 2);
+            f(x.w, bit << 3);
+        }
+    }
+    // The threads' sets of entries into the first CTA's list; false, and nothing is moved, if
+    // they are more than it holds. The CTAs' counts were sent, as value i.
+    QDQ_DEV bool gather_list(u64 own, int i, u64 &listed) {
+        u64 at = 0;
+        listed = 0;
         for (uint32_t c = 0; c < ctas; ++c) {
             if (c == rank) at = listed;
-            listed += part(c, 0);
+            listed += part(c, i);
         }
         if (listed > kList) return false;
         unsigned all;
-        uint32_t to = remote(&sh.list[0], 0) + 8 * ((uint32_t)at + before(own, &all));
-        if (own)
-            each<false>([&](float x, uint32_t index) {
-                if (!take(x)) return;
-                store_remote(to, ((u64)key_of(x) << 32) | (uint32_t)~index);
-                to += 8;
-            });
+        uint32_t to = remote(&sh.list[0], 0) + 8 * ((uint32_t)at + before((unsigned)__popcll(own), &all));
+        for (; own; own &= own - 1, to += 8) {
+            const int k = __ffsll(own) - 1, e = 4 * tid + (k >> 2) * 4 * kThreads + (k & 3);
+            store_remote(to, ((u64)key_of(sh.x[e]) << 32) | (uint32_t)~(uint32_t)(i_first + e));
+        }
         cluster_sync();
         return true;
     }
@@ -511,8 +529,9 @@ struct Row {
         u64 top_k, ahead, target;
         int bin;
     };
+    // `own`: with top-p alone, in a cluster, the thread's entries in that bin (sent as value 1).
     template <bool ALONE>
-    QDQ_DEV void finish(const SampleArgs &a, int b, First first, float top_p, float floor_w) {
+    QDQ_DEV void finish(const SampleArgs &a, int b, First first, float top_p, float floor_w, u64 own = 0) {
         uint32_t cut = kLowest;
         u64 ties = ~0ull, here = 0;  // entries above `cut` are kept, and the first `ties` at it
         if (first.top_k) {
@@ -541,7 +560,9 @@ struct Row {
                 first.ahead = sh.found[1];
             }
             uint32_t key;
-            const u64 mass = resolve<ALONE, true>(first.bin, cut, first.ahead, first.target, key);
+            const u64 mass = ALONE || first.top_k
+                                 ? resolve<ALONE, true>(first.bin, cut, first.ahead, first.target, key)
+                                 : resolve_listed<true>(first.bin, own, 1, cut, first.ahead, first.target, key);
             // the fewest of the entries at the key that reach the target (one alone, mostly)
             const u64 f = fixed(weight(value_of(key)));
             u64 need = 1;
@@ -750,11 +771,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         first.bin = (int)sh.found[0] & (kBins - 1);
         first.ahead = sh.found[1];
     }
+    u64 in_bin = 0;
     if (first.bin < kBins - 1) {
-        unsigned own = 0;
-        r.each<false>([&](float x, uint32_t) { own += r.bin_of(x) <= first.bin; });
-        u64 listed, at;
-        if (r.gather_list(own, listed, at, [&](float x) { return r.bin_of(x) <= first.bin; })) {
+        // the entries down to that bin, and those in it
+        u64 own = 0, listed;
+        r.each_bit([&](float x, u64 bit) {
+            const int k = r.bin_of(x);
+            own |= k <= first.bin ? bit : 0;
+            in_bin |= k == first.bin ? bit : 0;
+        });
+        r.send<false>(__reduce_add_sync(kAll, __popcll(own)), __reduce_add_sync(kAll, __popcll(in_bin)), ctas);
+        cluster_sync();
+        if (r.gather_list(own, 0, listed)) {
             if (rank) return;
             r.n = (int)listed;
             if (listed <= kFew) r.finish_few(a, b, first, share, floor_w);
@@ -763,7 +791,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         }
     }
     if (maxima) r.first_counts<false>((u64)top_k, alive, first.bin, first.ahead);
-    r.finish<false>(a, b, first, share, floor_w);
+    r.finish<false>(a, b, first, share, floor_w, in_bin);
 }
 
 // CTAs per row: enough to hold it (16384 entries each, which leaves room for two CTAs an
