@@ -86,20 +86,21 @@ struct Shape {
     static constexpr uint32_t kGroup8 = (uint32_t)kHalves * 1024u;  // 8 positions of a slot
     static constexpr uint32_t kQ = 0, kRing = 2 * kQTile;
     static constexpr uint32_t kBars = kRing + kSlots * kSlot;
-    static constexpr uint32_t kScratch = kBars + 256;        // joins: 2 groups x 128 x (maximum, 1 / sum)
+    static constexpr uint32_t kScratch = kBars + 288;        // joins: 2 groups x 128 x (maximum, 1 / sum)
     static constexpr uint32_t kStart = kScratch + 2 * 128 * 8;  // the CTA's first piece, tensor-memory base
-    static constexpr uint32_t kTotal = kStart + 64;
+    static constexpr uint32_t kPieces = kStart + 64;
+    static constexpr uint32_t kTotal = kPieces + 192;
 };
 // barriers (8 bytes each) at kBars
 constexpr int kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 21, kBarS = 22, kBarP = 24, kBarPv = 26,
-              kBarOFree = 28, kBarDrain = 30;
+              kBarOFree = 28, kBarDrain = 30, kBarPiece = 31, kBarPieceFree = 33;
 
 struct Start {
     long long total, item, pos, end;  // units: of all items, where the first one begins, the CTA's range
     int seq, block, head, ctas, live;
 };
 
-// A walk over the pieces of a CTA's range; every role walks it by itself.
+// A walk over the pieces of a CTA's range, by the copying warp.
 struct Walk {
     long long item, pos, end;  // units: where the item begins, the rest of the range
     int seq, block, head, off, n;  // the piece: n key tiles from the item's off-th on
@@ -146,14 +147,28 @@ struct Walk {
     }
 };
 
+// What the other warps need of a piece, in one of two places in shared memory.
+struct Piece {
+    const int32_t *pages;  // the sequence's page table
+    int n;                 // key tiles; 0 ends the walk
+    int t0;                // the first
+    int lo, hi;            // positions that the block attends to
+    int tokens, token0, p0;  // the block's tokens, the row of the first, its position
+    int head;
+    int tile_t0[2], tile_t1[2];
+    int alt, whole;        // alternate key tiles of one tile of rows; the whole item
+    int c_first, c_last;   // the CTAs that hold parts of the item, if not
+};
+static_assert(2 * sizeof(Piece) <= 192, "Shape::kPieces");
+
 // The pages of key tile j that hold positions of [lo, hi): lane l's entry of the page
 // table (for the tile's l-th run of min(page, 128) positions), or -1 where there is none.
 // The entry is checked where it is used, a tile later, so that nothing waits for the load.
-QDQ_DEV int tile_page(const KernelArgs &a, const Walk &w, int j, int run_shift) {
+QDQ_DEV int tile_page(const KernelArgs &a, const Piece &w, int j, int run_shift) {
     const int lane = threadIdx.x & 31;
     const int64_t p = (int64_t)j * kTileN + (lane << run_shift);
     int page = -1;
-    if (lane < (kTileN >> run_shift) && p < w.b.hi && p + (1 << run_shift) > w.b.lo)
+    if (lane < (kTileN >> run_shift) && p < w.hi && p + (1 << run_shift) > w.lo)
         page = w.pages[(int)p >> a.page_shift];  // (inside the table: hi is)
     return page;
 }
@@ -288,13 +303,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kBarPv + i), 1);
             mbar_init(bar(kBarOFree + i), 4);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarPiece + i), 1);
+            mbar_init(bar(kBarPieceFree + i), 9);
+        }
         mbar_init(bar(kBarDrain), 1);
         fence_mbar_init();
     }
     find_start<HD>(a, smem, start);
     if (!start->live) return;
     const Start s0 = *start;
-    const long long total = s0.total;
     __syncthreads();
     fence_async_smem();  // the ring's memory goes over to the copies
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kStart);
@@ -305,13 +323,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
 
     const int run_shift = min(a.page_shift, 7), tq = a.g.tokens;
+    Piece *pieces = reinterpret_cast<Piece *>(smem + L::kPieces);
 
     if (warp == kWarpLoad) {
         // ---- copies ---------------------------------------------------------------------
         const uint32_t q_rows = (uint32_t)(tq * a.g.group), run_bytes = (L::kGroup8 << run_shift) >> 3;
         uint32_t seq_no = 0, items = 0;
-        for (Walk w(a, s0); w.more(); w.next(a), ++items) {
-            const int n = w.n, t0 = w.t_beg(), tiles = w.b.i1 - w.b.i0 > tq ? 2 : 1;
+        for (Walk w(a, s0);; w.next(a), ++items) {
+            const int n = w.n, t0 = w.t_beg();
+            Piece &piece = pieces[items & 1];
+            mbar_wait(bar(kBarPieceFree + (items & 1)), ((items >> 1) & 1) ^ 1, status);
+            if (lane == 0) {
+                piece.n = n;
+                if (n) {
+                    piece.pages = w.pages;
+                    piece.t0 = t0;
+                    piece.lo = w.b.lo, piece.hi = w.b.hi;
+                    piece.tokens = w.b.i1 - w.b.i0, piece.token0 = w.first + w.b.i0, piece.p0 = w.kv - w.count + w.b.i0;
+                    piece.head = w.head;
+                    for (int i = 0; i < 2; ++i) piece.tile_t0[i] = w.b.tile_t0[i], piece.tile_t1[i] = w.b.tile_t1[i];
+                    piece.alt = block_alternates(a.g, w.b);
+                    piece.whole = w.whole();
+                    if (!w.whole()) {
+                        piece.c_first = range_owner(s0.total, s0.ctas, w.item + kItemUnits);
+                        piece.c_last = range_owner(s0.total, s0.ctas, w.item + item_units(w.b) - 1);
+                    }
+                }
+                mbar_arrive(bar(kBarPiece + (items & 1)));
+            }
+            __syncwarp();
+            if (!w.more()) break;
+            const int tiles = w.b.i1 - w.b.i0 > tq ? 2 : 1;
             mbar_wait(bar(kBarQEmpty), (items & 1) ^ 1, status);
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar(kBarQFull), tiles * L::kHalves * q_rows * 128u);
@@ -320,10 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
                                     w.first + w.b.i0 + i * tq, bar(kBarQFull));
             }
-            int page = tile_page(a, w, t0, run_shift);
+            int page = tile_page(a, piece, t0, run_shift);
             for (int j = 0; j < n; ++j) {
                 const int here = (unsigned)page < (unsigned)a.n_pages ? page : -1;
-                if (j + 1 < n) page = tile_page(a, w, t0 + j + 1, run_shift);
+                if (j + 1 < n) page = tile_page(a, piece, t0 + j + 1, run_shift);
                 const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0);
                 const uint32_t bytes = __popc(have) * run_bytes;
                 // the lane's run of positions: its first group of 8 rows in the pools
@@ -403,10 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         };
         Place kp = {0, 0}, vp = {1, 0};
-        for (Walk w(a, s0); w.more(); w.next(a), ++items) {
-            const int n = uniform(w.n), t0 = w.t_beg();
+        for (;; ++items) {
+            const Piece &w = pieces[items & 1];
+            mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
+            const int n = uniform(w.n), t0 = uniform(w.t0);
+            if (n == 0) break;
             mbar_wait(bar(kBarQFull), items & 1, status);
-            if (uniform(block_alternates(a.g, w.b))) {
+            if (uniform(w.alt)) {
                 for (int k = 0; k < 2 && k < n; ++k, kp.step(2)) {
                     full(kp);
                     begin(k, 0, kp);
@@ -426,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 // the sets' key tiles, counted from the piece's first
-                const int b0 = uniform(w.b.tile_t0[0] - t0), e0 = uniform(min(w.b.tile_t1[0] - t0, n));
-                const int b1 = uniform(w.b.tile_t0[1] - t0), e1 = uniform(min(w.b.tile_t1[1] - t0, n));
+                const int b0 = uniform(w.tile_t0[0] - t0), e0 = uniform(min(w.tile_t1[0] - t0, n));
+                const int b1 = uniform(w.tile_t0[1] - t0), e1 = uniform(min(w.tile_t1[1] - t0, n));
                 bool begun0 = false, begun1 = false;
                 full(kp);
                 if (b0 <= 0 && 0 < e0) begin(0, 0, kp);
@@ -459,7 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (elect_lane()) tc_commit(bar(kBarQEmpty));
+            if (elect_lane()) {
+                tc_commit(bar(kBarQEmpty));
+                mbar_arrive(bar(kBarPieceFree + (items & 1)));
+            }
             __syncwarp();
         }
         if (elect_lane()) tc_commit(bar(kBarDrain));
@@ -476,19 +524,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r_token = r / a.g.group, r_head = r - r_token * a.g.group;
         uint32_t seq_no = 0, ns = 0, npv = 0;
         bool lent = false;  // the second set's scratch holds a state that the first may not have read
-        for (Walk w(a, s0); w.more(); w.next(a)) {
-            const int n = w.n, t0 = w.t_beg();
+        for (uint32_t items = 0;; ++items) {
+            const Piece &w = pieces[items & 1];
+            mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
+            const int n = w.n, t0 = w.t0;
+            if (n == 0) break;
+            const auto done = [&] {  // the piece's place is free again
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarPieceFree + (items & 1)));
+            };
             const uint32_t base = seq_no;
             seq_no += 2 * n;
-            const bool alt = block_alternates(a.g, w.b);
+            const bool alt = w.alt != 0;
             // this set's rows and key tiles of the piece
-            const int qi = alt ? 0 : i, a0 = w.b.i0 + qi * tq, tokens = min(tq, w.b.i1 - a0), rows = tokens * a.g.group;
-            if (rows <= 0) continue;
+            const int qi = alt ? 0 : i, tokens = min(tq, w.tokens - qi * tq), rows = tokens * a.g.group;
+            if (rows <= 0) {
+                done();
+                continue;
+            }
             const bool idle = (warp & 3) * 32 >= rows;  // no row of the warp's lanes is one
             const int step = alt ? 2 : 1;
-            const int j0 = alt ? t0 + i : max(t0, qi ? w.b.tile_t0[1] : w.b.tile_t0[0]);
-            const int j1 = alt ? t0 + n : min(t0 + n, qi ? w.b.tile_t1[1] : w.b.tile_t1[0]);
-            const int p_first = w.kv - w.count + a0;
+            const int j0 = alt ? t0 + i : max(t0, w.tile_t0[qi]);
+            const int j1 = alt ? t0 + n : min(t0 + n, w.tile_t1[qi]);
+            const int p_first = w.p0 + qi * tq;
             int lo, hi, lo_last, hi_first, x;
             span(a.g, p_first + min(r_token, tokens - 1), 1, lo, hi);
             span(a.g, p_first, 1, x, hi_first);
@@ -501,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (j + step < j1) page = tile_page(a, w, j + step, run_shift);
                 const int p0 = j * kTileN;
                 const unsigned all = (1u << (kTileN >> run_shift)) - 1;
-                const bool dirty = have != all || p0 < w.b.lo || p0 + kTileN > w.b.hi;
+                const bool dirty = have != all || p0 < w.lo || p0 + kTileN > w.hi;
                 const bool masked = dirty || p0 < lo_last || p0 + kTileN > hi_first;
                 // columns 32 k .. 32 k + 31 of a masked tile: those outside [lo, hi) and whole
                 // runs of absent pages become -inf
@@ -592,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // zero the rows of V that hold no position of the block (row r of the slot)
                     const uint32_t vs = base + 2 * (j - t0) + 1;
                     mbar_wait(bar(kBarFull + vs % L::kSlots), (vs / L::kSlots) & 1, status);
-                    if (p0 + r < w.b.lo || p0 + r >= w.b.hi || !((have >> (r >> run_shift)) & 1)) {
+                    if (p0 + r < w.lo || p0 + r >= w.hi || !((have >> (r >> run_shift)) & 1)) {
                         char *row = smem + L::kRing + (vs % L::kSlots) * L::kSlot + (r / 8) * L::kGroup8 + (r % 8) * 128;
 #pragma unroll
                         for (int k = 0; k < HD / 8; ++k)
@@ -618,10 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (alt && i == 1) {
                 if (lent) named_bar_sync(4, 256);
                 lent = both;
-                if (!both) continue;
-                scratch[r] = make_float2(mc, l);
-                tc_before();
-                named_bar_arrive(3, 256);
+                if (both) {
+                    scratch[r] = make_float2(mc, l);
+                    tc_before();
+                    named_bar_arrive(3, 256);
+                }
+                done();
                 continue;
             }
             if (both) {
@@ -660,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (both) mbar_arrive(bar(kBarOFree + 1));
                 }
             };
-            const int64_t first_token = w.first + a0, first_head = (int64_t)w.head * a.g.group;
+            const int64_t first_token = w.token0 + qi * tq, first_head = (int64_t)w.head * a.g.group;
             auto put8 = [&](int64_t at, const float *o, float f) {
                 if (a.out_f32) {
                     float4 *to = reinterpret_cast<float4 *>((float *)a.out + at);
@@ -673,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             const float ln2 = 0.6931471805599453f;
-            if (w.whole()) {
+            if (w.whole) {
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 const int64_t token = first_token + r_token, head = first_head + r_head;
                 const int64_t at = token * a.out_stride + head * HD;
@@ -696,11 +756,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 read_done();
                 if (a.lse && r < rows) a.lse[token * a.n_heads + head] = l > 0.0f ? (mc + log2f(l)) * ln2 : -INFINITY;
+                done();
                 continue;
             }
             // partial state: O as [column / 4][row][4], so that rows of a warp are contiguous
-            const int c_first = range_owner(total, s0.ctas, w.item + kItemUnits);
-            const int c_last = range_owner(total, s0.ctas, w.item + item_units(w.b) - 1);
+            const int c_first = w.c_first, c_last = w.c_last;
+            done();
             auto part_of = [&](int cta) { return (cta * 2 + (cta == c_first ? 1 : 0)) * 2 + i; };
             {
                 const int part = part_of(blockIdx.x);
