@@ -58,7 +58,7 @@ __device__ int g_attend_status;
 
 constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 320;
 constexpr float kLag = 8.0f;  // log2 of how far the running maximum may lag
-constexpr int kColO = 256;    // tensor memory: S/P of the two sets in columns 0..255, then O
+constexpr int kColO = 256;
 
 struct KernelArgs {
     int n_seqs, n_tokens, max_pages;
@@ -86,14 +86,20 @@ struct Shape {
     static constexpr uint32_t kGroup8 = (uint32_t)kHalves * 1024u;  // 8 positions of a slot
     static constexpr uint32_t kQ = 0, kRing = 2 * kQTile;
     static constexpr uint32_t kBars = kRing + kSlots * kSlot;
-    static constexpr uint32_t kScratch = kBars + 288;        // joins: 2 groups x 128 x (maximum, 1 / sum)
+    static constexpr uint32_t kScratch = kBars + 304;        // joins: 2 groups x 128 x (maximum, 1 / sum)
     static constexpr uint32_t kStart = kScratch + 2 * 128 * 8;  // the CTA's first piece, tensor-memory base
+    // Tensor memory: S of the two sets in columns 0..255, O from kColO on. At 64 dims P has
+    // columns of its own, so that the next S can be computed while the weights still are; at
+    // 128 dims nothing is left, and P lies over S.
+    static constexpr bool kApart = HD == 64;
+    static constexpr int kColP = kApart ? kColO + 2 * HD : 0, kPitchP = kApart ? 64 : 128;
     static constexpr uint32_t kPieces = kStart + 64;
     static constexpr uint32_t kTotal = kPieces + 192;
 };
 // barriers (8 bytes each) at kBars
 constexpr int kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 21, kBarS = 22, kBarP = 24, kBarPv = 26,
-              kBarOFree = 28, kBarDrain = 30, kBarPiece = 31, kBarPieceFree = 33;
+              kBarOFree = 28, kBarDrain = 30, kBarPiece = 31, kBarPieceFree = 33,
+              kBarSFree = 35;
 
 struct Start {
     long long total, item, pos, end;  // units: of all items, where the first one begins, the CTA's range
@@ -302,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(kBarP + i), 4);
             mbar_init(bar(kBarPv + i), 1);
             mbar_init(bar(kBarOFree + i), 4);
+            mbar_init(bar(kBarSFree + i), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBarPiece + i), 1);
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Everything that an instruction's operands depend on is kept known to be the same in
         // every lane (values out of memory go through a shuffle), or each operand costs moves.
         constexpr uint32_t q_hi = sdesc_hi(1024), kv_hi = sdesc_hi(L::kGroup8);
-        uint32_t items = 0, np = 0, no = 0;  // np, no: bit i is the phase of set i's barrier
+        uint32_t items = 0, np = 0, no = 0, nf = 0;  // np, no, nf: bit i is the phase of set i's barrier
         const uint32_t q_lo = sdesc_lo(16) | ((sb + L::kQ) >> 4);
         const uint32_t k_lo = sdesc_lo(16) | ((sb + L::kRing) >> 4), v_lo = sdesc_lo(1024) | ((sb + L::kRing) >> 4);
         auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
@@ -423,13 +430,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_lane()) qk(i, qi, p);
             __syncwarp();
         };
-        // O_i (+)= P_i V, and, if there is a next tile, its S_i right behind (over P_i, which the
-        // instructions before it have read)
+        // O_i (+)= P_i V, and, if there is a next tile, its S_i: once the last one has been read, or
+        // (over P_i, which the instructions before it have read) right behind
         auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more) {
             const uint32_t vd = v_lo + (uint32_t)v.slot * (L::kSlot >> 4);
             if (first) {
                 mbar_wait(bar(kBarOFree + i), ((no >> i) & 1) ^ 1, status);
                 no ^= 1u << i;
+            }
+            if (L::kApart) {
+                mbar_wait_spin(bar(kBarSFree + i), (nf >> i) & 1, status);
+                nf ^= 1u << i;
+                tc_after();
+                if (more) begin(i, qi, k_next);
             }
             mbar_wait_spin(bar(kBarP + i), (np >> i) & 1, status);
             np ^= 1u << i;
@@ -437,10 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_lane()) {
 #pragma unroll
                 for (int k = 0; k < kTileN / 16; ++k)
-                    tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + 128u * i + 8u * k,
+                    tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColP + L::kPitchP * i + 8u * k,
                               desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
                 tc_commit(bar(kBarPv + i));
-                if (more) qk(i, qi, k_next);
+                if (!L::kApart && more) qk(i, qi, k_next);
             }
             __syncwarp();
         };
@@ -518,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = warp >> 2, r = threadIdx.x & 127;  // set; row = tensor-memory lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t t_s = tmem + lanes + 128u * i, t_o = tmem + lanes + kColO + (uint32_t)HD * i;
+        const uint32_t t_p = tmem + lanes + L::kColP + L::kPitchP * i;
         const float c = a.scale_log2;
         const uint64_t c2 = pack2(c, c);
         float2 *scratch = reinterpret_cast<float2 *>(smem + L::kScratch) + i * 128;
@@ -573,6 +587,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 mbar_wait_spin(bar(kBarS + i), ns++ & 1, status);
                 tc_after();
+                const auto s_read = [&] {  // S may be overwritten
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarSFree + i));
+                };
+                if (L::kApart && idle) s_read();
                 if (!idle) {
                 // The row's maximum, 64 columns at a time: the last 64 are read again when
                 // their turn comes, so that a thread holds 64 scores and not 128.
@@ -635,14 +655,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 weights(s0, u);
                 tc_ld32(t_s + 64, s0);
                 weights(s1, u + 16);
-                tc_st32(t_s, u);
+                if (L::kApart && npv > 0) {  // the last tile's weights have been read
+                    mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
+                    tc_after();
+                }
+                tc_st32(t_p, u);
                 tc_ld32(t_s + 96, s1);
                 tc_wait_ld<32>(s0);
                 tc_wait_ld<32>(s1);
+                if (L::kApart) s_read();
                 if (masked) mask(s0, 2), mask(s1, 3);
                 weights(s0, u);
                 weights(s1, u + 16);
-                tc_st32(t_s + 32, u);
+                tc_st32(t_p + 32, u);
                 const uint64_t t = fadd2(sum[0], sum[1]);
                 l += lo_of(t) + hi_of(t);
                 }
