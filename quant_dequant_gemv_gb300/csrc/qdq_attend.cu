@@ -56,7 +56,7 @@ namespace {
 
 __device__ int g_attend_status;
 
-constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 320;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 384;
 constexpr float kLag = 8.0f;  // log2 of how far the running maximum may lag
 constexpr int kColO = 256;
 
@@ -332,201 +332,208 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int run_shift = min(a.page_shift, 7), tq = a.g.tokens;
     Piece *pieces = reinterpret_cast<Piece *>(smem + L::kPieces);
 
-    if (warp == kWarpLoad) {
-        // ---- copies ---------------------------------------------------------------------
-        const uint32_t q_rows = (uint32_t)(tq * a.g.group), run_bytes = (L::kGroup8 << run_shift) >> 3;
-        uint32_t seq_no = 0, items = 0;
-        for (Walk w(a, s0);; w.next(a), ++items) {
-            const int n = w.n, t0 = w.t_beg();
-            Piece &piece = pieces[items & 1];
-            mbar_wait(bar(kBarPieceFree + (items & 1)), ((items >> 1) & 1) ^ 1, status);
-            if (lane == 0) {
-                piece.n = n;
-                if (n) {
-                    piece.pages = w.pages;
-                    piece.t0 = t0;
-                    piece.lo = w.b.lo, piece.hi = w.b.hi;
-                    piece.tokens = w.b.i1 - w.b.i0, piece.token0 = w.first + w.b.i0, piece.p0 = w.kv - w.count + w.b.i0;
-                    piece.head = w.head;
-                    for (int i = 0; i < 2; ++i) piece.tile_t0[i] = w.b.tile_t0[i], piece.tile_t1[i] = w.b.tile_t1[i];
-                    piece.alt = block_alternates(a.g, w.b);
-                    piece.whole = w.whole();
-                    if (!w.whole()) {
-                        piece.c_first = range_owner(s0.total, s0.ctas, w.item + kItemUnits);
-                        piece.c_last = range_owner(s0.total, s0.ctas, w.item + item_units(w.b) - 1);
+    // Registers: launched with 168 a thread, three warpgroups of them; the softmax groups go
+    // up to 216, which holds a row's 128 scores without spilling, and the third, of which two
+    // warps work, comes down to 72: 2 x 216 + 72 = 3 x 168 (attend_create checks the 168).
+    if (warp >= kWarpMma) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == kWarpLoad) {
+            // ---- copies ---------------------------------------------------------------------
+            const uint32_t q_rows = (uint32_t)(tq * a.g.group), run_bytes = (L::kGroup8 << run_shift) >> 3;
+            uint32_t seq_no = 0, items = 0;
+            for (Walk w(a, s0);; w.next(a), ++items) {
+                const int n = w.n, t0 = w.t_beg();
+                Piece &piece = pieces[items & 1];
+                mbar_wait(bar(kBarPieceFree + (items & 1)), ((items >> 1) & 1) ^ 1, status);
+                if (lane == 0) {
+                    piece.n = n;
+                    if (n) {
+                        piece.pages = w.pages;
+                        piece.t0 = t0;
+                        piece.lo = w.b.lo, piece.hi = w.b.hi;
+                        piece.tokens = w.b.i1 - w.b.i0, piece.token0 = w.first + w.b.i0, piece.p0 = w.kv - w.count + w.b.i0;
+                        piece.head = w.head;
+                        for (int i = 0; i < 2; ++i) piece.tile_t0[i] = w.b.tile_t0[i], piece.tile_t1[i] = w.b.tile_t1[i];
+                        piece.alt = block_alternates(a.g, w.b);
+                        piece.whole = w.whole();
+                        if (!w.whole()) {
+                            piece.c_first = range_owner(s0.total, s0.ctas, w.item + kItemUnits);
+                            piece.c_last = range_owner(s0.total, s0.ctas, w.item + item_units(w.b) - 1);
+                        }
+                    }
+                    mbar_arrive(bar(kBarPiece + (items & 1)));
+                }
+                __syncwarp();
+                if (!w.more()) break;
+                const int tiles = w.b.i1 - w.b.i0 > tq ? 2 : 1;
+                mbar_wait(bar(kBarQEmpty), (items & 1) ^ 1, status);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(kBarQFull), tiles * L::kHalves * q_rows * 128u);
+                    for (int i = 0; i < tiles; ++i)
+                        for (int h = 0; h < L::kHalves; ++h)
+                            tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
+                                        w.first + w.b.i0 + i * tq, bar(kBarQFull));
+                }
+                int page = tile_page(a, piece, t0, run_shift);
+                for (int j = 0; j < n; ++j) {
+                    const int here = (unsigned)page < (unsigned)a.n_pages ? page : -1;
+                    if (j + 1 < n) page = tile_page(a, piece, t0 + j + 1, run_shift);
+                    const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0);
+                    const uint32_t bytes = __popc(have) * run_bytes;
+                    // the lane's run of positions: its first group of 8 rows in the pools
+                    const int in_page = ((t0 + j) * kTileN + (lane << run_shift)) & ((1 << a.page_shift) - 1);
+                    const int row8 = a.row8_layer + (int)((((int64_t)here << a.page_shift) + in_page) >> 3);
+    #pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++seq_no) {
+                        const int slot = seq_no % L::kSlots;
+                        mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
+                        if (lane == 0) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
+                        __syncwarp();
+                        if (here >= 0)
+                            tma_load_4d(sb + L::kRing + slot * L::kSlot + (uint32_t)lane * run_bytes, kv ? &v_map : &k_map, 0,
+                                        0, w.head * L::kHalves, row8, bar(kBarFull + slot));
                     }
                 }
-                mbar_arrive(bar(kBarPiece + (items & 1)));
             }
-            __syncwarp();
-            if (!w.more()) break;
-            const int tiles = w.b.i1 - w.b.i0 > tq ? 2 : 1;
-            mbar_wait(bar(kBarQEmpty), (items & 1) ^ 1, status);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar(kBarQFull), tiles * L::kHalves * q_rows * 128u);
-                for (int i = 0; i < tiles; ++i)
-                    for (int h = 0; h < L::kHalves; ++h)
-                        tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
-                                    w.first + w.b.i0 + i * tq, bar(kBarQFull));
-            }
-            int page = tile_page(a, piece, t0, run_shift);
-            for (int j = 0; j < n; ++j) {
-                const int here = (unsigned)page < (unsigned)a.n_pages ? page : -1;
-                if (j + 1 < n) page = tile_page(a, piece, t0 + j + 1, run_shift);
-                const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0);
-                const uint32_t bytes = __popc(have) * run_bytes;
-                // the lane's run of positions: its first group of 8 rows in the pools
-                const int in_page = ((t0 + j) * kTileN + (lane << run_shift)) & ((1 << a.page_shift) - 1);
-                const int row8 = a.row8_layer + (int)((((int64_t)here << a.page_shift) + in_page) >> 3);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv, ++seq_no) {
-                    const int slot = seq_no % L::kSlots;
-                    mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
-                    if (lane == 0) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
-                    __syncwarp();
-                    if (here >= 0)
-                        tma_load_4d(sb + L::kRing + slot * L::kSlot + (uint32_t)lane * run_bytes, kv ? &v_map : &k_map, 0,
-                                    0, w.head * L::kHalves, row8, bar(kBarFull + slot));
+            // every copy has landed before the CTA can end, also after a wait that ran out
+            for (uint32_t i = seq_no < (uint32_t)L::kSlots ? 0 : seq_no - L::kSlots; i < seq_no; ++i)
+                mbar_wait(bar(kBarFull + i % L::kSlots), (i / L::kSlots) & 1, status);
+            if (items) mbar_wait(bar(kBarQFull), (items - 1) & 1, status);
+        } else if (warp == kWarpMma) {
+            // ---- matrix instructions ----------------------------------------------------------
+            // Everything that an instruction's operands depend on is kept known to be the same in
+            // every lane (values out of memory go through a shuffle), or each operand costs moves.
+            constexpr uint32_t q_hi = sdesc_hi(1024), kv_hi = sdesc_hi(L::kGroup8);
+            uint32_t items = 0, np = 0, no = 0, nf = 0;  // np, no, nf: bit i is the phase of set i's barrier
+            const uint32_t q_lo = sdesc_lo(16) | ((sb + L::kQ) >> 4);
+            const uint32_t k_lo = sdesc_lo(16) | ((sb + L::kRing) >> 4), v_lo = sdesc_lo(1024) | ((sb + L::kRing) >> 4);
+            auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+            // A place in the ring; keys and values alternate, so the next of a kind is two on.
+            struct Place {
+                int slot;
+                uint32_t phase;
+                QDQ_DEV void step(int by) {
+                    slot += by;
+                    if (slot >= L::kSlots) slot -= L::kSlots, phase ^= 1;
                 }
-            }
-        }
-        // every copy has landed before the CTA can end, also after a wait that ran out
-        for (uint32_t i = seq_no < (uint32_t)L::kSlots ? 0 : seq_no - L::kSlots; i < seq_no; ++i)
-            mbar_wait(bar(kBarFull + i % L::kSlots), (i / L::kSlots) & 1, status);
-        if (items) mbar_wait(bar(kBarQFull), (items - 1) & 1, status);
-    } else if (warp == kWarpMma) {
-        // ---- matrix instructions ----------------------------------------------------------
-        // Everything that an instruction's operands depend on is kept known to be the same in
-        // every lane (values out of memory go through a shuffle), or each operand costs moves.
-        constexpr uint32_t q_hi = sdesc_hi(1024), kv_hi = sdesc_hi(L::kGroup8);
-        uint32_t items = 0, np = 0, no = 0, nf = 0;  // np, no, nf: bit i is the phase of set i's barrier
-        const uint32_t q_lo = sdesc_lo(16) | ((sb + L::kQ) >> 4);
-        const uint32_t k_lo = sdesc_lo(16) | ((sb + L::kRing) >> 4), v_lo = sdesc_lo(1024) | ((sb + L::kRing) >> 4);
-        auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-        // A place in the ring; keys and values alternate, so the next of a kind is two on.
-        struct Place {
-            int slot;
-            uint32_t phase;
-            QDQ_DEV void step(int by) {
-                slot += by;
-                if (slot >= L::kSlots) slot -= L::kSlots, phase ^= 1;
-            }
-        };
-        auto full = [&](const Place &p) { mbar_wait(bar(kBarFull + p.slot), p.phase, status); };
-        auto release = [&](const Place &p) {
-            if (elect_lane()) tc_commit(bar(kBarEmpty + p.slot));
-            __syncwarp();
-        };
-        // S_i = Q K^T with rows of tile qi (in an elected lane)
-        auto qk = [&](int i, int qi, const Place &p) {
-            const uint32_t kd = k_lo + (uint32_t)p.slot * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
-#pragma unroll
-            for (int k = 0; k < HD / 16; ++k)
-                tc_mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
-                          desc64(kd + (k / 4) * 64u + (k % 4) * 2u, kv_hi), a.idesc_qk, k > 0);
-            tc_commit(bar(kBarS + i));
-        };
-        auto begin = [&](int i, int qi, const Place &p) {
-            if (elect_lane()) qk(i, qi, p);
-            __syncwarp();
-        };
-        // O_i (+)= P_i V, and, if there is a next tile, its S_i: once the last one has been read, or
-        // (over P_i, which the instructions before it have read) right behind
-        auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more) {
-            const uint32_t vd = v_lo + (uint32_t)v.slot * (L::kSlot >> 4);
-            if (first) {
-                mbar_wait(bar(kBarOFree + i), ((no >> i) & 1) ^ 1, status);
-                no ^= 1u << i;
-            }
-            if (L::kApart) {
-                mbar_wait_spin(bar(kBarSFree + i), (nf >> i) & 1, status);
-                nf ^= 1u << i;
+            };
+            auto full = [&](const Place &p) { mbar_wait(bar(kBarFull + p.slot), p.phase, status); };
+            auto release = [&](const Place &p) {
+                if (elect_lane()) tc_commit(bar(kBarEmpty + p.slot));
+                __syncwarp();
+            };
+            // S_i = Q K^T with rows of tile qi (in an elected lane)
+            auto qk = [&](int i, int qi, const Place &p) {
+                const uint32_t kd = k_lo + (uint32_t)p.slot * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
+    #pragma unroll
+                for (int k = 0; k < HD / 16; ++k)
+                    tc_mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
+                              desc64(kd + (k / 4) * 64u + (k % 4) * 2u, kv_hi), a.idesc_qk, k > 0);
+                tc_commit(bar(kBarS + i));
+            };
+            auto begin = [&](int i, int qi, const Place &p) {
+                if (elect_lane()) qk(i, qi, p);
+                __syncwarp();
+            };
+            // O_i (+)= P_i V, and, if there is a next tile, its S_i: once the last one has been read, or
+            // (over P_i, which the instructions before it have read) right behind
+            auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more) {
+                const uint32_t vd = v_lo + (uint32_t)v.slot * (L::kSlot >> 4);
+                if (first) {
+                    mbar_wait(bar(kBarOFree + i), ((no >> i) & 1) ^ 1, status);
+                    no ^= 1u << i;
+                }
+                if (L::kApart) {
+                    mbar_wait_spin(bar(kBarSFree + i), (nf >> i) & 1, status);
+                    nf ^= 1u << i;
+                    tc_after();
+                    if (more) begin(i, qi, k_next);
+                }
+                mbar_wait_spin(bar(kBarP + i), (np >> i) & 1, status);
+                np ^= 1u << i;
                 tc_after();
-                if (more) begin(i, qi, k_next);
-            }
-            mbar_wait_spin(bar(kBarP + i), (np >> i) & 1, status);
-            np ^= 1u << i;
-            tc_after();
-            if (elect_lane()) {
-#pragma unroll
-                for (int k = 0; k < kTileN / 16; ++k)
-                    tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColP + L::kPitchP * i + 8u * k,
-                              desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
-                tc_commit(bar(kBarPv + i));
-                if (!L::kApart && more) qk(i, qi, k_next);
-            }
-            __syncwarp();
-        };
-        Place kp = {0, 0}, vp = {1, 0};
-        for (;; ++items) {
-            const Piece &w = pieces[items & 1];
-            mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
-            const int n = uniform(w.n), t0 = uniform(w.t0);
-            if (n == 0) break;
-            mbar_wait(bar(kBarQFull), items & 1, status);
-            if (uniform(w.alt)) {
-                for (int k = 0; k < 2 && k < n; ++k, kp.step(2)) {
-                    full(kp);
-                    begin(k, 0, kp);
-                    release(kp);
+                if (elect_lane()) {
+    #pragma unroll
+                    for (int k = 0; k < kTileN / 16; ++k)
+                        tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColP + L::kPitchP * i + 8u * k,
+                                  desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
+                    tc_commit(bar(kBarPv + i));
+                    if (!L::kApart && more) qk(i, qi, k_next);
                 }
-                for (int k = 0; k < n; ++k, vp.step(2)) {
-                    // (few rows wait for memory: no key is waited for ahead of a product that could run)
-                    full(vp);
-                    turn(k & 1, 0, vp, k < 2, kp, false);
-                    release(vp);
-                    if (k + 2 < n) {
+                __syncwarp();
+            };
+            Place kp = {0, 0}, vp = {1, 0};
+            for (;; ++items) {
+                const Piece &w = pieces[items & 1];
+                mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
+                const int n = uniform(w.n), t0 = uniform(w.t0);
+                if (n == 0) break;
+                mbar_wait(bar(kBarQFull), items & 1, status);
+                if (uniform(w.alt)) {
+                    for (int k = 0; k < 2 && k < n; ++k, kp.step(2)) {
                         full(kp);
-                        begin(k & 1, 0, kp);
+                        begin(k, 0, kp);
                         release(kp);
-                        kp.step(2);
+                    }
+                    for (int k = 0; k < n; ++k, vp.step(2)) {
+                        // (few rows wait for memory: no key is waited for ahead of a product that could run)
+                        full(vp);
+                        turn(k & 1, 0, vp, k < 2, kp, false);
+                        release(vp);
+                        if (k + 2 < n) {
+                            full(kp);
+                            begin(k & 1, 0, kp);
+                            release(kp);
+                            kp.step(2);
+                        }
+                    }
+                } else {
+                    // the sets' key tiles, counted from the piece's first
+                    const int b0 = uniform(w.tile_t0[0] - t0), e0 = uniform(min(w.tile_t1[0] - t0, n));
+                    const int b1 = uniform(w.tile_t0[1] - t0), e1 = uniform(min(w.tile_t1[1] - t0, n));
+                    bool begun0 = false, begun1 = false;
+                    full(kp);
+                    if (b0 <= 0 && 0 < e0) begin(0, 0, kp);
+                    if (b1 <= 0 && 0 < e1) begin(1, 1, kp);
+                    release(kp);
+                    kp.step(2);
+                    for (int k = 0; k < n; ++k, vp.step(2)) {
+                        const bool more = k + 1 < n;
+                        const bool on0 = b0 <= k && k < e0, next0 = b0 <= k + 1 && k + 1 < e0;
+                        const bool on1 = b1 <= k && k < e1, next1 = b1 <= k + 1 && k + 1 < e1;
+                        full(vp);
+                        if (more) full(kp);
+                        if (on0) {
+                            turn(0, 0, vp, !begun0, kp, next0);
+                            begun0 = true;
+                        } else if (next0) {
+                            begin(0, 0, kp);
+                        }
+                        if (on1) {
+                            turn(1, 1, vp, !begun1, kp, next1);
+                            begun1 = true;
+                        } else if (next1) {
+                            begin(1, 1, kp);
+                        }
+                        release(vp);
+                        if (more) {
+                            release(kp);
+                            kp.step(2);
+                        }
                     }
                 }
-            } else {
-                // the sets' key tiles, counted from the piece's first
-                const int b0 = uniform(w.tile_t0[0] - t0), e0 = uniform(min(w.tile_t1[0] - t0, n));
-                const int b1 = uniform(w.tile_t0[1] - t0), e1 = uniform(min(w.tile_t1[1] - t0, n));
-                bool begun0 = false, begun1 = false;
-                full(kp);
-                if (b0 <= 0 && 0 < e0) begin(0, 0, kp);
-                if (b1 <= 0 && 0 < e1) begin(1, 1, kp);
-                release(kp);
-                kp.step(2);
-                for (int k = 0; k < n; ++k, vp.step(2)) {
-                    const bool more = k + 1 < n;
-                    const bool on0 = b0 <= k && k < e0, next0 = b0 <= k + 1 && k + 1 < e0;
-                    const bool on1 = b1 <= k && k < e1, next1 = b1 <= k + 1 && k + 1 < e1;
-                    full(vp);
-                    if (more) full(kp);
-                    if (on0) {
-                        turn(0, 0, vp, !begun0, kp, next0);
-                        begun0 = true;
-                    } else if (next0) {
-                        begin(0, 0, kp);
-                    }
-                    if (on1) {
-                        turn(1, 1, vp, !begun1, kp, next1);
-                        begun1 = true;
-                    } else if (next1) {
-                        begin(1, 1, kp);
-                    }
-                    release(vp);
-                    if (more) {
-                        release(kp);
-                        kp.step(2);
-                    }
+                if (elect_lane()) {
+                    tc_commit(bar(kBarQEmpty));
+                    mbar_arrive(bar(kBarPieceFree + (items & 1)));
                 }
+                __syncwarp();
             }
-            if (elect_lane()) {
-                tc_commit(bar(kBarQEmpty));
-                mbar_arrive(bar(kBarPieceFree + (items & 1)));
-            }
+            if (elect_lane()) tc_commit(bar(kBarDrain));
             __syncwarp();
+            mbar_wait(bar(kBarDrain), 0, status);
         }
-        if (elect_lane()) tc_commit(bar(kBarDrain));
-        __syncwarp();
-        mbar_wait(bar(kBarDrain), 0, status);
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---- softmax, output ----------------------------------------------------------------
         const int i = warp >> 2, r = threadIdx.x & 127;  // set; row = tensor-memory lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -594,82 +601,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 if (L::kApart && idle) s_read();
                 if (!idle) {
-                // The row's maximum, 64 columns at a time: the last 64 are read again when
-                // their turn comes, so that a thread holds 64 scores and not 128.
-                float s0[32], s1[32], mx[4];
-                tc_ld32(t_s + 64, s0);
-                tc_ld32(t_s + 96, s1);
-                tc_wait_ld<32>(s0);
-                tc_wait_ld<32>(s1);
-                if (masked) mask(s0, 2), mask(s1, 3);
+                    float s[4][32], mx[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s0[y], s1[y]);
+                    for (int k = 0; k < 4; ++k) tc_ld32(t_s + 32 * k, s[k]);
 #pragma unroll
-                for (int y = 4; y < 32; ++y) mx[y & 3] = max3(mx[y & 3], s0[y], s1[y]);
-                tc_ld32(t_s, s0);
-                tc_ld32(t_s + 32, s1);
-                tc_wait_ld<32>(s0);
-                tc_wait_ld<32>(s1);
-                if (masked) mask(s0, 0), mask(s1, 1);
+                    for (int k = 0; k < 4; ++k) tc_wait_ld<32>(s[k]);
+                    if (masked) {
 #pragma unroll
-                for (int y = 0; y < 32; ++y) mx[y & 3] = max3(mx[y & 3], s0[y], s1[y]);
-                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                if (j == j0) {
-                    m = mn;
-                } else if (__any_sync(0xFFFFFFFFu, (mn - m) * c > kLag)) {
-                    // raise the maximum of the warp's rows: O and l change units
-                    const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
-                    m = mn;
-                    l *= f;
-                    mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
-                    tc_after();
-                    const uint64_t f2 = pack2(f, f);
+                        for (int k = 0; k < 4; ++k) mask(s[k], k);
+                    }
 #pragma unroll
-                    for (int k = 0; k < HD / 16; ++k) {
-                        float o[16];
-                        tc_ld16(t_o + 16 * k, o);
-                        tc_wait_ld<16>(o);
+                    for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s[y][0], s[y][1]);
 #pragma unroll
-                        for (int y = 0; y < 16; y += 2) {
-                            const uint64_t v = fmul2(pack2(o[y], o[y + 1]), f2);
-                            o[y] = lo_of(v);
-                            o[y + 1] = hi_of(v);
+                    for (int k = 2; k < 32; k += 2)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[y][k], s[y][k + 1]);
+                    const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    if (j == j0) {
+                        m = mn;
+                    } else if (__any_sync(0xFFFFFFFFu, (mn - m) * c > kLag)) {
+                        // raise the maximum of the warp's rows: O and l change units
+                        const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
+                        m = mn;
+                        l *= f;
+                        mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
+                        tc_after();
+                        const uint64_t f2 = pack2(f, f);
+#pragma unroll
+                        for (int k = 0; k < HD / 16; ++k) {
+                            float o[16];
+                            tc_ld16(t_o + 16 * k, o);
+                            tc_wait_ld<16>(o);
+#pragma unroll
+                            for (int y = 0; y < 16; y += 2) {
+                                const uint64_t v = fmul2(pack2(o[y], o[y + 1]), f2);
+                                o[y] = lo_of(v);
+                                o[y + 1] = hi_of(v);
+                            }
+                            tc_st16(t_o + 16 * k, reinterpret_cast<uint32_t *>(o));
                         }
-                        tc_st16(t_o + 16 * k, reinterpret_cast<uint32_t *>(o));
+                        tc_wait_st();
                     }
-                    tc_wait_st();
-                }
-                const float mc = m == -INFINITY ? 0.0f : m * c;
-                const uint64_t mc2 = pack2(-mc, -mc);
-                uint64_t sum[2] = {};
-                uint32_t u[32];
-                auto weights = [&](const float *s, uint32_t *to) {
+                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const uint64_t mc2 = pack2(-mc, -mc);
+                    uint64_t sum[2] = {};
+                    uint32_t u[32];
+                    auto weights = [&](const float *s, uint32_t *to) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        const uint64_t e = ffma2(pack2(s[k], s[k + 1]), c2, mc2);
-                        const float p = ex2(lo_of(e)), q = ex2(hi_of(e));
-                        sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
-                        to[k / 2] = F16::pack(p, q);
+                        for (int k = 0; k < 32; k += 2) {
+                            const uint64_t e = ffma2(pack2(s[k], s[k + 1]), c2, mc2);
+                            const float p = ex2(lo_of(e)), q = ex2(hi_of(e));
+                            sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
+                            to[k / 2] = F16::pack(p, q);
+                        }
+                    };
+                    if (L::kApart) s_read();
+                    weights(s[0], u);
+                    weights(s[1], u + 16);
+                    if (L::kApart && npv > 0) {  // the last tile's weights have been read
+                        mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
+                        tc_after();
                     }
-                };
-                weights(s0, u);
-                tc_ld32(t_s + 64, s0);
-                weights(s1, u + 16);
-                if (L::kApart && npv > 0) {  // the last tile's weights have been read
-                    mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
-                    tc_after();
-                }
-                tc_st32(t_p, u);
-                tc_ld32(t_s + 96, s1);
-                tc_wait_ld<32>(s0);
-                tc_wait_ld<32>(s1);
-                if (L::kApart) s_read();
-                if (masked) mask(s0, 2), mask(s1, 3);
-                weights(s0, u);
-                weights(s1, u + 16);
-                tc_st32(t_p + 32, u);
-                const uint64_t t = fadd2(sum[0], sum[1]);
-                l += lo_of(t) + hi_of(t);
+                    tc_st32(t_p, u);
+                    weights(s[2], u);
+                    weights(s[3], u + 16);
+                    tc_st32(t_p + 32, u);
+                    const uint64_t t = fadd2(sum[0], sum[1]);
+                    l += lo_of(t) + hi_of(t);
                 }
                 if (dirty) {
                     // zero the rows of V that hold no position of the block (row r of the slot)
@@ -960,6 +958,8 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
     const size_t parts = (size_t)sm_count * 4, n_o = parts * 128 * p.head_dim * 4, n_s = parts * 128 * 8;
     const size_t bytes = n_o + n_s + (size_t)sm_count * 2 * sizeof(unsigned);
     ok = ok && cudaMalloc((void **)&st->mem, bytes) == cudaSuccess && cudaMemset(st->mem, 0, bytes) == cudaSuccess;
+    cudaFuncAttributes fa;  // (the kernel's shares of registers add up to its launch's)
+    ok = ok && cudaFuncGetAttributes(&fa, kernel_of(p.head_dim, p.bf16)) == cudaSuccess && fa.numRegs == 168;
     ok = ok && cudaFuncSetAttribute(kernel_of(p.head_dim, p.bf16), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     smem_of(p.head_dim)) == cudaSuccess;
     if (!ok) {
