@@ -86,7 +86,7 @@ struct Shape {
     static constexpr uint32_t kGroup8 = (uint32_t)kHalves * 1024u;  // 8 positions of a slot
     static constexpr uint32_t kQ = 0, kRing = 2 * kQTile;
     static constexpr uint32_t kBars = kRing + kSlots * kSlot;
-    static constexpr uint32_t kScratch = kBars + 304;        // joins: 2 groups x 128 x (maximum, 1 / sum)
+    static constexpr uint32_t kScratch = kBars + 304;        // a state handed from set to set, a join's flag
     static constexpr uint32_t kStart = kScratch + 2 * 128 * 8;  // the CTA's first piece, tensor-memory base
     // Tensor memory: S of the two sets in columns 0..255, O from kColO on. At 64 dims P has
     // columns of its own, so that the next S can be computed while the weights still are; at
@@ -193,31 +193,32 @@ QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
     long long *pre = reinterpret_cast<long long *>(smem + L::kRing + 8 * kMaxSeqs);  // [n_seqs]
     constexpr int kAlone = 8;  // blocks that one thread sums; longer sequences are summed by a warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    bool longer = false;
     for (int s = tid; s < a.n_seqs; s += kThreads) {
         int first, count;
         seq_tokens(a.q_start, s, a.n_tokens, first, count);
         const int kv = max(a.kv_len[s], 0), nb = seq_blocks(a.g, count);
         cnt[s] = count;
         kvs[s] = kv;
-        long long sum = 0;
-        if (nb <= kAlone)
-            for (int b = 0; b < nb; ++b) {
-                sum += item_units(block_of(a.g, count, kv, b));
-            }
-        pre[s] = sum * a.g.kv_heads;
-    }
-    __syncthreads();
-    for (int s = warp; s < a.n_seqs; s += kThreads / 32) {
-        const int nb = seq_blocks(a.g, cnt[s]);
-        if (nb <= kAlone) continue;
-        long long sum = 0;
-        for (int b = lane; b < nb; b += 32) {
-            sum += item_units(block_of(a.g, cnt[s], kvs[s], b));
+        int sum = 0;
+        if (nb <= kAlone) {
+            for (int b = 0; b < nb; ++b) sum += item_units(block_of(a.g, count, kv, b));
+        } else {
+            longer = true;
         }
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (lane == 0) pre[s] = sum * a.g.kv_heads;
+        pre[s] = (long long)sum * a.g.kv_heads;
     }
-    __syncthreads();
+    if (__syncthreads_or(longer)) {
+        for (int s = warp; s < a.n_seqs; s += kThreads / 32) {
+            const int nb = seq_blocks(a.g, cnt[s]);
+            if (nb <= kAlone) continue;
+            long long sum = 0;
+            for (int b = lane; b < nb; b += 32) sum += item_units(block_of(a.g, cnt[s], kvs[s], b));
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            if (lane == 0) pre[s] = sum * a.g.kv_heads;
+        }
+        __syncthreads();
+    }
     if (warp == 0) {
         // a scan over lanes, each with a contiguous run of sequences
         const int per = (a.n_seqs + 31) / 32, s0 = min(lane * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
@@ -809,50 +810,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 named_bar_sync(4, 256);
                 lent = false;
             }
-            __threadfence();
             named_bar_sync(1 + i, 128);
             if (r == 0) {
-                unsigned *ctr = a.counters + 2 * c_first + i;
-                const bool last = atomicAdd(ctr, 1u) == (unsigned)(c_last - c_first);
-                if (last) *ctr = 0;
+                // (the fence covers the whole set's stores, which the barrier has shown this thread;
+                // the count goes back to zero by itself)
+                __threadfence();
+                const bool last = atomicInc(a.counters + 2 * c_first + i, (unsigned)(c_last - c_first)) == (unsigned)(c_last - c_first);
                 __threadfence();
                 scratch[0].x = last ? 1.0f : 0.0f;
             }
             named_bar_sync(1 + i, 128);
             const bool last = scratch[0].x != 0.0f;
-            named_bar_sync(1 + i, 128);
+            named_bar_sync(1 + i, 128);  // (scratch is free again)
             if (!last) continue;
-            if (r < rows) {
-                float M = -INFINITY, S = 0.0f;
-                for (int cta = c_first; cta <= c_last; cta += 8) {
-                    float2 ml[8];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) ml[y] = cta + y <= c_last ? __ldcg(a.part_ml + part_of(cta + y) * 128 + r) : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const float mn = fmaxf(M, ml[y].x);
-                        if (ml[y].y > 0.0f) S = (S > 0.0f ? S * ex2(M - mn) : 0.0f) + ml[y].y * ex2(ml[y].x - mn);
-                        M = mn;
-                    }
-                }
-                scratch[r] = make_float2(M, S > 0.0f ? 1.0f / S : 0.0f);
-                if (a.lse) a.lse[(first_token + r_token) * a.n_heads + first_head + r_head] = S > 0.0f ? (M + log2f(S)) * ln2 : -INFINITY;
-            }
-            named_bar_sync(1 + i, 128);
             // thread by thread eight columns of a row; many loads in flight: several such, or several parts
             const int pieces = rows * (HD / 8);
             auto join = [&](auto items_at_once, auto parts_at_once) {
                 constexpr int U = decltype(items_at_once)::value, P = decltype(parts_at_once)::value;
                 for (int k = r; k < pieces; k += 128 * U) {
-                    float acc[U][8] = {};
+                    float acc[U][8] = {}, M[U], S[U] = {};
                     int row[U], col[U];
-                    float M[U];
 #pragma unroll
                     for (int z = 0; z < U; ++z) {
                         const int x = min(k + 128 * z, pieces - 1);
                         col[z] = x / rows;
                         row[z] = x - col[z] * rows;
-                        M[z] = scratch[row[z]].x;
+                        M[z] = -INFINITY;
                     }
                     for (int cta = c_first; cta <= c_last; cta += P) {
                         float2 p[P][U];
@@ -872,24 +855,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int z = 0; z < U; ++z) {
                                 if (cta + y > c_last || !(p[y][z].y > 0.0f)) continue;
-                                const float f = ex2(p[y][z].x - M[z]);
+                                const float mn = fmaxf(M[z], p[y][z].x), g = ex2(M[z] - mn), f = ex2(p[y][z].x - mn);
+                                M[z] = mn;
+                                S[z] = S[z] * g + p[y][z].y * f;
                                 const float e[8] = {v[y][z][0].x, v[y][z][0].y, v[y][z][0].z, v[y][z][0].w,
                                                     v[y][z][1].x, v[y][z][1].y, v[y][z][1].z, v[y][z][1].w};
 #pragma unroll
-                                for (int t = 0; t < 8; ++t) acc[z][t] = fmaf(f, e[t], acc[z][t]);
+                                for (int t = 0; t < 8; ++t) acc[z][t] = fmaf(f, e[t], acc[z][t] * g);
                             }
                     }
 #pragma unroll
                     for (int z = 0; z < U; ++z) {
                         if (k + 128 * z >= pieces) continue;
                         const int64_t token = first_token + row[z] / a.g.group, head = first_head + row[z] % a.g.group;
-                        put8(token * a.out_stride + head * HD + 8 * col[z], acc[z], scratch[row[z]].y);
+                        put8(token * a.out_stride + head * HD + 8 * col[z], acc[z], S[z] > 0.0f ? 1.0f / S[z] : 0.0f);
+                        if (a.lse && col[z] == 0) a.lse[token * a.n_heads + head] = S[z] > 0.0f ? (M[z] + log2f(S[z])) * ln2 : -INFINITY;
                     }
                 }
             };
             if (pieces > 256) join(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
             else join(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
-            named_bar_sync(1 + i, 128);  // (scratch is free again)
         }
         if (lent) named_bar_sync(4, 256);
     }

@@ -44,7 +44,7 @@ QDQ_PLAN_FN int plan_min(int a, int b) { return a < b ? a : b; }
 QDQ_PLAN_FN int plan_max(int a, int b) { return a > b ? a : b; }
 QDQ_PLAN_FN int seq_blocks(const AttendGeometry &g, int count) {
     const int b = 2 * g.tokens;
-    return (count + b - 1) / b;
+    return count <= b ? (count > 0 ? 1 : 0) : (count + b - 1) / b;
 }
 
 // Positions first..last-1 of tokens i0..i1-1, the first of which is at position p0.
@@ -82,8 +82,14 @@ QDQ_PLAN_FN bool block_alternates(const AttendGeometry &g, const AttendBlock &b)
 }
 
 // CTA c of n takes units range_start(c) .. range_start(c + 1) - 1 of `total`.
-QDQ_PLAN_FN int64_t range_start(int64_t total, int n, int c) { return total * c / n; }
-QDQ_PLAN_FN int range_owner(int64_t total, int n, int64_t x) { return (int)(((x + 1) * n - 1) / total); }
+// (Small totals divide in 32 bits: a 64-bit division is some 500 clocks of a kernel's start.)
+QDQ_PLAN_FN int64_t range_start(int64_t total, int n, int c) {
+    return total < (1 << 22) && n < 512 ? (int64_t)((uint32_t)total * (uint32_t)c / (uint32_t)n) : total * c / n;
+}
+QDQ_PLAN_FN int range_owner(int64_t total, int n, int64_t x) {
+    return total < (1 << 22) && n < 512 ? (int)((((uint32_t)x + 1) * (uint32_t)n - 1) / (uint32_t)total)
+                                        : (int)(((x + 1) * n - 1) / total);
+}
 QDQ_PLAN_FN int item_units(const AttendBlock &b) { return kItemUnits + b.t1 - b.t0; }
 // Of an item whose units begin at `item`, the key tiles [first, last) of the range [x, end).
 QDQ_PLAN_FN void piece_of(const AttendBlock &b, int64_t item, int64_t x, int64_t end, int &first, int &last) {
