@@ -787,6 +787,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c_first = w.c_first, c_last = w.c_last;
             done();
             auto part_of = [&](int cta) { return (cta * 2 + (cta == c_first ? 1 : 0)) * 2 + i; };
+            // One more part onto a joined state, in CTA order on every path: g and f are the factors
+            // of what is there and of what comes.
+            auto onto = [](float2 p, float &M, float &S, float &g, float &f) {
+                const float mn = fmaxf(M, p.x);
+                g = M == -INFINITY ? 0.0f : ex2(M - mn);
+                f = p.y > 0.0f ? ex2(p.x - mn) : 0.0f;
+                M = mn;
+                S = fmaf(S, g, p.y * f);
+            };
+            if (lent) {
+                named_bar_sync(4, 256);
+                lent = false;
+            }
+            // Many rows, and the other parts are all written: this one is joined as it is, a thread
+            // its row (writing it and reading all back costs some 15 000 clocks at 128 rows).
+            unsigned *counter = a.counters + 2 * c_first + i;
+            const int pieces = rows * (HD / 8);
+            if (pieces > 256) {
+                if (r == 0) {
+                    const bool rest = ld_acquire_gpu(counter) == (unsigned)(c_last - c_first);
+                    if (rest) *counter = 0;
+                    scratch[0].x = rest ? 1.0f : 0.0f;
+                }
+                named_bar_sync(1 + i, 128);
+                const bool rest = scratch[0].x != 0.0f;
+                named_bar_sync(1 + i, 128);
+                if (rest) {
+                    const int row = min(r, rows - 1);
+                    const int64_t token = first_token + r_token, head = first_head + r_head;
+                    float M, S;
+#pragma unroll 1
+                    for (int k = 0; k < HD / 32; ++k) {
+                        float acc[32] = {};
+                        M = -INFINITY, S = 0.0f;
+                        for (int cta = c_first; cta <= c_last; ++cta) {
+                            float o[32], g, f;
+                            float2 ml = make_float2(mc, l);
+                            if (cta == (int)blockIdx.x) {
+                                read(k, o);
+                            } else {
+                                ml = __ldcg(a.part_ml + part_of(cta) * 128 + row);
+                                const float4 *src = reinterpret_cast<const float4 *>(a.part_o) + ((int64_t)part_of(cta) * (HD / 4) + 8 * k) * 128 + row;
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) {
+                                    const float4 v = __ldcg(src + y * 128);
+                                    o[4 * y] = v.x, o[4 * y + 1] = v.y, o[4 * y + 2] = v.z, o[4 * y + 3] = v.w;
+                                }
+                            }
+                            onto(ml, M, S, g, f);
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) acc[y] = fmaf(f, f > 0.0f ? o[y] : 0.0f, acc[y] * g);
+                        }
+                        if (r < rows) {
+                            const float inv = S > 0.0f ? 1.0f / S : 0.0f;
+#pragma unroll
+                            for (int y = 0; y < 32; y += 8) put8(token * a.out_stride + head * HD + 32 * k + y, acc + y, inv);
+                        }
+                    }
+                    read_done();
+                    if (a.lse && r < rows) a.lse[token * a.n_heads + head] = S > 0.0f ? (M + log2f(S)) * ln2 : -INFINITY;
+                    continue;
+                }
+            }
             {
                 const int part = part_of(blockIdx.x);
                 float4 *po = reinterpret_cast<float4 *>(a.part_o) + (int64_t)part * (HD / 4) * 128;
@@ -805,17 +868,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 read_done();
                 if (r < rows) __stcg(a.part_ml + part * 128 + r, make_float2(mc, l));
             }
-            // the last of the item's parts joins them all, in order
-            if (lent) {
-                named_bar_sync(4, 256);
-                lent = false;
-            }
+            // the last of the item's parts joins them all
             named_bar_sync(1 + i, 128);
             if (r == 0) {
                 // (the fence covers the whole set's stores, which the barrier has shown this thread;
                 // the count goes back to zero by itself)
                 __threadfence();
-                const bool last = atomicInc(a.counters + 2 * c_first + i, (unsigned)(c_last - c_first)) == (unsigned)(c_last - c_first);
+                const bool last = atomicInc(counter, (unsigned)(c_last - c_first)) == (unsigned)(c_last - c_first);
                 __threadfence();
                 scratch[0].x = last ? 1.0f : 0.0f;
             }
@@ -824,7 +883,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync(1 + i, 128);  // (scratch is free again)
             if (!last) continue;
             // thread by thread eight columns of a row; many loads in flight: several such, or several parts
-            const int pieces = rows * (HD / 8);
             auto join = [&](auto items_at_once, auto parts_at_once) {
                 constexpr int U = decltype(items_at_once)::value, P = decltype(parts_at_once)::value;
                 for (int k = r; k < pieces; k += 128 * U) {
@@ -854,14 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int y = 0; y < P; ++y)
 #pragma unroll
                             for (int z = 0; z < U; ++z) {
-                                if (cta + y > c_last || !(p[y][z].y > 0.0f)) continue;
-                                const float mn = fmaxf(M[z], p[y][z].x), g = ex2(M[z] - mn), f = ex2(p[y][z].x - mn);
-                                M[z] = mn;
-                                S[z] = S[z] * g + p[y][z].y * f;
+                                if (cta + y > c_last) continue;
+                                float g, f;
+                                onto(p[y][z], M[z], S[z], g, f);
                                 const float e[8] = {v[y][z][0].x, v[y][z][0].y, v[y][z][0].z, v[y][z][0].w,
                                                     v[y][z][1].x, v[y][z][1].y, v[y][z][1].z, v[y][z][1].w};
 #pragma unroll
-                                for (int t = 0; t < 8; ++t) acc[z][t] = fmaf(f, e[t], acc[z][t] * g);
+                                for (int t = 0; t < 8; ++t) acc[z][t] = fmaf(f, f > 0.0f ? e[t] : 0.0f, acc[z][t] * g);
                             }
                     }
 #pragma unroll
