@@ -60,8 +60,9 @@
  *     failures return QDQ_ERR_CUDA. A device-side failure (a bounded wait that
  *     ran out) is recorded in a per-device status word, read back by
  *     qdq_get_device_status(). Nothing aborts, traps or exits.
- *   - The caller owns every buffer. Besides plans (below), the library keeps no
- *     device allocations: only a status word in module memory per device.
+ *   - The caller owns every buffer. Besides plans, models and paged caches (below),
+ *     the library keeps no device allocations: only a status word in module memory
+ *     per device.
  *   - Calls on different streams may run concurrently. Only sm_103 (GB300)
  *     devices are accepted; others give QDQ_ERR_DEVICE.
  */
@@ -330,7 +331,8 @@ void qdq_llama_destroy(qdq_llama *model);
  * page holds which positions is the caller's to decide: position j of a
  * sequence lives in row j % page_size of page page_table[seq][j / page_size].
  * A handle keeps the geometry, the rotation's frequency table and the attention's
- * workspace (all device memory it needs: the calls allocate nothing).
+ * workspace (all device memory it needs, 1024 bytes x SMs x head_dim x 2 and a little:
+ * 40 MB at 128 dims; the calls allocate nothing).
  *
  * A step's batch (all arrays int32 on the device, 4-byte aligned, read when the
  * kernels run, so a captured graph replays with their new contents):
@@ -362,8 +364,10 @@ typedef struct qdq_paged_batch {
     const int32_t *q_start, *kv_len, *page_table;
 } qdq_paged_batch;
 typedef struct qdq_paged qdq_paged;
-/* The pools must outlive the handle. Calls of one handle must not overlap on the
- * GPU (they share the workspace); use one handle per stream otherwise. */
+/* The pools must outlive the handle. Attention calls of one handle must not overlap on
+ * the GPU (they share the workspace); use one handle per stream otherwise. If
+ * qdq_get_device_status() reports QDQ_ERR_TIMEOUT after one, destroy the handle and
+ * create another before the next. */
 int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, qdq_paged **out);
 void qdq_paged_destroy(qdq_paged *cache);
 
