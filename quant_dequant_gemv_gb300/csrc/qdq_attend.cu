@@ -723,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 o = scratch[128 + r];
                 named_bar_arrive(4, 256);
                 const float M = fmaxf(mc, o.x);
-                f0 = l > 0.0f ? ex2(mc - M) : 0.0f;
-                f1 = o.y > 0.0f ? ex2(o.x - M) : 0.0f;
+                f0 = l != 0.0f ? ex2(mc - M) : 0.0f;
+                f1 = o.y != 0.0f ? ex2(o.x - M) : 0.0f;
                 l = l * f0 + o.y * f1;
                 mc = M;
             }
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const float ln2 = 0.6931471805599453f;
             if (w.whole) {
-                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                const float inv = l != 0.0f ? 1.0f / l : 0.0f;
                 const int64_t token = first_token + r_token, head = first_head + r_head;
                 const int64_t at = token * a.out_stride + head * HD;
                 if (!idle) {
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (r < rows) {
 #pragma unroll
                             for (int y = 0; y < 32; y += 8) {
-                                if (!(l > 0.0f)) {
+                                if (l == 0.0f) {
 #pragma unroll
                                     for (int z = 0; z < 8; ++z) o[y + z] = 0.0f;  // (nothing to attend to)
                                 }
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 read_done();
-                if (a.lse && r < rows) a.lse[token * a.n_heads + head] = l > 0.0f ? (mc + log2f(l)) * ln2 : -INFINITY;
+                if (a.lse && r < rows) a.lse[token * a.n_heads + head] = l != 0.0f ? (mc + log2f(l)) * ln2 : -INFINITY;
                 done();
                 continue;
             }
@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto onto = [](float2 p, float &M, float &S, float &g, float &f) {
                 const float mn = fmaxf(M, p.x);
                 g = M == -INFINITY ? 0.0f : ex2(M - mn);
-                f = p.y > 0.0f ? ex2(p.x - mn) : 0.0f;
+                f = p.y != 0.0f ? ex2(p.x - mn) : 0.0f;  // (a sum that is no number stays none)
                 M = mn;
                 S = fmaf(S, g, p.y * f);
             };
@@ -849,13 +849,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int y = 0; y < 32; ++y) acc[y] = fmaf(f, f > 0.0f ? o[y] : 0.0f, acc[y] * g);
                         }
                         if (r < rows) {
-                            const float inv = S > 0.0f ? 1.0f / S : 0.0f;
+                            const float inv = S != 0.0f ? 1.0f / S : 0.0f;
 #pragma unroll
                             for (int y = 0; y < 32; y += 8) put8(token * a.out_stride + head * HD + 32 * k + y, acc + y, inv);
                         }
                     }
                     read_done();
-                    if (a.lse && r < rows) a.lse[token * a.n_heads + head] = S > 0.0f ? (M + log2f(S)) * ln2 : -INFINITY;
+                    if (a.lse && r < rows) a.lse[token * a.n_heads + head] = S != 0.0f ? (M + log2f(S)) * ln2 : -INFINITY;
                     continue;
                 }
             }
@@ -934,8 +934,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int z = 0; z < U; ++z) {
                         if (k + 128 * z >= pieces) continue;
                         const int64_t token = first_token + row[z] / a.g.group, head = first_head + row[z] % a.g.group;
-                        put8(token * a.out_stride + head * HD + 8 * col[z], acc[z], S[z] > 0.0f ? 1.0f / S[z] : 0.0f);
-                        if (a.lse && col[z] == 0) a.lse[token * a.n_heads + head] = S[z] > 0.0f ? (M[z] + log2f(S[z])) * ln2 : -INFINITY;
+                        put8(token * a.out_stride + head * HD + 8 * col[z], acc[z], S[z] != 0.0f ? 1.0f / S[z] : 0.0f);
+                        if (a.lse && col[z] == 0) a.lse[token * a.n_heads + head] = S[z] != 0.0f ? (M[z] + log2f(S[z])) * ln2 : -INFINITY;
                     }
                 }
             };

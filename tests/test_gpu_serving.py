@@ -307,6 +307,71 @@ def test_attention_is_repeatable_and_reads_its_batch_when_it_runs(qdq):
     assert qdq.get_device_status() == 0
 
 
+@pytest.mark.parametrize("lens", [[(1, 0)], [(1, 700), (3, 5)], [(300, 40)]])
+def test_attention_keeps_a_query_that_is_no_number_to_itself(qdq, lens):
+    b = make(qdq, lens, 8, 2, 128, 32, "bf16", seed=5)
+    fill_held(b)
+    T = b["tokens"]
+    q = torch.from_numpy(b["rng"].standard_normal((T, 8 * 128))).bfloat16().cuda()
+    out, clean = (torch.zeros(T, 8 * 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse = torch.zeros(T, 8, device="cuda")
+    b["cache"].attention(0, b["batch"], q, clean)
+    q[T - 1, 3 * 128 + 7] = float("nan")
+    b["cache"].attention(0, b["batch"], q, out, lse=lse)
+    got = out.view(T, 8, 128)
+    assert got[T - 1, 3].isnan().all() and lse[T - 1, 3].isnan()
+    got[T - 1, 3] = clean.view(T, 8, 128)[T - 1, 3]
+    assert torch.equal(out, clean)
+
+
+def test_attention_without_any_page(qdq):
+    b = make(qdq, [(3, 0), (1, 9)], 4, 2, 64, 16, "f16")
+    b["batch"] = qdq.PagedBatch(torch.from_numpy(b["q_start"]).cuda(), torch.from_numpy(b["kv_len"]).cuda(),
+                                torch.zeros(2, 0, dtype=torch.int32, device="cuda"), 4)
+    q = torch.ones(4, 256, dtype=torch.float16, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((4, 4), 7.0, device="cuda")
+    b["cache"].attention(0, b["batch"], q, out, lse=lse)
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    k = torch.ones(4, 128, dtype=torch.float16, device="cuda")
+    b["cache"].append(0, b["batch"], q, k, k, out)
+    assert out.isfinite().all() and b["pools"].isnan().all()
+
+
+def test_a_step_in_a_graph(qdq):
+    """Append, attention and sampling captured together, replayed on other tokens and lengths."""
+    b = make(qdq, [(9, 0), (1, 70)], 4, 2, 64, 16, "f16", seed=21, spare=9)
+    fill_held(b)
+    T, V = b["tokens"], 5000
+    rng = np.random.default_rng(1)
+    new = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).cuda()
+    q, k, v, w = new(T, 256), new(T, 128), new(T, 128), new(256, V)
+    q16, att = (torch.zeros(T, 256, dtype=t, device="cuda") for t in (torch.float16, torch.float32))
+    logits, u = torch.zeros(T, V, device="cuda"), torch.full((T,), 0.6, device="cuda")
+    top_p = torch.full((T,), 0.8, device="cuda")
+    tokens = [torch.zeros(T, dtype=torch.int64, device="cuda") for _ in range(2)]
+    torch.mm(att, w, out=logits)  # (the matrix product's own first call)
+
+    def step(out):
+        b["cache"].append(0, b["batch"], q, k, v, q16)
+        b["cache"].attention(0, b["batch"], q16, att)
+        torch.mm(att, w, out=logits)
+        qdq.sample(logits, u, out, top_p=top_p)
+
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        step(tokens[0])
+    for n in range(3):
+        q.normal_()
+        k.normal_()
+        b["batch"]._keep[1][1] = 71 - 9 * n
+        g.replay()
+        torch.cuda.synchronize()
+        step(tokens[1])
+        torch.cuda.synchronize()
+        assert torch.equal(tokens[0], tokens[1]) and qdq.get_device_status() == 0
+
+
 def test_append_then_attention_on_a_side_stream(qdq):
     b = make(qdq, [(12, 0), (1, 0)], 4, 2, 64, 16, "f16", seed=12)
     T, H, G, D = 13, 4, 2, 64
