@@ -396,7 +396,9 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * rounded to the pools' type before they meet v (as its matrix product takes
  * them), so an fp32 out is accurate to about that rounding too. A token with
  * nothing to attend to gets a zero row and lse = -inf. Keys and values of
- * positions outside a sequence's range are never used, whatever they hold.
+ * positions outside a sequence's range are never used, whatever they hold; values
+ * inside it are taken to be finite (a position that only later tokens of a chunk
+ * attend to has weight zero for the earlier ones, and 0 x inf is no number).
  * One launch; results do not depend on timing (no floating-point atomics). */
 int qdq_paged_attention(qdq_paged *cache, int layer, const qdq_paged_batch *batch, const void *q, int64_t q_stride,
                         int out_type, void *out, int64_t out_stride, float scale, int window, float *lse,

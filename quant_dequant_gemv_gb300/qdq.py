@@ -157,9 +157,9 @@ def _stream(stream) -> int:
     if stream is None:
         import torch
         # torch.cuda.current_stream().cuda_stream without the Stream object (3 us a call)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and device is not None and torch.cuda.is_initialized():
+            return raw(device())
         return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
@@ -350,26 +350,38 @@ class Llama:
             pass
 
 
+_float_types: dict = {}
+
+
 def _float_type(t) -> int:
     """The qdq_float_type of a torch tensor (0, which every call refuses, for another type)."""
-    import torch
-    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}.get(t.dtype, 0)
+    if not _float_types:
+        import torch
+        _float_types.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    return _float_types.get(t.dtype, 0)
 
 
-def _rows_of(t, what: str) -> int:
-    """The row stride of a [rows, n] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.stride(1) != 1:
+def _rows_of(t, what: str) -> tuple[int, int, int]:
+    """Rows, width and row stride of a [rows, n] tensor whose rows are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or stride[1] != 1:
         raise ValueError(f"{what}: a 2-D tensor with contiguous rows is needed")
-    return t.stride(0)
+    return shape[0], shape[1], stride[0]
+
+
+_names: dict = {}  # dtype -> its name
 
 
 def _vector(t, n: int, dtype: str, what: str) -> int:
     """Address of a contiguous tensor of at least n elements of `dtype`; 0 for None."""
     if t is None:
         return 0
-    if str(t.dtype) != "torch." + dtype or not t.is_contiguous() or t.numel() < n:
+    name = _names.get(t.dtype)
+    if name is None:
+        name = _names[t.dtype] = str(t.dtype).removeprefix("torch.")
+    if name != dtype or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{what}: a contiguous {dtype} tensor of {n} elements is needed")
-    return int(t.data_ptr())
+    return t.data_ptr()
 
 
 class PagedBatch:
@@ -412,8 +424,8 @@ class PagedCache:
         self._h = h
 
     def _width(self, t, n_tokens: int, heads: int, what: str) -> int:
-        stride = _rows_of(t, what)
-        if t.shape[0] < n_tokens or t.shape[1] != heads * self.head_dim:
+        rows, width, stride = _rows_of(t, what)
+        if rows < n_tokens or width != heads * self.head_dim:
             raise ValueError(f"{what}: {n_tokens} rows of {heads * self.head_dim} are needed")
         return stride
 
@@ -466,7 +478,7 @@ def sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=No
     """The next token of each row of logits from the random numbers u (qdq_sample). logits:
     [rows, vocab] fp32, fp16 or bf16; per row u, temperature, top_p, min_p fp32, top_k int32
     (None switches a filter off); tokens int64, logprobs fp32."""
-    stride, (rows, vocab) = _rows_of(logits, "logits"), logits.shape
+    rows, vocab, stride = _rows_of(logits, "logits")
     _check(lib().qdq_sample(_float_type(logits), logits.data_ptr(), stride, rows, vocab,
                             _vector(temperature, rows, "float32", "temperature"),
                             _vector(top_k, rows, "int32", "top_k"), _vector(top_p, rows, "float32", "top_p"),
