@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *status = &g_attend_status;
     Start *start = reinterpret_cast<Start *>(smem + L::kStart);
     auto bar = [&](int i) { return sb + L::kBars + 8u * i; };
+    follow_last_kernel();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kSlots; ++i) {
@@ -1061,8 +1062,8 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, q_row};
     const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)k.g.tokens};
     if (!encode(&q_map, p.bf16, 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
-    kernel_of(p.head_dim, p.bf16)<<<st->ctas, kThreads, smem_of(p.head_dim), stream>>>(k, q_map, st->k_map, st->v_map);
-    return cudaGetLastError() == cudaSuccess ? QDQ_OK : QDQ_ERR_CUDA;
+    return launch_following(kernel_of(p.head_dim, p.bf16), st->ctas, kThreads, smem_of(p.head_dim), 1, stream, k, q_map,
+                            st->k_map, st->v_map);
 }
 
 int take_status_attend() {

@@ -108,6 +108,32 @@ struct RelaxedCaptureScope {
     RelaxedCaptureScope &operator=(const RelaxedCaptureScope &) = delete;
 };
 
+// Launches a kernel that begins with follow_last_kernel() (qdq_paged.cuh), in clusters of
+// `cluster` CTAs.
+template <typename... P, typename... A>
+int launch_following(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                     cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return QDQ_ERR_CUDA;
+    }
+    return QDQ_OK;
+}
+
 constexpr int kMaxPlanDescs = 192;
 constexpr int kMaxPlanLevels = 128;
 constexpr int kMaxGroupDescs = 8;

@@ -39,6 +39,7 @@ struct AppendArgs {
 template <typename TI, typename TC, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
     constexpr int G = D / 8, RW = 32 / G;  // lanes per row, rows per warp step
+    follow_last_kernel();
     const int lane = threadIdx.x & 31, u = lane % G, sub = lane / G;
     const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int t = (int)(unit / a.splits);
@@ -149,9 +150,9 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
 }
 
 template <typename TI, typename TC, int D>
-void launch_append_typed(const AppendArgs &a, bool interleaved, unsigned grid, cudaStream_t stream) {
-    if (interleaved) append_kernel<TI, TC, D, true><<<grid, 128, 0, stream>>>(a);
-    else append_kernel<TI, TC, D, false><<<grid, 128, 0, stream>>>(a);
+int launch_append_typed(const AppendArgs &a, bool interleaved, unsigned grid, cudaStream_t stream) {
+    return launch_following(interleaved ? append_kernel<TI, TC, D, true> : append_kernel<TI, TC, D, false>, grid, 128, 0,
+                            1, stream, a);
 }
 
 int launch_append(AppendArgs a, bool in_f32, bool bf16, bool interleaved, int head_dim, cudaStream_t stream,
@@ -172,10 +173,9 @@ int launch_append(AppendArgs a, bool in_f32, bool bf16, bool interleaved, int he
 #define QDQ_APPEND(TI, TC)                                                          \
     (head_dim == 64 ? launch_append_typed<TI, TC, 64>(a, interleaved, g, stream)    \
                     : launch_append_typed<TI, TC, 128>(a, interleaved, g, stream))
-    if (in_f32) bf16 ? QDQ_APPEND(float, __nv_bfloat16) : QDQ_APPEND(float, __half);
-    else bf16 ? QDQ_APPEND(__nv_bfloat16, __nv_bfloat16) : QDQ_APPEND(__half, __half);
+    if (in_f32) return bf16 ? QDQ_APPEND(float, __nv_bfloat16) : QDQ_APPEND(float, __half);
+    return bf16 ? QDQ_APPEND(__nv_bfloat16, __nv_bfloat16) : QDQ_APPEND(__half, __half);
 #undef QDQ_APPEND
-    return cudaGetLastError() == cudaSuccess ? QDQ_OK : QDQ_ERR_CUDA;
 }
 
 }  // namespace

@@ -13,6 +13,15 @@ namespace qdq {
 
 constexpr int kMaxSeqs = 1024;
 
+// The serving kernels are launched with programmatic stream serialisation: the CTAs of a
+// call may be placed while the last kernel of the stream still runs, wait here until it
+// has completed and its writes are visible, and let the next call's be placed in turn.
+// First thing in a kernel, before any access to memory that another kernel may write.
+QDQ_DEV void follow_last_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // The new tokens of sequence s, inside [0, n_tokens].
 QDQ_DEV void seq_tokens(const int32_t *q_start, int s, int n_tokens, int &first, int &count) {
     const int a = min(max(q_start[s], 0), n_tokens), b = min(max(q_start[s + 1], 0), n_tokens);

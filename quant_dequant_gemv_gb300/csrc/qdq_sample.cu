@@ -681,6 +681,7 @@ struct Row {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) char smem[];
+    follow_last_kernel();
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     Row r(sh, cluster_rank(), cluster_size());
     const uint32_t ctas = r.ctas, rank = r.rank;
@@ -831,23 +832,7 @@ int launch_sample(SampleArgs a, int sm_count, cudaStream_t stream) {
             attr_set[dev] = true;
         }
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.rows * c, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)c;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) != cudaSuccess) {
-        cudaGetLastError();
-        return QDQ_ERR_CUDA;
-    }
-    return QDQ_OK;
+    return launch_following(sample_kernel<T>, (unsigned)a.rows * c, kThreads, smem, c, stream, a);
 }
 
 }  // namespace
