@@ -4,8 +4,8 @@
 //   o = sum_j p_j v_j / l,  p_j = 2^(c s_j - m),  l = sum_j p_j,  c = scale * log2(e)
 // in one pass over the keys with a running maximum m and sum l (fp32). For a tile of 128
 // rows (tokens x the query heads that share a kv head) and a tile of 128 positions,
-// S = Q K^T goes to tensor memory, 128 threads take a row each, write P (16-bit) over S,
-// and O += P V accumulates in tensor memory. The maximum that p is taken against lags
+// S = Q K^T goes to tensor memory, 128 threads take a row each, write P (16-bit) back (over
+// S at 128 dims), and O += P V accumulates in tensor memory. The maximum that p is taken against lags
 // the true one by up to 2^8, so that O is rescaled a few times a row and not every tile;
 // the factor cancels in o and in l.
 //
@@ -20,14 +20,15 @@
 // of 8 x 128 bytes, which is the operand layout for K (K-major) and for V (N-major)).
 // A page that lies outside the block's positions is not read.
 //
-// The key tiles of all items are dealt to the CTAs in equal contiguous ranges
+// The work of all items is dealt to the CTAs in equal contiguous ranges
 // (qdq_attend_plan.h); the parts of an item that several CTAs hold are written to a
 // workspace, and the CTA that finishes last (an integer counter) joins them in CTA
 // order, so the result does not depend on which one that was. No CTA waits for another.
+// The copying warp walks the range and publishes each piece; the rest follow it.
 //
 // What bounds it, as measured (GB300; 32 query and 8 kv heads of 128 unless said):
-// * single tokens: HBM. 64 sequences of 30 to 8192 positions 191 us = 6.27 TB/s, 92 % of the
-//   copy rate; one sequence of 131001 positions 91 us, 87 % (the rest is the start, the
+// * single tokens: HBM. 64 sequences of 30 to 8192 positions 184 us = 6.52 TB/s, 96 % of the
+//   copy rate; one sequence of 131001 positions 89 us, 89 % (the rest is the start, the
 //   first tile's latency and the join, about 10 us, which is all of a 520-position call).
 // * prompts: the chain S -> softmax -> P V -> next S of each set, about 3000 clocks a tile
 //   where the matrix instructions of both sets need 2048: 8191 tokens 402 us = 1.37 PFLOP/s,
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the lane's run of positions: its first group of 8 rows in the pools
                     const int in_page = ((t0 + j) * kTileN + (lane << run_shift)) & ((1 << a.page_shift) - 1);
                     const int row8 = a.row8_layer + (int)((((int64_t)here << a.page_shift) + in_page) >> 3);
-    #pragma unroll
+#pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++seq_no) {
                         const int slot = seq_no % L::kSlots;
                         mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // S_i = Q K^T with rows of tile qi (in an elected lane)
             auto qk = [&](int i, int qi, const Place &p) {
                 const uint32_t kd = k_lo + (uint32_t)p.slot * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
-    #pragma unroll
+#pragma unroll
                 for (int k = 0; k < HD / 16; ++k)
                     tc_mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
                               desc64(kd + (k / 4) * 64u + (k % 4) * 2u, kv_hi), a.idesc_qk, k > 0);
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 np ^= 1u << i;
                 tc_after();
                 if (elect_lane()) {
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < kTileN / 16; ++k)
                         tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColP + L::kPitchP * i + 8u * k,
                                   desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);

@@ -34,7 +34,7 @@ struct AppendArgs {
 // that wraps (the frequency is kept in units of 2^-64 turn), so its error is 2^-65
 // turn per position whatever the position; the fraction then goes through sincospi.
 // Bound by HBM: 274 MB (7436 tokens of 32 + 2 x 8 heads of 128, fp32 in, bf16 out) in
-// 53 us = 5.15 TB/s, 76 % of the copy rate with issue slots half used; a few tokens take 2.8 us,
+// 51 us = 5.34 TB/s, 79 % of the copy rate with issue slots half used; a few tokens take 2.6 us,
 // which is the launch and three dependent loads.
 template <typename TI, typename TC, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {

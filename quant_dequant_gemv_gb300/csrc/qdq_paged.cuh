@@ -56,7 +56,6 @@ struct Float16<__half> {
         return d;
     }
     static QDQ_DEV float2 unpack(uint32_t v) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); }
-    static QDQ_DEV __half one(float v) { return __float2half_rn(v); }
 };
 template <>
 struct Float16<__nv_bfloat16> {
@@ -66,7 +65,6 @@ struct Float16<__nv_bfloat16> {
         return d;
     }
     static QDQ_DEV float2 unpack(uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)); }
-    static QDQ_DEV __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
 };
 
 // Four consecutive values, read once, as floats.
