@@ -611,7 +611,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kBarSFree + i));
                 };
-                if (L::kApart && idle) s_read();
+                const auto p_free = [&] {  // the last tile's weights have been read
+                    if (npv == 0) return;
+                    mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
+                    tc_after();
+                };
+                if (L::kApart && idle) {
+                    // (S comes ahead of the last tile's P V, so a warp without rows has to wait here
+                    // too, or its arrival would count for the last tile's weights)
+                    s_read();
+                    p_free();
+                }
                 if (!idle) {
                     float s[4][32], mx[4];
 #pragma unroll
@@ -670,10 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (L::kApart) s_read();
                     weights(s[0], u);
                     weights(s[1], u + 16);
-                    if (L::kApart && npv > 0) {  // the last tile's weights have been read
-                        mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
-                        tc_after();
-                    }
+                    if (L::kApart) p_free();
                     tc_st32(t_p, u);
                     weights(s[2], u);
                     weights(s[3], u + 16);

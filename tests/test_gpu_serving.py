@@ -307,6 +307,24 @@ def test_attention_is_repeatable_and_reads_its_batch_when_it_runs(qdq):
     assert qdq.get_device_status() == 0
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,window", [([(23, 1200), (55, 900)], 1000), ([(19, 3000), (40, 700), (3, 400)], 0)])
+def test_attention_partly_filled_tiles_are_repeatable(qdq, dim, lens, window):
+    """Tiles of rows in which whole warps have none: many passes, each with the oracle's result."""
+    b = make(qdq, lens, 32, 4, dim, 16, "f16", seed=17)
+    b["pools"].copy_(torch.randn(b["pools"].shape, device="cuda"))
+    first = check_attention(qdq, b, window=window)
+    q = torch.from_numpy(b["rng"].standard_normal((b["tokens"], 32 * dim))).half().cuda()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    outs = [torch.zeros_like(first) for _ in range(2)]
+    b["cache"].attention(0, b["batch"], q, outs[0], window=window)
+    for _ in range(400):
+        outs[1].zero_()
+        b["cache"].attention(0, b["batch"], q, outs[1], window=window)
+        wrong += (outs[0] != outs[1]).any()
+    assert int(wrong) == 0 and qdq.get_device_status() == 0
+
+
 @pytest.mark.parametrize("lens", [[(1, 0)], [(1, 700), (3, 5)], [(300, 40)]])
 def test_attention_keeps_a_query_that_is_no_number_to_itself(qdq, lens):
     b = make(qdq, lens, 8, 2, 128, 32, "bf16", seed=5)
