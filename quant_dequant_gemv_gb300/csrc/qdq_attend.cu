@@ -576,6 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             const bool idle = (warp & 3) * 32 >= rows;  // no row of the warp's lanes is one
+            // (lanes past the last row hold the next sequence's queries or what was in the tile: they
+            // have no say in when the maximum is raised)
+            const float lag = r < rows ? kLag : INFINITY;
             const int step = alt ? 2 : 1;
             const int j0 = alt ? t0 + i : max(t0, w.tile_t0[qi]);
             const int j1 = alt ? t0 + n : min(t0 + n, w.tile_t1[qi]);
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                     if (j == j0) {
                         m = mn;
-                    } else if (__any_sync(0xFFFFFFFFu, (mn - m) * c > kLag)) {
+                    } else if (__any_sync(0xFFFFFFFFu, (mn - m) * c > lag)) {
                         // raise the maximum of the warp's rows: O and l change units
                         const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
                         m = mn;

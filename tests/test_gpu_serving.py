@@ -325,6 +325,38 @@ def test_attention_partly_filled_tiles_are_repeatable(qdq, dim, lens, window):
     assert int(wrong) == 0 and qdq.get_device_status() == 0
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", [8, 14])
+def test_attention_of_a_sequence_keeps_its_bits_whatever_its_neighbours_ask(qdq, heads, dim):
+    """The rows of a tile after a sequence's last one hold the next sequence's queries."""
+    b = make(qdq, [(5, 1500), (7, 1400)] * 20, heads, 2, dim, 16, "f16", seed=23)
+    b["pools"].copy_(torch.randn(b["pools"].shape, device="cuda"))
+    q = torch.from_numpy(b["rng"].standard_normal((b["tokens"], heads * dim))).half().cuda()
+    mine = torch.from_numpy(np.arange(b["tokens"]) % 12 < 5).cuda()
+    got = []
+    for loud in (0.0, 12.0):
+        x = torch.where(mine[:, None], q, q * loud)
+        out, lse = torch.zeros_like(x), torch.zeros(b["tokens"], heads, device="cuda")
+        b["cache"].attention(0, b["batch"], x, out, lse=lse)
+        got.append((out[mine], lse[mine]))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert qdq.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_is_repeatable_where_heads_do_not_fill_a_tile(qdq, dim):
+    """Seven heads to a key head: 126 of a tile's 128 rows are of the sequence."""
+    b = make(qdq, [(202, 1), (335, 0), (570, 2), (607, 1)] * 3, 14, 2, dim, 128, "f16", seed=29)
+    b["pools"].copy_(torch.randn(b["pools"].shape, device="cuda"))
+    q = 2 * torch.from_numpy(b["rng"].standard_normal((b["tokens"], 14 * dim))).half().cuda()
+    out, other, junk = (torch.zeros_like(q) for _ in range(3))
+    b["cache"].attention(0, b["batch"], q, out, window=263)
+    for k in range(20):
+        b["cache"].attention(0, b["batch"], q * (1 + k), junk, window=263)
+        b["cache"].attention(0, b["batch"], q, other, window=263)
+        assert torch.equal(out, other), k
+
+
 @pytest.mark.parametrize("lens", [[(1, 0)], [(1, 700), (3, 5)], [(300, 40)]])
 def test_attention_keeps_a_query_that_is_no_number_to_itself(qdq, lens):
     b = make(qdq, lens, 8, 2, 128, 32, "bf16", seed=5)
