@@ -27,12 +27,13 @@
 // The copying warp walks the range and publishes each piece; the rest follow it.
 //
 // What bounds it, as measured (GB300; 32 query and 8 kv heads of 128 unless said):
-// * single tokens: HBM. 64 sequences of 30 to 8192 positions 184 us = 6.52 TB/s, 96 % of the
-//   copy rate; one sequence of 131001 positions 89 us, 89 % (the rest is the start, the
-//   first tile's latency and the join, about 10 us, which is all of a 520-position call).
+// * single tokens: HBM. 64 sequences of 30 to 8192 positions 184 to 189 us = 6.3 to 6.5 TB/s, 93
+//   to 96 % of the copy rate; one sequence of 131001 positions 92.5 us, 85 % (the rest is the
+//   start, the first tile's latency and the join, about 10 us, which is all of a 520-position
+//   call, and the second term of an fp16 cache's weights).
 // * prompts: the chain S -> softmax -> P V -> next S of each set, about 3000 clocks a tile
-//   where the matrix instructions of both sets need 2048: 8191 tokens 402 us = 1.37 PFLOP/s,
-//   69 % of the cuBLAS bf16 rate, tensor pipe 62 % busy. At 64 dims the softmax alone (some
+//   where the matrix instructions of both sets need 2048: 8191 tokens 406 us = 1.35 PFLOP/s,
+//   68 % of the cuBLAS bf16 rate, tensor pipe 62 % busy. At 64 dims the softmax alone (some
 //   2500 clocks a tile and set) bounds it.
 //
 // Values in rows of V outside the block's positions are zeroed in shared memory before
@@ -103,6 +104,12 @@ struct Shape {
     // 128 dims nothing is left, and P lies over S.
     static constexpr bool kApart = HD == 64;
     static constexpr int kColP = kApart ? kColO + 2 * HD : 0, kPitchP = kApart ? 64 : 128;
+    // P is rounded to the cache's type, by as much as the result is. Over S there is room for
+    // what the rounding leaves, too, and fp16 caches, chosen for their bits, have that multiplied
+    // as well where the sets share few rows: one token over 131001 positions is then 2.1e-4 off
+    // (relative; the result's own rounding) and not 2.8e-4 to 3.2e-4, for 92.5 us and not 90.0.
+    // In bf16 (64 single tokens: 1.66e-3 and not 2.2e-3 off, 197 us and not 188) it is left.
+    static constexpr int kColRest = kApart ? -1 : kColP + 64;
     static constexpr uint32_t kPieces = kStart + 64;
     static constexpr uint32_t kTotal = kPieces + 192;
 };
@@ -300,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using L = Shape<HD>;
     using F16 = Float16<typename std::conditional<BF16, __nv_bfloat16, __half>::type>;
+    constexpr bool kRest = L::kColRest >= 0 && !BF16;  // what the weights' rounding leaves is multiplied too
     extern __shared__ __align__(1024) char smem[];
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -449,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // O_i (+)= P_i V, and, if there is a next tile, its S_i: once the last one has been read, or
             // (over P_i, which the instructions before it have read) right behind
-            auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more) {
+            auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more, auto rest) {
                 const uint32_t vd = v_lo + (uint32_t)v.slot * (L::kSlot >> 4);
                 if (first) {
                     mbar_wait(bar(kBarOFree + i), ((no >> i) & 1) ^ 1, status);
@@ -469,6 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < kTileN / 16; ++k)
                         tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColP + L::kPitchP * i + 8u * k,
                                   desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
+                    if constexpr (rest.value) {
+#pragma unroll
+                        for (int k = 0; k < kTileN / 16; ++k)
+                            tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColRest + L::kPitchP * i + 8u * k,
+                                      desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, true);
+                    }
                     tc_commit(bar(kBarPv + i));
                     if (!L::kApart && more) qk(i, qi, k_next);
                 }
@@ -490,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < n; ++k, vp.step(2)) {
                         // (few rows wait for memory: no key is waited for ahead of a product that could run)
                         full(vp);
-                        turn(k & 1, 0, vp, k < 2, kp, false);
+                        turn(k & 1, 0, vp, k < 2, kp, false, std::bool_constant<kRest>());
                         release(vp);
                         if (k + 2 < n) {
                             full(kp);
@@ -516,13 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         full(vp);
                         if (more) full(kp);
                         if (on0) {
-                            turn(0, 0, vp, !begun0, kp, next0);
+                            turn(0, 0, vp, !begun0, kp, next0, std::false_type());
                             begun0 = true;
                         } else if (next0) {
                             begin(0, 0, kp);
                         }
                         if (on1) {
-                            turn(1, 1, vp, !begun1, kp, next1);
+                            turn(1, 1, vp, !begun1, kp, next1, std::false_type());
                             begun1 = true;
                         } else if (next1) {
                             begin(1, 1, kp);
@@ -670,24 +684,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float mc = m == -INFINITY ? 0.0f : m * c;
                     const uint64_t mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {};
-                    uint32_t u[32];
-                    auto weights = [&](const float *s, uint32_t *to) {
+                    auto weights = [&](const float *s, uint32_t *to, uint32_t *left, auto rest) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
                             const uint64_t e = ffma2(pack2(s[k], s[k + 1]), c2, mc2);
                             const float p = ex2(lo_of(e)), q = ex2(hi_of(e));
                             sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
                             to[k / 2] = F16::pack(p, q);
+                            if constexpr (rest.value) {
+                                const float2 h = F16::unpack(to[k / 2]);
+                                left[k / 2] = F16::pack(p - h.x, q - h.y);
+                            }
+                        }
+                    };
+                    auto store = [&](auto rest) {
+                        uint32_t u[32], left[32];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            weights(s[2 * h], u, left, rest);
+                            weights(s[2 * h + 1], u + 16, left + 16, rest);
+                            if (L::kApart && h == 0) p_free();
+                            tc_st32(t_p + 32 * h, u);
+                            if constexpr (rest.value) tc_st32(t_p + L::kColRest - L::kColP + 32 * h, left);
                         }
                     };
                     if (L::kApart) s_read();
-                    weights(s[0], u);
-                    weights(s[1], u + 16);
-                    if (L::kApart) p_free();
-                    tc_st32(t_p, u);
-                    weights(s[2], u);
-                    weights(s[3], u + 16);
-                    tc_st32(t_p + 32, u);
+                    if (kRest && alt) store(std::bool_constant<kRest>());
+                    else store(std::false_type());
                     const uint64_t t = fadd2(sum[0], sum[1]);
                     l += lo_of(t) + hi_of(t);
                 }

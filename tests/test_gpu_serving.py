@@ -172,7 +172,8 @@ def test_append_bad_pages_and_negative_positions(qdq):
 
 
 # ---- attention ----------------------------------------------------------------------------
-def check_attention(qdq, b, window=0, scale=None, layer=0, out_dtype=None, q_scale=1.5, sample=None, pad=0):
+def check_attention(qdq, b, window=0, scale=None, layer=0, out_dtype=None, q_scale=1.5, sample=None, pad=0,
+                    weight_half=None):
     T, H, D = b["tokens"], b["heads"], b["dim"]
     scale = D ** -0.5 if scale is None else scale
     wide = torch.from_numpy(b["rng"].standard_normal((T, H * D + pad)) * q_scale).to(DT[b["dtype"]]).cuda()
@@ -188,7 +189,7 @@ def check_attention(qdq, b, window=0, scale=None, layer=0, out_dtype=None, q_sca
     none = np.isnan(ref_lse)
     assert (got[none] == 7).all() and (got_lse[none] == 7).all(), "rows of no sequence were written"
     assert (f64(out[:, H * D:]) == 7).all()
-    half = torch.finfo(DT[b["dtype"]]).eps / 2
+    half = torch.finfo(DT[b["dtype"]]).eps / 2 if weight_half is None else weight_half
     half_out = torch.finfo(out.dtype).eps / 2
     n = int(b["kv_len"].max())
     ds = 2 * D * 2.0 ** -24 * reach
@@ -323,6 +324,14 @@ def test_attention_partly_filled_tiles_are_repeatable(qdq, dim, lens, window):
         b["cache"].attention(0, b["batch"], q, outs[1], window=window)
         wrong += (outs[0] != outs[1]).any()
     assert int(wrong) == 0 and qdq.get_device_status() == 0
+
+
+@pytest.mark.parametrize("lens", [[(1, 700)], [(1, 130), (1, 0), (1, 2000), (16, 300), (3, 900)]])
+def test_attention_of_few_rows_keeps_what_the_weights_rounding_leaves(qdq, lens):
+    """At 128 dims an fp16 weight is held in two terms, the second rounded by half a step of half a step."""
+    b = make(qdq, lens, 16, 2, 128, 16, "f16", seed=31)
+    fill_held(b)
+    check_attention(qdq, b, out_dtype="f32", weight_half=(torch.finfo(torch.float16).eps / 2) ** 2)
 
 
 @pytest.mark.parametrize("dim", [64, 128])
