@@ -34,6 +34,9 @@
 //
 // CTAs of a cluster send sums to each other before a cluster barrier and read each
 // other's bins after one; two sets of buffers take turns, so a step needs one barrier.
+// Another CTA's shared memory may be touched only once that CTA is known to run: every CTA
+// arrives at a first barrier as it starts and waits there before it sends anything, with
+// the load of its slice in between.
 #include <cmath>
 #include <mutex>
 
@@ -80,6 +83,9 @@ struct Shared {
 QDQ_DEV void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of a barrier that says only that every CTA of the cluster has started.
+QDQ_DEV void cluster_started_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+QDQ_DEV void cluster_started_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 QDQ_DEV uint32_t cluster_rank() {
     uint32_t r;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -681,6 +687,7 @@ struct Row {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) char smem[];
+    cluster_started_arrive();
     follow_last_kernel();
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     Row r(sh, cluster_rank(), cluster_size());
@@ -728,6 +735,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         const u64 e = __shfl_xor_sync(kAll, best, o);
         best = e > best ? e : best;
     }
+    cluster_started_wait();
     r.send<true>(best, __reduce_add_sync(kAll, live), ctas);
     cluster_sync();
     best = 0;

@@ -1,0 +1,29 @@
+"""Rules of the serving kernels and their host code whose breach a GPU may not show (or may only show
+by faulting), read off the sources."""
+import re
+from pathlib import Path
+
+CSRC = Path(__file__).resolve().parents[1] / "quant_dequant_gemv_gb300" / "csrc"
+
+
+def body(source: str, head: str) -> str:
+    """The braces that follow the first `head` in a file, without comments."""
+    text = re.sub(r"//[^\n]*", "", (CSRC / source).read_text())
+    at = text.index("{", text.index(head))
+    depth = 0
+    for end in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[end], 0)
+        if depth == 0:
+            return text[at:end + 1]
+    raise AssertionError(f"{head} in {source} has no end")
+
+
+def test_sampling_reaches_other_ctas_only_once_all_have_started():
+    """Distributed shared memory may be accessed only while its CTA runs: the barrier of the cluster's
+    start is passed before the first call that stores to, or reads from, another CTA."""
+    kernel = body("qdq_sample.cu", "sample_kernel(const SampleArgs a)")
+    arrive, wait = kernel.index("cluster_started_arrive()"), kernel.index("cluster_started_wait()")
+    first = min(m.start() for m in re.finditer(r"send<|gather_|first_counts<|finish<|resolve|narrow<|remote|mapa|"
+                                               r"cluster_sync", kernel))
+    assert arrive < wait < first
+    assert "return;" not in kernel[:wait], "every thread passes the barrier"
