@@ -270,7 +270,14 @@ int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, 
     }
     c->pools = {k_pages, v_pages, cfg->n_layers, cfg->n_pages, cfg->page_size, cfg->n_heads, cfg->n_kv_heads,
                 cfg->head_dim, cfg->type == QDQ_BF16};
-    if ((rc = attend_create(c->pools, c->sm_count, &c->attend))) {
+    rc = attend_create(c->pools, c->sm_count, &c->attend);
+    // The table's copy and the counters' clearing are asynchronous and in the default stream,
+    // which non-blocking streams do not follow: both are done before the handle is used.
+    if (!rc && cudaStreamSynchronize(nullptr) != cudaSuccess) {
+        cudaGetLastError();
+        rc = QDQ_ERR_CUDA;
+    }
+    if (rc) {
         qdq_paged_destroy(c);
         return rc;
     }

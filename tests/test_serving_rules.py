@@ -27,3 +27,13 @@ def test_sampling_reaches_other_ctas_only_once_all_have_started():
                                                r"cluster_sync", kernel))
     assert arrive < wait < first
     assert "return;" not in kernel[:wait], "every thread passes the barrier"
+
+
+def test_a_cache_is_ready_on_every_stream_when_create_returns():
+    """The handle's table and counters are written in the default stream, which streams created as
+    non-blocking do not follow: create waits for it after the last of those writes."""
+    create = body("qdq_paged.cu", "int qdq_paged_create(")
+    copy, clear = create.index("cudaMemcpy("), create.index("attend_create(")
+    assert "cudaMemset(" in body("qdq_attend.cu", "int attend_create(")
+    wait = create.index("cudaStreamSynchronize(nullptr)")
+    assert copy < clear < wait < create.index("*out = c;")
