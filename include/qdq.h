@@ -389,6 +389,8 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * with kv head h / (n_heads / n_kv_heads),
  *   out[t][h] = sum_j a_j v_j,  a = softmax_j(scale * q . k_j),
  * over the sequence's positions j <= p, and j > p - window when window > 0.
+ * scale: of either sign, or 0 (the mean of the values); scale * log2(e) has to be
+ * finite in fp32 (QDQ_ERR_SHAPE).
  * q: [n_tokens][n_heads * head_dim] of the pools' type (append's q_out), out: of
  * the pools' type or QDQ_F32; row strides in elements, rows 16-byte aligned.
  * lse (NULL or fp32 [n_tokens][n_heads]): log sum_j exp(scale * q . k_j).

@@ -41,6 +41,7 @@
 // by -inf whatever K held.
 #include <cmath>
 #include <cuda.h>
+#include <limits>
 #include <mutex>
 #include <new>
 #include <type_traits>
@@ -1072,7 +1073,9 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     k.n_seqs = a.n_seqs, k.n_tokens = a.n_tokens, k.max_pages = a.max_pages;
     k.q_start = a.q_start, k.kv_len = a.kv_len, k.page_table = a.page_table;
     k.out = a.out, k.lse = a.lse, k.out_stride = a.out_stride;
-    k.scale_log2 = (float)(std::fabs((double)a.scale) * 1.4426950408889634);
+    // (masked scores are -inf and are multiplied by the scale: for a scale of 0 by the smallest number
+    // instead, which leaves them -inf and moves the weight of any finite score by less than 2^-20 of it)
+    k.scale_log2 = std::fmax((float)(std::fabs((double)a.scale) * 1.4426950408889634), std::numeric_limits<float>::denorm_min());
     k.n_pages = p.n_pages;
     while ((1 << k.page_shift) < p.page_size) ++k.page_shift;
     k.row8_layer = (int)((int64_t)a.layer * p.n_pages * p.page_size / 8);

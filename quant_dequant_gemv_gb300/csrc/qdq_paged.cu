@@ -333,7 +333,8 @@ int qdq_paged_attention(qdq_paged *c, int layer, const qdq_paged_batch *b, const
     if (rc) return rc;
     const qdq_paged_config &g = c->cfg;
     if (out_type != QDQ_F32 && out_type != g.type) return QDQ_ERR_TYPE;
-    if (!std::isfinite(scale) || window < 0) return QDQ_ERR_SHAPE;
+    // (the kernel takes scale * log2(e) as fp32)
+    if (!std::isfinite((float)(scale * 1.4426950408889634)) || window < 0) return QDQ_ERR_SHAPE;
     if (!work) return QDQ_OK;
     const int n = b->n_tokens;
     const int64_t width = (int64_t)g.n_heads * g.head_dim;
