@@ -394,9 +394,11 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * q: [n_tokens][n_heads * head_dim] of the pools' type (append's q_out), out: of
  * the pools' type or QDQ_F32; row strides in elements, rows 16-byte aligned.
  * lse (NULL or fp32 [n_tokens][n_heads]): log sum_j exp(scale * q . k_j).
- * Scores, maxima, sums and the accumulator are fp32; the softmax weights are
- * rounded to the pools' type before they meet v (as its matrix product takes
- * them), so an fp32 out is accurate to about that rounding too. A token with
+ * Scores, maxima, sums and the accumulator are fp32. The softmax weights meet v in
+ * the pools' type, as its matrix product takes them: in two terms, which keep 16
+ * bits of a weight or more, for an fp32 out and for sequences (or last pieces of
+ * them) of at most 128 / (n_heads / n_kv_heads) new tokens; otherwise rounded once,
+ * which is an error of the size of the 16-bit out's own rounding. A token with
  * nothing to attend to gets a zero row and lse = -inf. Keys and values of
  * positions outside a sequence's range are never used, whatever they hold; values
  * inside it are taken to be finite (a position that only later tokens of a chunk

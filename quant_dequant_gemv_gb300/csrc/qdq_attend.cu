@@ -4,10 +4,23 @@
 //   o = sum_j p_j v_j / l,  p_j = 2^(c s_j - m),  l = sum_j p_j,  c = scale * log2(e)
 // in one pass over the keys with a running maximum m and sum l (fp32). For a tile of 128
 // rows (tokens x the query heads that share a kv head) and a tile of 128 positions,
-// S = Q K^T goes to tensor memory, 128 threads take a row each, write P (16-bit) back (over
-// S at 128 dims), and O += P V accumulates in tensor memory. The maximum that p is taken against lags
+// S = Q K^T goes to tensor memory, 128 threads take a row each, write P back, and O += P V
+// accumulates in tensor memory. The maximum that p is taken against lags
 // the true one by up to 2^8, so that O is rescaled a few times a row and not every tile;
 // the factor cancels in o and in l.
+//
+// The matrix instruction takes P in the cache's 16-bit type. A weight rounded to it once is off by
+// as much as a 16-bit result is by its own rounding (the whole error is 1.37 times that); two
+// terms, what the type keeps of a weight and what it leaves, and a second product make the
+// result's rounding all the error. Two terms are multiplied
+// * for an fp32 result always: a caller who asks for more bits than the cache has gets them
+//   (8191 tokens 557 us and not 433, ragged pieces 117 and not 86);
+// * of a block of one tile of rows, single tokens as a rule, in any type, since it waits for memory
+//   (64 single tokens bf16: 1.66e-3 and not 2.2e-3 off, 194 us and not 189; one over 131001
+//   positions fp16: 2.1e-4 and not 2.9e-4, 93 and not 90; one over 520: 10.8 and not 10.2).
+// Two tiles of rows with a 16-bit result have one term: the products bound them (8191 tokens bf16:
+// 2.15e-3 and not 1.64e-3 off, 413 us and not the 540 that a second term takes; a window at 64
+// dims 84 and not 101, ragged pieces 83 and not 103).
 //
 // A CTA (one per SM) has ten working warps: two groups of four that each own one S/P/O set
 // (the softmax), one that issues the matrix instructions and one that issues the copies.
@@ -82,7 +95,6 @@ struct KernelArgs {
     uint32_t idesc_qk, idesc_pv;
     int n_pages, page_shift, row8_layer;  // row8_layer: first group of 8 rows of the layer
     int n_heads;
-    bool out_f32;
     AttendGeometry g;
     float *part_o;
     float2 *part_ml;
@@ -100,17 +112,12 @@ struct Shape {
     static constexpr uint32_t kBars = kRing + kSlots * kSlot;
     static constexpr uint32_t kScratch = kBars + 304;        // a state handed from set to set, a join's flag
     static constexpr uint32_t kStart = kScratch + 2 * 128 * 8;  // the CTA's first piece, tensor-memory base
-    // Tensor memory: S of the two sets in columns 0..255, O from kColO on. At 64 dims P has
-    // columns of its own, so that the next S can be computed while the weights still are; at
-    // 128 dims nothing is left, and P lies over S.
+    // Tensor memory: S of the two sets in columns 0..255, O from kColO on. A weight's two terms
+    // lie over S, 64 columns each. One term alone has, at 64 dims, columns of its own, so that the
+    // next S can be computed while the weights still are; at 128 dims none are left.
     static constexpr bool kApart = HD == 64;
-    static constexpr int kColP = kApart ? kColO + 2 * HD : 0, kPitchP = kApart ? 64 : 128;
-    // P is rounded to the cache's type, by as much as the result is. Over S there is room for
-    // what the rounding leaves, too, and fp16 caches, chosen for their bits, have that multiplied
-    // as well where the sets share few rows: one token over 131001 positions is then 2.1e-4 off
-    // (relative; the result's own rounding) and not 2.8e-4 to 3.2e-4, for 92.5 us and not 90.0.
-    // In bf16 (64 single tokens: 1.66e-3 and not 2.2e-3 off, 197 us and not 188) it is left.
-    static constexpr int kColRest = kApart ? -1 : kColP + 64;
+    static constexpr int kColOne = kApart ? kColO + 2 * HD : 0, kPitchOne = kApart ? 64 : 128;
+    static constexpr int kColRest = 64;  // of the second term, from the first one's
     static constexpr uint32_t kPieces = kStart + 64;
     static constexpr uint32_t kTotal = kPieces + 192;
 };
@@ -302,13 +309,16 @@ QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
     __syncthreads();
 }
 
-template <int HD, bool BF16>
+template <int HD, bool BF16, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using L = Shape<HD>;
     using F16 = Float16<typename std::conditional<BF16, __nv_bfloat16, __half>::type>;
-    constexpr bool kRest = L::kColRest >= 0 && !BF16;  // what the weights' rounding leaves is multiplied too
+    // Whether both terms of the weights are multiplied, with the sets on alternate key tiles and on two
+    // tiles of rows.
+    using TwoAlternate = std::true_type;
+    using TwoTiles = std::bool_constant<OUT32>;
     extern __shared__ __align__(1024) char smem[];
     const uint32_t sb = smem_u32(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -458,13 +468,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // O_i (+)= P_i V, and, if there is a next tile, its S_i: once the last one has been read, or
             // (over P_i, which the instructions before it have read) right behind
-            auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more, auto rest) {
+            auto turn = [&](int i, int qi, const Place &v, bool first, const Place &k_next, bool more, auto two) {
+                constexpr bool apart = L::kApart && !decltype(two)::value;
+                const uint32_t p = tmem + (two.value ? 128u * i : (uint32_t)(L::kColOne + L::kPitchOne * i));
                 const uint32_t vd = v_lo + (uint32_t)v.slot * (L::kSlot >> 4);
                 if (first) {
                     mbar_wait(bar(kBarOFree + i), ((no >> i) & 1) ^ 1, status);
                     no ^= 1u << i;
                 }
-                if (L::kApart) {
+                if (apart) {
                     mbar_wait_spin(bar(kBarSFree + i), (nf >> i) & 1, status);
                     nf ^= 1u << i;
                     tc_after();
@@ -476,16 +488,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect_lane()) {
 #pragma unroll
                     for (int k = 0; k < kTileN / 16; ++k)
-                        tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColP + L::kPitchP * i + 8u * k,
+                        tc_mma_ts(tmem + kColO + (uint32_t)HD * i, p + 8u * k,
                                   desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
-                    if constexpr (rest.value) {
+                    if constexpr (two.value) {
 #pragma unroll
                         for (int k = 0; k < kTileN / 16; ++k)
-                            tc_mma_ts(tmem + kColO + (uint32_t)HD * i, tmem + L::kColRest + L::kPitchP * i + 8u * k,
+                            tc_mma_ts(tmem + kColO + (uint32_t)HD * i, p + L::kColRest + 8u * k,
                                       desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, true);
                     }
                     tc_commit(bar(kBarPv + i));
-                    if (!L::kApart && more) qk(i, qi, k_next);
+                    if (!apart && more) qk(i, qi, k_next);
                 }
                 __syncwarp();
             };
@@ -505,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < n; ++k, vp.step(2)) {
                         // (few rows wait for memory: no key is waited for ahead of a product that could run)
                         full(vp);
-                        turn(k & 1, 0, vp, k < 2, kp, false, std::bool_constant<kRest>());
+                        turn(k & 1, 0, vp, k < 2, kp, false, TwoAlternate());
                         release(vp);
                         if (k + 2 < n) {
                             full(kp);
@@ -531,13 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         full(vp);
                         if (more) full(kp);
                         if (on0) {
-                            turn(0, 0, vp, !begun0, kp, next0, std::false_type());
+                            turn(0, 0, vp, !begun0, kp, next0, TwoTiles());
                             begun0 = true;
                         } else if (next0) {
                             begin(0, 0, kp);
                         }
                         if (on1) {
-                            turn(1, 1, vp, !begun1, kp, next1, std::false_type());
+                            turn(1, 1, vp, !begun1, kp, next1, TwoTiles());
                             begun1 = true;
                         } else if (next1) {
                             begin(1, 1, kp);
@@ -565,7 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = warp >> 2, r = threadIdx.x & 127;  // set; row = tensor-memory lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t t_s = tmem + lanes + 128u * i, t_o = tmem + lanes + kColO + (uint32_t)HD * i;
-        const uint32_t t_p = tmem + lanes + L::kColP + L::kPitchP * i;
         const float c = a.scale_log2;
         const uint64_t c2 = pack2(c, c);
         float2 *scratch = reinterpret_cast<float2 *>(smem + L::kScratch) + i * 128;
@@ -583,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const uint32_t base = seq_no;
             seq_no += 2 * n;
-            const bool alt = w.alt != 0;
+            const bool alt = w.alt != 0, apart = L::kApart && !TwoTiles::value && !alt;
             // this set's rows and key tiles of the piece
             const int qi = alt ? 0 : i, tokens = min(tq, w.tokens - qi * tq), rows = tokens * a.g.group;
             if (rows <= 0) {
@@ -634,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
                     tc_after();
                 };
-                if (L::kApart && idle) {
+                if (apart && idle) {
                     // (S comes ahead of the last tile's P V, so a warp without rows has to wait here
                     // too, or its arrival would count for the last tile's weights)
                     s_read();
@@ -704,14 +715,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int h = 0; h < 2; ++h) {
                             weights(s[2 * h], u, left, rest);
                             weights(s[2 * h + 1], u + 16, left + 16, rest);
-                            if (L::kApart && h == 0) p_free();
-                            tc_st32(t_p + 32 * h, u);
-                            if constexpr (rest.value) tc_st32(t_p + L::kColRest - L::kColP + 32 * h, left);
+                            if constexpr (rest.value) {
+                                tc_st32(t_s + 32 * h, u);
+                                tc_st32(t_s + L::kColRest + 32 * h, left);
+                            } else {
+                                if (L::kApart && h == 0) p_free();
+                                tc_st32(tmem + lanes + L::kColOne + L::kPitchOne * i + 32 * h, u);
+                            }
                         }
                     };
-                    if (L::kApart) s_read();
-                    if (kRest && alt) store(std::bool_constant<kRest>());
-                    else store(std::false_type());
+                    if (apart) s_read();
+                    if (!alt) store(TwoTiles());
+                    else store(TwoAlternate());
                     const uint64_t t = fadd2(sum[0], sum[1]);
                     l += lo_of(t) + hi_of(t);
                 }
@@ -791,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const int64_t first_token = w.token0 + qi * tq, first_head = (int64_t)w.head * a.g.group;
             auto put8 = [&](int64_t at, const float *o, float f) {
-                if (a.out_f32) {
+                if constexpr (OUT32) {
                     float4 *to = reinterpret_cast<float4 *>((float *)a.out + at);
                     to[0] = make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
                     to[1] = make_float4(o[4] * f, o[5] * f, o[6] * f, o[7] * f);
@@ -1019,9 +1034,13 @@ bool encode(CUtensorMap *map, bool bf16, int rank, const void *base, const cuuin
 }
 
 using Kernel = void (*)(KernelArgs, CUtensorMap, CUtensorMap, CUtensorMap);
+template <bool OUT32>
 Kernel kernel_of(int head_dim, bool bf16) {
-    if (head_dim == 64) return bf16 ? attend_kernel<64, true> : attend_kernel<64, false>;
-    return bf16 ? attend_kernel<128, true> : attend_kernel<128, false>;
+    if (head_dim == 64) return bf16 ? attend_kernel<64, true, OUT32> : attend_kernel<64, false, OUT32>;
+    return bf16 ? attend_kernel<128, true, OUT32> : attend_kernel<128, false, OUT32>;
+}
+Kernel kernel_of(int head_dim, bool bf16, bool out_f32) {
+    return out_f32 ? kernel_of<true>(head_dim, bf16) : kernel_of<false>(head_dim, bf16);
 }
 uint32_t smem_of(int head_dim) { return head_dim == 64 ? Shape<64>::kTotal : Shape<128>::kTotal; }
 
@@ -1045,10 +1064,12 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
     const size_t parts = (size_t)sm_count * 4, n_o = parts * 128 * p.head_dim * 4, n_s = parts * 128 * 8;
     const size_t bytes = n_o + n_s + (size_t)sm_count * 2 * sizeof(unsigned);
     ok = ok && cudaMalloc((void **)&st->mem, bytes) == cudaSuccess && cudaMemset(st->mem, 0, bytes) == cudaSuccess;
-    cudaFuncAttributes fa;  // (the kernel's shares of registers add up to its launch's)
-    ok = ok && cudaFuncGetAttributes(&fa, kernel_of(p.head_dim, p.bf16)) == cudaSuccess && fa.numRegs == 168;
-    ok = ok && cudaFuncSetAttribute(kernel_of(p.head_dim, p.bf16), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem_of(p.head_dim)) == cudaSuccess;
+    for (bool out_f32 : {false, true}) {
+        cudaFuncAttributes fa;  // (the kernel's shares of registers add up to its launch's)
+        const Kernel f = kernel_of(p.head_dim, p.bf16, out_f32);
+        ok = ok && cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == 168;
+        ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(p.head_dim)) == cudaSuccess;
+    }
     if (!ok) {
         cudaGetLastError();
         attend_destroy(st);
@@ -1080,7 +1101,6 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     while ((1 << k.page_shift) < p.page_size) ++k.page_shift;
     k.row8_layer = (int)((int64_t)a.layer * p.n_pages * p.page_size / 8);
     k.n_heads = p.n_heads;
-    k.out_f32 = a.out_f32;
     k.g.group = p.n_heads / p.n_kv_heads;
     k.g.tokens = kTileM / k.g.group;
     k.g.kv_heads = p.n_kv_heads;
@@ -1099,7 +1119,7 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, q_row};
     const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)k.g.tokens};
     if (!encode(&q_map, p.bf16, 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
-    return launch_following(kernel_of(p.head_dim, p.bf16), st->ctas, kThreads, smem_of(p.head_dim), 1, stream, k, q_map,
+    return launch_following(kernel_of(p.head_dim, p.bf16, a.out_f32), st->ctas, kThreads, smem_of(p.head_dim), 1, stream, k, q_map,
                             st->k_map, st->v_map);
 }
 

@@ -77,10 +77,10 @@ QDQ_PLAN_FN AttendBlock block_of(const AttendGeometry &g, int count, int kv, int
     return r;
 }
 
-// Item of one tile of rows and two key tiles or more: its two softmax groups take
-// alternate key tiles of the same rows.
+// Item of one tile of rows that attends to anything: its two softmax groups take alternate
+// key tiles of the same rows (the first group has the only one of a single tile).
 QDQ_PLAN_FN bool block_alternates(const AttendGeometry &g, const AttendBlock &b) {
-    return b.i1 - b.i0 <= g.tokens && b.t1 - b.t0 >= 2;
+    return b.i1 - b.i0 <= g.tokens && b.hi > b.lo;
 }
 
 // CTA c of n takes units range_start(c) .. range_start(c + 1) - 1 of `total`.
