@@ -398,7 +398,8 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * the pools' type, as its matrix product takes them: in two terms, which keep 16
  * bits of a weight or more, for an fp32 out and for sequences (or last pieces of
  * them) of at most 128 / (n_heads / n_kv_heads) new tokens; otherwise rounded once,
- * which is an error of the size of the 16-bit out's own rounding. A token with
+ * which is an error of the size of the 16-bit out's own rounding. (fp16 also has a
+ * smallest step: weights may be off by 2^-32 of the largest that the row has.) A token with
  * nothing to attend to gets a zero row and lse = -inf. Keys and values of
  * positions outside a sequence's range are never used, whatever they hold; values
  * inside it are taken to be finite (a position that only later tokens of a chunk

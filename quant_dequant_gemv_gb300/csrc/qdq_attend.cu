@@ -84,6 +84,12 @@ __device__ int g_attend_status;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 384;
 constexpr float kLag = 8.0f;  // log2 of how far the running maximum may lag
 constexpr int kColO = 256;
+// log2 of what weights are kept times. fp16's last step below 2^-14 is 2^-24: with the largest weight
+// at 2^7 (and up to 2^15 where the maximum lags) half of it is 2^-32 of that weight, and many small
+// weights beside a large one keep their sum (at 1 they would vanish below 2^-25 of it). The factor is
+// in m and cancels in o and l. bf16 has fp32's range.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.0f : 7.0f;
 
 struct KernelArgs {
     int n_seqs, n_tokens, max_pages;
@@ -693,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc_wait_st();
                     }
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    const float mc = m == -INFINITY ? 0.0f : fmaf(m, c, -kLift<BF16>);
                     const uint64_t mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {};
                     auto weights = [&](const float *s, uint32_t *to, uint32_t *left, auto rest) {
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---- the piece's end ------------------------------------------------------------
             const bool any = j1 > j0;
-            float mc = m == -INFINITY ? -INFINITY : m * c, f0 = 1.0f, f1 = 0.0f;
+            float mc = m == -INFINITY ? -INFINITY : fmaf(m, c, -kLift<BF16>), f0 = 1.0f, f1 = 0.0f;
             if (any) {
                 mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
                 tc_after();
