@@ -9,6 +9,8 @@ sampling. The weights are multiplied once for all rows of a step.
 """
 from __future__ import annotations
 
+import operator
+
 from . import qdq, synth
 
 ROWS = 8  # plans take at most eight columns
@@ -64,6 +66,15 @@ class PagedLlama:
         self._pages[seq] = []
         self.lengths[seq] = 0
 
+    def _word(self, token) -> int:
+        try:
+            word = operator.index(token)
+        except TypeError:
+            word = -1
+        if not 0 <= word < self.vocab:  # (-1 is what sampling draws from a row of nothing)
+            raise ValueError(f"tokens 0 to {self.vocab - 1} are needed, not {token!r}")
+        return word
+
     def step(self, work: dict[int, list[int]], u, stream=None, **sampling) -> dict[int, tuple[int, int]]:
         """Runs the new tokens of each sequence in `work` (at most eight in all) and draws the next
         token of each with the random numbers u [8] and sampling's per-row tensors (temperature,
@@ -74,6 +85,7 @@ class PagedLlama:
         if not 1 <= rows <= ROWS or any(not 0 <= s < self.max_seqs or not t for s, t in work.items()):
             raise ValueError(f"1 to {ROWS} tokens of sequences 0 to {self.max_seqs - 1}")
         order = sorted(work)
+        words = [self._word(t) for s in order for t in work[s]]
         need = {s: -(-(self.lengths[s] + len(work[s])) // self.page_size) - len(self._pages[s]) for s in order}
         if sum(need.values()) > len(self._free) or \
                 any(len(self._pages[s]) + need[s] > self.max_pages for s in order):
@@ -96,7 +108,7 @@ class PagedLlama:
             kind, W = self.embd
             row = self.dim // qdq.block_weights(kind) * qdq.block_bytes(kind)
             self.h[rows:].zero_()
-            for r, token in enumerate(t for s in order for t in work[s]):
+            for r, token in enumerate(words):
                 qdq.dequant(kind, W.view(-1)[token * row:], self.dim, self.h[r])
             for l, (before, after) in enumerate(zip(self._before, self._after)):
                 before.run()
