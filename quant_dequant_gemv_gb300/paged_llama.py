@@ -79,7 +79,7 @@ class PagedLlama:
         """Runs the new tokens of each sequence in `work` (at most eight in all) and draws the next
         token of each with the random numbers u [8] and sampling's per-row tensors (temperature,
         top_k, top_p, min_p: see qdq.sample). Returns {sequence: (row, next token)}; `logits` and
-        `logprobs` hold the rows'."""
+        `logprobs` hold the rows'. A step that raises leaves the sequences as they were."""
         import torch
         rows = sum(len(t) for t in work.values())
         if not 1 <= rows <= ROWS or any(not 0 <= s < self.max_seqs or not t for s, t in work.items()):
@@ -90,9 +90,12 @@ class PagedLlama:
         if sum(need.values()) > len(self._free) or \
                 any(len(self._pages[s]) + need[s] > self.max_pages for s in order):
             raise RuntimeError("the page pool, or a sequence's page table, is full")
+        # what the sequences hold after the step: theirs once it has run whole, so that one that is
+        # refused on the way (a sampling argument, say) can be run again
+        free, pages, lengths = list(self._free), {}, list(self.lengths)
         for s in order:
-            self._pages[s] += [self._free.pop() for _ in range(need[s])]
-            self.lengths[s] += len(work[s])
+            pages[s] = self._pages[s] + [free.pop() for _ in range(need[s])]
+            lengths[s] += len(work[s])
         starts, last, at = [0], {}, 0
         for s in range(self.max_seqs):
             at += len(work.get(s, ()))
@@ -101,10 +104,10 @@ class PagedLlama:
                 last[s] = at - 1
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(torch.cuda.current_stream()):
             self.q_start.copy_(torch.tensor(starts, dtype=torch.int32))
-            self.kv_len.copy_(torch.tensor(self.lengths, dtype=torch.int32))
+            self.kv_len.copy_(torch.tensor(lengths, dtype=torch.int32))
             for s in order:
                 if need[s]:
-                    self.table[s, :len(self._pages[s])] = torch.tensor(self._pages[s], dtype=torch.int32).cuda()
+                    self.table[s, :len(pages[s])] = torch.tensor(pages[s], dtype=torch.int32).cuda()
             kind, W = self.embd
             row = self.dim // qdq.block_weights(kind) * qdq.block_bytes(kind)
             self.h[rows:].zero_()
@@ -118,6 +121,9 @@ class PagedLlama:
             self._head.run()
             qdq.sample(self.logits, u, self.tokens, logprobs=self.logprobs, **sampling)
             drawn = self.tokens.tolist()
+        self._free, self.lengths = free, lengths
+        for s in order:
+            self._pages[s] = pages[s]
         return {s: (r, drawn[r]) for s, r in last.items()}
 
     def close(self) -> None:

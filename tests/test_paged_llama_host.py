@@ -79,3 +79,28 @@ def test_tokens_of_any_integer_type_are_taken(model):
     model.step({0: [np.int64(3), torch.tensor(4)], 1: [5]}, U)
     rows = [a[1].numel() for n, a, _ in model.calls if n == "dequant"]
     assert rows == [(VOCAB - t) * 144 for t in (3, 4, 5)]
+
+
+@pytest.mark.parametrize("call", ["dequant", "head", "sample"])
+def test_a_refused_step_leaves_the_sequences_as_they_were(model, call):
+    """The caller mends the argument and runs the same tokens again, at the same positions."""
+    model.step({0: [1, 2, 3], 1: [9]}, U)
+    before = state(model)
+    model.refuse = call
+    with pytest.raises(Refused):
+        model.step({0: [4, 5], 2: [6]}, U)
+    assert state(model) == before
+    model.refuse = None
+    assert model.step({0: [4, 5], 2: [6]}, U) == {0: (1, 1), 2: (2, 2)}
+    assert model.lengths == [5, 1, 1] and model.kv_len.tolist() == [5, 1, 1]
+    assert model.table[0, :2].tolist() == model._pages[0] and model.table[2, 0] == model._pages[2][0]
+    held = [p for pages in model._pages for p in pages] + model._free
+    assert sorted(held) == list(range(PAGES))
+
+
+def test_a_sampling_argument_that_qdq_sample_refuses(model, monkeypatch):
+    real = []
+    monkeypatch.setattr(qdq, "sample", lambda *a, **k: real.append(1) or (_ for _ in ()).throw(ValueError("top_k")))
+    with pytest.raises(ValueError):
+        model.step({0: [1]}, U, top_k=torch.zeros(8))
+    assert real and state(model) == (list(range(PAGES)), [[], [], []], [0, 0, 0])
