@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import hashlib
 import os
+import re
 import shutil
 import subprocess
 from concurrent.futures import ThreadPoolExecutor
@@ -23,6 +24,21 @@ SOURCES = ["qdq_api.cu", "qdq_dequant.cu", "qdq_stream.cu", "qdq_stream1.cu", "q
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               f"-I{INCLUDE}", f"-I{CSRC}"] + os.environ.get("QDQ_EXTRA_NVCC_FLAGS", "").split()
+
+
+# Kernels that move registers between their warps: the shares add up to what the launch has only
+# with this many a thread, and a kernel that asked for more would wait for ever.
+REGISTERS = {"qdq_attend.cu": ("attend_kernel", 168)}
+
+
+def check_registers(src: str, ptxas: str) -> None:
+    """Raises if a kernel of REGISTERS[src] was given another number of registers (ptxas -v's report)."""
+    name, want = REGISTERS[src]
+    got = re.findall(r"Compiling entry function '(\w*%s\w*)'.*?Used (\d+) registers" % name, ptxas, re.S)
+    bad = sorted({int(n) for _, n in got if int(n) != want})
+    if not got or bad:
+        raise RuntimeError(f"{src}: {name} has {bad or 'no'} registers a thread, and its setmaxnreg shares need {want}: "
+                           "built with another toolkit or other flags (QDQ_EXTRA_NVCC_FLAGS), they have to be set anew")
 
 
 def nvcc() -> str:
@@ -52,11 +68,13 @@ def build(verbose: bool = False, force: bool = False) -> Path:
     def compile_one(src: str) -> Path:
         obj = BUILD / (Path(src).stem + ".o")
         cmd = [cc, *ARCH, *NVCC_FLAGS, "-c", str(CSRC / src), "-o", str(obj)]
-        if verbose:
+        if verbose or src in REGISTERS:
             cmd.insert(1, "-Xptxas=-v")
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        if src in REGISTERS:
+            check_registers(src, r.stdout + r.stderr)
         if verbose and r.stderr:
             print(r.stderr)
         return obj

@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Registers: launched with 168 a thread, three warpgroups of them; the softmax groups go
     // up to 216, which holds a row's 128 scores without spilling, and the third, of which two
-    // warps work, comes down to 72: 2 x 216 + 72 = 3 x 168 (attend_create checks the 168).
+    // warps work, comes down to 72: 2 x 216 + 72 = 3 x 168 (the build refuses to make a library
+    // with another number, attend_create to run one).
     if (warp >= kWarpMma) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kWarpLoad) {

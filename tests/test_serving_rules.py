@@ -3,6 +3,8 @@ by faulting), read off the sources."""
 import re
 from pathlib import Path
 
+import pytest
+
 CSRC = Path(__file__).resolve().parents[1] / "quant_dequant_gemv_gb300" / "csrc"
 
 
@@ -37,3 +39,15 @@ def test_a_cache_is_ready_on_every_stream_when_create_returns():
     assert "cudaMemset(" in body("qdq_attend.cu", "int attend_create(")
     wait = create.index("cudaStreamSynchronize(nullptr)")
     assert copy < clear < wait < create.index("*out = c;")
+
+
+def test_the_build_refuses_other_register_counts():
+    from quant_dequant_gemv_gb300 import build
+    entry = "ptxas info    : Compiling entry function '_ZN3qdq{}ILi64EEE' for 'sm_103a'\nptxas info    : Used {} registers, used 1 barriers\n"
+    build.check_registers("qdq_attend.cu", entry.format("13attend_kernel", 168) + entry.format("5other", 40))
+    for text in (entry.format("13attend_kernel", 168) + entry.format("13attend_kernel", 160), entry.format("5other", 168), ""):
+        with pytest.raises(RuntimeError, match="qdq_attend.cu"):
+            build.check_registers("qdq_attend.cu", text)
+    inc, dec = (int(re.search(r"setmaxnreg\.%s\S* (\d+);" % way, (CSRC / "qdq_attend.cu").read_text()).group(1))
+                for way in ("inc", "dec"))
+    assert 2 * inc + dec == 3 * build.REGISTERS["qdq_attend.cu"][1]
