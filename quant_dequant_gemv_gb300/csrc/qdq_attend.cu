@@ -55,7 +55,6 @@
 #include <cmath>
 #include <cuda.h>
 #include <limits>
-#include <mutex>
 #include <new>
 #include <type_traits>
 
@@ -360,10 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_async_smem();  // the ring's memory goes over to the copies
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kStart);
-    if (warp == kWarpMma) tc_alloc(smem_u32(tmem_slot), 512);
-    tc_before();
+    if (warp == kWarpMma) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
     __syncthreads();
-    tc_after();
+    tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(tmem_slot), 0);
 
     const int run_shift = min(a.page_shift, 7), tq = a.g.tokens;
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto full = [&](const Place &p) { mbar_wait(bar(kBarFull + p.slot), p.phase, status); };
             auto release = [&](const Place &p) {
-                if (elect_lane()) tc_commit(bar(kBarEmpty + p.slot));
+                if (elect_one()) mma_commit(bar(kBarEmpty + p.slot));
                 __syncwarp();
             };
             // S_i = Q K^T with rows of tile qi (in an elected lane)
@@ -465,12 +467,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t kd = k_lo + (uint32_t)p.slot * (L::kSlot >> 4), qd = q_lo + qi * (L::kQTile >> 4);
 #pragma unroll
                 for (int k = 0; k < HD / 16; ++k)
-                    tc_mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
+                    mma_ss(tmem + 128u * i, desc64(qd + (k / 4) * 1024u + (k % 4) * 2u, q_hi),
                               desc64(kd + (k / 4) * 64u + (k % 4) * 2u, kv_hi), a.idesc_qk, k > 0);
-                tc_commit(bar(kBarS + i));
+                mma_commit(bar(kBarS + i));
             };
             auto begin = [&](int i, int qi, const Place &p) {
-                if (elect_lane()) qk(i, qi, p);
+                if (elect_one()) qk(i, qi, p);
                 __syncwarp();
             };
             // O_i (+)= P_i V, and, if there is a next tile, its S_i: once the last one has been read, or
@@ -486,24 +488,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (apart) {
                     mbar_wait_spin(bar(kBarSFree + i), (nf >> i) & 1, status);
                     nf ^= 1u << i;
-                    tc_after();
+                    tc_fence_after();
                     if (more) begin(i, qi, k_next);
                 }
                 mbar_wait_spin(bar(kBarP + i), (np >> i) & 1, status);
                 np ^= 1u << i;
-                tc_after();
-                if (elect_lane()) {
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kTileN / 16; ++k)
-                        tc_mma_ts(tmem + kColO + (uint32_t)HD * i, p + 8u * k,
+                        mma_ts(tmem + kColO + (uint32_t)HD * i, p + 8u * k,
                                   desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, !first || k > 0);
                     if constexpr (two.value) {
 #pragma unroll
                         for (int k = 0; k < kTileN / 16; ++k)
-                            tc_mma_ts(tmem + kColO + (uint32_t)HD * i, p + L::kColRest + 8u * k,
+                            mma_ts(tmem + kColO + (uint32_t)HD * i, p + L::kColRest + 8u * k,
                                       desc64(vd + k * (2 * L::kGroup8 >> 4), kv_hi), a.idesc_pv, true);
                     }
-                    tc_commit(bar(kBarPv + i));
+                    mma_commit(bar(kBarPv + i));
                     if (!apart && more) qk(i, qi, k_next);
                 }
                 __syncwarp();
@@ -568,13 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (elect_lane()) {
-                    tc_commit(bar(kBarQEmpty));
+                if (elect_one()) {
+                    mma_commit(bar(kBarQEmpty));
                     mbar_arrive(bar(kBarPieceFree + (items & 1)));
                 }
                 __syncwarp();
             }
-            if (elect_lane()) tc_commit(bar(kBarDrain));
+            if (elect_one()) mma_commit(bar(kBarDrain));
             __syncwarp();
             mbar_wait(bar(kBarDrain), 0, status);
         }
@@ -641,16 +643,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int y = 0; y < 32; ++y) s[y] = (keep >> y) & 1 ? s[y] : -INFINITY;
                 };
                 mbar_wait_spin(bar(kBarS + i), ns++ & 1, status);
-                tc_after();
+                tc_fence_after();
                 const auto s_read = [&] {  // S may be overwritten
-                    tc_before();
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(kBarSFree + i));
                 };
                 const auto p_free = [&] {  // the last tile's weights have been read
                     if (npv == 0) return;
                     mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
-                    tc_after();
+                    tc_fence_after();
                 };
                 if (apart && idle) {
                     // (S comes ahead of the last tile's P V, so a warp without rows has to wait here
@@ -683,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = mn;
                         l *= f;
                         mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
-                        tc_after();
+                        tc_fence_after();
                         const uint64_t f2 = pack2(f, f);
 #pragma unroll
                         for (int k = 0; k < HD / 16; ++k) {
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             tc_st16(t_o + 16 * k, reinterpret_cast<uint32_t *>(o));
                         }
-                        tc_wait_st();
+                        tmem_wait_st();
                     }
                     const float mc = m == -INFINITY ? 0.0f : fmaf(m, c, -kLift<BF16>);
                     const uint64_t mc2 = pack2(-mc, -mc);
@@ -749,8 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_async_smem();
                 }
-                tc_wait_st();
-                tc_before();
+                tmem_wait_st();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(kBarP + i));
                 ++npv;
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mc = m == -INFINITY ? -INFINITY : fmaf(m, c, -kLift<BF16>), f0 = 1.0f, f1 = 0.0f;
             if (any) {
                 mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
-                tc_after();
+                tc_fence_after();
             }
             const bool both = alt && n >= 2;  // two states of the same rows
             if (alt && i == 1) {
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lent = both;
                 if (both) {
                     scratch[r] = make_float2(mc, l);
-                    tc_before();
+                    tc_fence_before();
                     named_bar_arrive(3, 256);
                 }
                 done();
@@ -777,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (both) {
                 named_bar_sync(3, 256);
-                tc_after();
+                tc_fence_after();
                 const float2 o = scratch[128 + r];
                 named_bar_arrive(4, 256);
                 const float M = fmaxf(mc, o.x);
@@ -804,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto read_done = [&] {  // the next piece may overwrite the accumulators
-                tc_before();
+                tc_fence_before();
                 __syncwarp();
                 if (any && lane == 0) {
                     mbar_arrive(bar(kBarOFree + i));
@@ -1003,31 +1005,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lent) named_bar_sync(4, 256);
     }
 
-    tc_before();
+    tc_fence_before();
     __syncthreads();
     if (warp == kWarpMma) {
-        tc_after();
-        tc_dealloc(tmem, 512);
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
     }
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-    static std::once_flag once;
-    static EncodeTiled fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(p);
-        else
-            cudaGetLastError();
-    });
-    return fn;
 }
 
 bool encode(CUtensorMap *map, bool bf16, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,

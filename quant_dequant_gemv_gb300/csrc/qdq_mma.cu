@@ -51,6 +51,7 @@
 
 #include "qdq_decode.cuh"
 #include "qdq_internal.h"
+#include "qdq_tcgen05.cuh"
 
 namespace qdq {
 namespace {
@@ -173,40 +174,11 @@ __host__ __device__ inline Layout layout_for(uint32_t stage_bytes, int nraw, int
 }
 
 // ---- tcgen05 / cluster PTX -------------------------------------------------------
-QDQ_DEV void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-                 : "memory");
-}
-QDQ_DEV void tmem_relinquish() { asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory"); }
-QDQ_DEV void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-QDQ_DEV uint32_t elect_one() {
-    uint32_t pred = 0;
-    asm volatile("{ .reg .pred P; elect.sync _|P, 0xffffffff; selp.u32 %0, 1, 0, P; }" : "=r"(pred));
-    return pred;
-}
-QDQ_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-QDQ_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// D (tensor memory) += A (tensor memory) x B (shared memory, by descriptor).
-QDQ_DEV void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrives on the mbarrier once every MMA this thread issued so far has completed.
-QDQ_DEV void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
 QDQ_DEV void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
-QDQ_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 QDQ_DEV void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -384,16 +356,6 @@ QDQ_DEV void tmem_ld8(uint32_t ta, uint32_t (&v)[8]) {
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
         : "r"(ta)
         : "memory");
-}
-
-// A shared-memory descriptor from its low word (start address, leading offset)
-// and high word. Building each MMA's descriptor as a 32-bit add on a
-// loop-invariant base keeps the MMA issue at about 10 ns; composing the 64-bit
-// value per MMA costs several times that.
-QDQ_DEV uint64_t desc_from_words(uint32_t lo, uint32_t hi) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    return d;
 }
 
 // A ring slot and its phase, advanced one use at a time (no divisions).
@@ -750,10 +712,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     const uint32_t dg = dbase + ((kG == 4) ? t : (t >> 1)) * gcols;
                                     const uint32_t acc = (kG == 4) ? 0u : (uint32_t)(t & 1);
                                     if constexpr (kStack) {
-                                        mma_ts(dg, tmem + 32u * s + 8 * t, desc_from_words(bt, xdesc_hi), idesc2, acc);
+                                        mma_ts(dg, tmem + 32u * s + 8 * t, desc64(bt, xdesc_hi), idesc2, acc);
                                     } else {
-                                        mma_ts(dg, tmem + 32u * s + 8 * t, desc_from_words(bt, xdesc_hi), idesc, acc);
-                                        mma_ts(dg, tmem + 32u * s + 8 * t, desc_from_words(bt + lo_step, xdesc_hi), idesc, 1u);
+                                        mma_ts(dg, tmem + 32u * s + 8 * t, desc64(bt, xdesc_hi), idesc, acc);
+                                        mma_ts(dg, tmem + 32u * s + 8 * t, desc64(bt + lo_step, xdesc_hi), idesc, 1u);
                                     }
                                 }
                             }
@@ -1121,26 +1083,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- host ----------------------------------------------------------------------------
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-    static std::once_flag once;
-    static EncodeTiled fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(p);
-        else
-            cudaGetLastError();
-    });
-    return fn;
-}
-
 int64_t gcd64(int64_t a, int64_t b) {
     while (b) {
         const int64_t t = a % b;
