@@ -396,7 +396,9 @@ int qdq_get_device_status(qdq_stream_t stream) {
     const int a1 = take_status_stream1();
     const int b = take_status_mma();
     const int c = take_status_attend();
-    return a != QDQ_OK ? a : a1 != QDQ_OK ? a1 : b != QDQ_OK ? b : c;
+    const int d = take_status_append();
+    const int e = take_status_sample();
+    return a != QDQ_OK ? a : a1 != QDQ_OK ? a1 : b != QDQ_OK ? b : c != QDQ_OK ? c : d != QDQ_OK ? d : e;
 }
 
 int qdq_selftest_wait_timeout(int64_t timeout_ns, qdq_stream_t stream) {

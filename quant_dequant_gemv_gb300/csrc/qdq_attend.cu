@@ -205,7 +205,8 @@ QDQ_DEV int tile_page(const KernelArgs &a, const Piece &w, int j, int run_shift)
     const int64_t p = (int64_t)j * kTileN + (lane << run_shift);
     int page = -1;
     if (lane < (kTileN >> run_shift) && p < w.hi && p + (1 << run_shift) > w.lo)
-        page = w.pages[(int)p >> a.page_shift];  // (inside the table: hi is)
+        if (QDQ_CHECK(&g_attend_status, ((int)p >> a.page_shift) >= 0 && ((int)p >> a.page_shift) < a.max_pages))
+            page = w.pages[(int)p >> a.page_shift];  // (inside the table: hi is)
     return page;
 }
 
@@ -411,7 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(bar(kBarQFull), tiles * L::kHalves * q_rows * 128u);
                     for (int i = 0; i < tiles; ++i)
                         for (int h = 0; h < L::kHalves; ++h)
-                            tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
+                            if (QDQ_CHECK(status, w.first + w.b.i0 + i * tq < a.n_tokens && (w.head + 1) * a.g.group <= a.n_heads &&
+                                                      q_rows * 128u <= 16384u))
+                                tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
                                         w.first + w.b.i0 + i * tq, bar(kBarQFull));
                 }
                 int page = tile_page(a, piece, t0, run_shift);
@@ -429,7 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
                         if (lane == 0) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
                         __syncwarp();
-                        if (here >= 0)
+                        if (here >= 0 &&
+                            QDQ_CHECK(status, row8 >= a.row8_layer && w.head < a.g.kv_heads && lane * run_bytes + run_bytes <= L::kSlot &&
+                                                  row8 + (1 << run_shift >> 3) <= a.row8_layer + (int)(((int64_t)a.n_pages << a.page_shift) >> 3)))
                             tma_load_4d(sb + L::kRing + slot * L::kSlot + (uint32_t)lane * run_bytes, kv ? &v_map : &k_map, 0,
                                         0, w.head * L::kHalves, row8, bar(kBarFull + slot));
                     }
@@ -747,7 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         char *row = smem + L::kRing + (vs % L::kSlots) * L::kSlot + (r / 8) * L::kGroup8 + (r % 8) * 128;
 #pragma unroll
                         for (int k = 0; k < HD / 8; ++k)
-                            *reinterpret_cast<uint4 *>(row + (k / 8) * 1024 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+                            if (QDQ_CHECK(status, row + (k / 8) * 1024 + (k % 8) * 16 + 16 <= smem + L::kBars))
+                                *reinterpret_cast<uint4 *>(row + (k / 8) * 1024 + (k % 8) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_async_smem();
                 }
@@ -815,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const int64_t first_token = w.token0 + qi * tq, first_head = (int64_t)w.head * a.g.group;
             auto put8 = [&](int64_t at, const float *o, float f) {
+                if (!QDQ_CHECK(status, at >= 0 && at % 8 == 0 && at + 8 <= (a.n_tokens - 1) * a.out_stride + (int64_t)a.n_heads * HD)) return;
                 if constexpr (OUT32) {
                     float4 *to = reinterpret_cast<float4 *>((float *)a.out + at);
                     to[0] = make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
@@ -855,7 +862,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // partial state: O as [column / 4][row][4], so that rows of a warp are contiguous
             const int c_first = w.c_first, c_last = w.c_last;
             done();
-            auto part_of = [&](int cta) { return (cta * 2 + (cta == c_first ? 1 : 0)) * 2 + i; };
+            auto part_of = [&](int cta) {
+                const int part = (cta * 2 + (cta == c_first ? 1 : 0)) * 2 + i;
+                return QDQ_CHECK(status, part >= 0 && part < 4 * (int)gridDim.x) ? part : i;
+            };
             // One more part onto a joined state, in CTA order on every path: g and f are the factors
             // of what is there and of what comes.
             auto onto = [](float2 p, float &M, float &S, float &g, float &f) {
@@ -871,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Many rows, and the other parts are all written: this one is joined as it is, a thread
             // its row (writing it and reading all back costs some 15 000 clocks at 128 rows).
-            unsigned *counter = a.counters + 2 * c_first + i;
+            unsigned *counter = a.counters + (QDQ_CHECK(status, c_first >= 0 && c_first < (int)gridDim.x) ? 2 * c_first : 0) + i;
             const int pieces = rows * (HD / 8);
             if (pieces > 256) {
                 if (r == 0) {

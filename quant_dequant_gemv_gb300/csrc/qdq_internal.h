@@ -95,6 +95,9 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out);
 void attend_destroy(AttendState *st);
 int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t stream);
 int take_status_attend();
+// Of the append and of sampling, which wait for nothing: what a debug build's checks recorded.
+int take_status_append();
+int take_status_sample();
 
 // While a caller's stream is being captured into a CUDA graph, one-time setup calls
 // (kernel attributes, occupancy queries, memory-pool creation) would invalidate a

@@ -11,6 +11,10 @@
 namespace qdq {
 namespace {
 
+#ifdef QDQ_DEBUG
+__device__ int g_append_status;
+#endif
+
 struct AppendArgs {
     int n_seqs, n_tokens, max_pages;
     const int32_t *q_start, *kv_len, *page_table;
@@ -63,7 +67,8 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
             const TI *src = is_q   ? (const TI *)a.q + (int64_t)t * a.q_stride + r * D
                             : is_k ? (const TI *)a.k + (int64_t)t * a.k_stride + (r - a.n_heads) * D
                                    : (const TI *)a.v + (int64_t)t * a.v_stride + (r - a.n_heads - a.n_kv_heads) * D;
-            if (rb + y * RW < r1) {  // (the whole warp)
+            if (rb + y * RW < r1 && QDQ_CHECK(&g_append_status, t < a.n_tokens && r >= 0 && r < rows && c0 + 4 <= D && c1 + 4 <= D &&
+                                                                    ((uintptr_t)(src + c0) | (uintptr_t)(src + c1)) % (4 * sizeof(TI)) == 0)) {  // (the whole warp)
                 load4(src + c0, x[y]);
                 load4(src + c1, x[y] + 4);
             }
@@ -136,6 +141,9 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
             TC *dst = is_q   ? (TC *)a.q_out + ((int64_t)t * a.n_heads + r) * D
                       : is_k ? (TC *)a.k_pages + (slot * a.n_kv_heads + r - a.n_heads) * D
                              : (TC *)a.v_pages + (slot * a.n_kv_heads + r - a.n_heads - a.n_kv_heads) * D;
+            if (!QDQ_CHECK(&g_append_status, (is_q || (slot >> a.page_shift) < a.n_pages) && r < rows &&
+                                                 (uintptr_t)(dst + c0) % (INTERLEAVED ? 16 : 8) == 0 && (uintptr_t)(dst + c1) % 8 == 0))
+                continue;
             // (v's values were loaded from the same two places and are only rounded)
             const uint2 lo2 = make_uint2(Float16<TC>::pack(v[0], v[1]), Float16<TC>::pack(v[2], v[3]));
             const uint2 hi2 = make_uint2(Float16<TC>::pack(v[4], v[5]), Float16<TC>::pack(v[6], v[7]));
@@ -179,6 +187,20 @@ int launch_append(AppendArgs a, bool in_f32, bool bf16, bool interleaved, int he
 }
 
 }  // namespace
+
+int take_status_append() {
+    int v = 0;
+#ifdef QDQ_DEBUG
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_append_status, sizeof(int)) != cudaSuccess ||
+        (v && cudaMemcpyToSymbol(g_append_status, &zero, sizeof(int)) != cudaSuccess)) {
+        cudaGetLastError();
+        return QDQ_ERR_CUDA;
+    }
+#endif
+    return v;
+}
+
 }  // namespace qdq
 
 using namespace qdq;

@@ -53,6 +53,10 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr uint32_t kLowest = 0x00800000u;  // the key of the lowest finite logit (-inf is one below)
 typedef unsigned long long u64;
 
+#ifdef QDQ_DEBUG
+__device__ int g_sample_status;
+#endif
+
 struct SampleArgs {
     const void *logits;
     int64_t stride;
@@ -195,6 +199,9 @@ struct Row {
     }
     QDQ_DEV u64 part(uint32_t r, int i) const { return sh.sums[turn_s ^ 1][r][i]; }
 
+    QDQ_DEV void count(int piece, int b, unsigned v) {
+        if (QDQ_CHECK(&g_sample_status, b >= 0 && b < kBins)) atomicAdd(&sh.bins[turn_b][piece][b], v);
+    }
     QDQ_DEV void clear_bins(int pieces) {
         for (int i = 0; i < pieces; ++i) sh.bins[turn_b][i][tid] = 0;
         __syncthreads();
@@ -202,7 +209,7 @@ struct Row {
     QDQ_DEV void add_mass(int b, float w) {
         unsigned p[3];
         pieces(w, p);
-        for (int i = 0; i < 3; ++i) atomicAdd(&sh.bins[turn_b][i][b], p[i]);
+        for (int i = 0; i < 3; ++i) count(i, b, p[i]);
     }
     // Bin `tid` over the whole cluster (each CTA reads all the others'): PIECES of mass, or a
     // count with PIECES = 1. Ends the turn.
@@ -305,7 +312,7 @@ struct Row {
                 sum += get(x[y], (uint32_t)(i_first + i + y), k);
             }
             sum = __reduce_add_sync(kAll, sum);
-            if (lane == 0 && sum) atomicAdd(&sh.bins[turn_b][0][(i_first + i0) >> shift], sum);
+            if (lane == 0 && sum) count(0, (i_first + i0) >> shift, sum);
         }
     }
 
@@ -332,7 +339,7 @@ struct Row {
                     if (!get(x, index, k) || k < lo || k > hi) return;
                     const int b = (int)((hi - k) >> shift);
                     if (MASS) add_mass(b, weight(x));
-                    else atomicAdd(&sh.bins[turn_b][0][b], 1u);
+                    else count(0, b, 1u);
                 });
             }
             const u64 v = gather_bins<ALONE, MASS ? 3 : 1>();
@@ -367,12 +374,12 @@ struct Row {
         clear_bins(1);
         each<ALONE>([&](float x, uint32_t) {
             const int k = bin_of(x);
-            if (k < kBins - 1) atomicAdd(&sh.bins[turn_b][0][k], 1u);
+            if (k < kBins - 1) count(0, k, 1u);
         });
-        const u64 count = gather_bins<ALONE, 1>();
+        const u64 counted = gather_bins<ALONE, 1>();
         u64 all;
-        const u64 excl = before(count, &all);
-        find(tid == kBins - 1 ? total - excl : count, excl, top_k);
+        const u64 excl = before(counted, &all);
+        find(tid == kBins - 1 ? total - excl : counted, excl, top_k);
         bin = (int)sh.found[0] & (kBins - 1);
         ahead = sh.found[1];
     }
@@ -450,7 +457,8 @@ struct Row {
         uint32_t to = remote(&sh.list[0], 0) + 8 * ((uint32_t)at + before((unsigned)__popcll(own), &all));
         for (; own; own &= own - 1, to += 8) {
             const int k = __ffsll(own) - 1, e = 4 * tid + (k >> 2) * 4 * kThreads + (k & 3);
-            store_remote(to, ((u64)key_of(sh.x[e]) << 32) | (uint32_t)~(uint32_t)(i_first + e));
+            if (QDQ_CHECK(&g_sample_status, to - remote(&sh.list[0], 0) < 8u * kList && e < n))
+                store_remote(to, ((u64)key_of(sh.x[e]) << 32) | (uint32_t)~(uint32_t)(i_first + e));
         }
         cluster_sync();
         return true;
@@ -517,7 +525,8 @@ struct Row {
             u64 excl = ahead + incl - own;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                if (excl < target && target <= excl + f[y]) {
+                if (excl < target && target <= excl + f[y] &&
+                    QDQ_CHECK(&g_sample_status, i_first + i0 + 4 * lane + y < a.vocab && b < a.rows)) {
                     a.tokens[b] = (int64_t)(i_first + i0 + 4 * lane + y);
                     if (a.logprobs) a.logprobs[b] = share_log(w[y], whole);
                 }
@@ -612,7 +621,7 @@ struct Row {
                                         &whole_mass, &a, b);
         const uint32_t token = ~inverted;
         each<ALONE>([&](float x, uint32_t index) {
-            if (index != token) return;
+            if (index != token || !QDQ_CHECK(&g_sample_status, token < (uint32_t)a.vocab && b < a.rows)) return;
             a.tokens[b] = (int64_t)token;
             if (a.logprobs) a.logprobs[b] = share_log(weight(x), whole_mass);
         });
@@ -672,7 +681,8 @@ struct Row {
             if ((uint32_t)sorted[j] >= (uint32_t)at) sum += mass[j];  // (inverted: an index not above this one)
         sum += __shfl_xor_sync(kAll, sum, 1);
         sum += __shfl_xor_sync(kAll, sum, 2);
-        if (q == 0 && f && sum >= target && sum - f < target) {
+        if (q == 0 && f && sum >= target && sum - f < target &&
+            QDQ_CHECK(&g_sample_status, (uint32_t)~(uint32_t)at < (uint32_t)a.vocab && b < a.rows)) {
             a.tokens[b] = (int64_t)(uint32_t)~(uint32_t)at;
             if (a.logprobs) a.logprobs[b] = share_log(weight(value_of((uint32_t)(at >> 32))), whole);
         }
@@ -719,15 +729,18 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         done = r.n & ~3;
 #pragma unroll 4
         for (int i = 4 * tid; i < done; i += 4 * kThreads) {
+            if (!QDQ_CHECK(&g_sample_status, i + 4 <= a.slice && r.i_first + i + 4 <= a.vocab && b < a.rows)) break;
             float x[4];
             load4(src + i, x);
             *reinterpret_cast<float4 *>(sh.x + i) = make_float4(put(x[0], i), put(x[1], i + 1), put(x[2], i + 2), put(x[3], i + 3));
         }
     }
 #pragma unroll 8
-    for (int i = done + tid; i < r.n; i += kThreads) sh.x[i] = put((float)src[i], i);
+    for (int i = done + tid; i < r.n; i += kThreads)
+        if (QDQ_CHECK(&g_sample_status, i < a.slice && r.i_first + i < a.vocab && b < a.rows)) sh.x[i] = put((float)src[i], i);
     u64 best = top_i < 0 ? 0 : ((u64)key_of(top_x) << 32) | (0xFFFFFFFFu - (unsigned)(r.i_first + top_i));
-    for (int i = r.n + tid; i < (r.n + 127) / 128 * 128; i += kThreads) sh.x[i] = -INFINITY;
+    for (int i = r.n + tid; i < (r.n + 127) / 128 * 128; i += kThreads)
+        if (QDQ_CHECK(&g_sample_status, i < a.slice)) sh.x[i] = -INFINITY;
     for (int i = 0; i < 3; ++i) sh.bins[0][i][tid] = 0;
     const uint32_t mine = (uint32_t)(best >> 32);  // (0, which is no logit's, for a thread without any)
 #pragma unroll
@@ -767,7 +780,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
     if (maxima) {
         const int k = mine >= kLowest ? r.bin_of(value_of(mine)) : kBins - 1;
         __syncthreads();
-        if (k < kBins - 1) atomicAdd(&sh.bins[0][0][k], 1u);
+        if (k < kBins - 1) r.count(0, k, 1u);
         const u64 count = r.gather_bins<false, 1>();
         const u64 ahead = r.before(count, &all);
         r.find(count, ahead, (u64)top_k);  // (the open bin if there are not as many)
@@ -798,7 +811,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
         r.send<false>(__reduce_add_sync(kAll, __popcll(own)), __reduce_add_sync(kAll, __popcll(in_bin)), ctas);
         cluster_sync();
         if (r.gather_list(own, 0, listed)) {
-            if (rank) return;
+            if (rank || !QDQ_CHECK(&g_sample_status, listed <= kList)) return;
             r.n = (int)listed;
             if (listed <= kFew) r.finish_few(a, b, first, share, floor_w);
             else r.finish<true>(a, b, first, share, floor_w);
@@ -844,6 +857,20 @@ int launch_sample(SampleArgs a, int sm_count, cudaStream_t stream) {
 }
 
 }  // namespace
+
+int take_status_sample() {
+    int v = 0;
+#ifdef QDQ_DEBUG
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_sample_status, sizeof(int)) != cudaSuccess ||
+        (v && cudaMemcpyToSymbol(g_sample_status, &zero, sizeof(int)) != cudaSuccess)) {
+        cudaGetLastError();
+        return QDQ_ERR_CUDA;
+    }
+#endif
+    return v;
+}
+
 }  // namespace qdq
 
 using namespace qdq;
