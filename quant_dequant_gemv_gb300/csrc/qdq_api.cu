@@ -305,6 +305,8 @@ static int plan_create(const qdq_gemv_desc *descs, const qdq_gemv_opts *opts, co
     if (has_argmax && (cudaMalloc((void **)&p->amax, 2 * sizeof(unsigned long long)) != cudaSuccess ||
                        cudaMemset(p->amax, 0, 2 * sizeof(unsigned long long)) != cudaSuccess))
         return fail(QDQ_ERR_CUDA);
+    // The clearing is asynchronous and in the default stream, which non-blocking streams do not follow.
+    if (cudaStreamSynchronize(nullptr) != cudaSuccess) return fail(QDQ_ERR_CUDA);
     if ((rc = stream_plan_build(descs, opts, level, n, batch, p->counters, p->amax, dev.sm_count, &p->host)))
         return fail(rc);
     *plan_out = p;

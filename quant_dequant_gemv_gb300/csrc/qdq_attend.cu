@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (QDQ_CHECK(status, w.first + w.b.i0 + i * tq < a.n_tokens && (w.head + 1) * a.g.group <= a.n_heads &&
                                                       q_rows * 128u <= 16384u))
                                 tma_load_3d(sb + L::kQ + i * L::kQTile + h * 16384u, &q_map, h * 64, w.head * a.g.group,
-                                        w.first + w.b.i0 + i * tq, bar(kBarQFull));
+                                            w.first + w.b.i0 + i * tq, bar(kBarQFull));
                 }
                 int page = tile_page(a, piece, t0, run_shift);
                 for (int j = 0; j < n; ++j) {

@@ -41,6 +41,14 @@ def test_a_cache_is_ready_on_every_stream_when_create_returns():
     assert copy < clear < wait < create.index("*out = c;")
 
 
+def test_a_plan_and_a_model_are_ready_on_every_stream_when_create_returns():
+    """The same for a plan's counters, and for a model, whose memory is cleared before its plan is made."""
+    create = body("qdq_api.cu", "static int plan_create(")
+    assert create.rindex("cudaMemset(") < create.index("cudaStreamSynchronize(nullptr)") < create.index("*plan_out = p;")
+    model = body("qdq_llama.cu", "int qdq_llama_create(")
+    assert model.rindex("cudaMemset(") < model.index("plan_create_with_attention(")
+
+
 def test_the_build_refuses_other_register_counts():
     from quant_dequant_gemv_gb300 import build
     entry = "ptxas info    : Compiling entry function '_ZN3qdq{}ILi64EEE' for 'sm_103a'\nptxas info    : Used {} registers, used 1 barriers\n"
