@@ -374,8 +374,9 @@ void qdq_paged_destroy(qdq_paged *cache);
 /* qdq_paged_append: one pass over the new tokens' q, k and v rows.
  *   y = x / sqrt(mean(x^2) + eps) * w over each head (q_norm, k_norm: fp32
  *       [head_dim], or NULL for none),
- *   q and k turned at their token's position (angles reduced exactly, so far
- *   positions lose nothing), all arithmetic in fp32,
+ *   q and k turned at their token's position (angles reduced modulo a turn
+ *   exactly, from frequencies within 2^-54 turn, so up to position 2^28 they are
+ *   those of the formula to fp32's rounding), all arithmetic in fp32,
  *   q_out[n_tokens][n_heads * head_dim] = q in the pools' type; k and v rounded
  *   to the pools' type and stored in `layer` of the pools (one rounding each).
  * in_type: QDQ_F32 (a GEMV's output) or the pools' type. Row strides are in
@@ -395,11 +396,12 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * the pools' type or QDQ_F32; row strides in elements, rows 16-byte aligned.
  * lse (NULL or fp32 [n_tokens][n_heads]): log sum_j exp(scale * q . k_j).
  * Scores, maxima, sums and the accumulator are fp32. The softmax weights meet v in
- * the pools' type, as its matrix product takes them: in two terms, which keep 16
- * bits of a weight or more, for an fp32 out and for sequences (or last pieces of
- * them) of at most 128 / (n_heads / n_kv_heads) new tokens; otherwise rounded once,
- * which is an error of the size of the 16-bit out's own rounding. (fp16 also has a
- * smallest step: weights may be off by 2^-32 of the largest that the row has.) A token with
+ * the pools' type, as its matrix product takes them. A sequence's new tokens are
+ * taken in blocks of 2 t, t = 128 / (n_heads / n_kv_heads); a block of at most t (a
+ * single token, a short last piece) and any block of an fp32 out have the weights
+ * in two terms, which keep 16 bits of each or more; other blocks have them rounded
+ * once, an error of the size of the 16-bit out's own rounding. (fp16's smallest
+ * step: a weight may be off by 2^-32 of the row's largest besides.) A token with
  * nothing to attend to gets a zero row and lse = -inf. Keys and values of
  * positions outside a sequence's range are never used, whatever they hold; values
  * inside it are taken to be finite (a position that only later tokens of a chunk

@@ -5,9 +5,9 @@
 // in one pass over the keys with a running maximum m and sum l (fp32). For a tile of 128
 // rows (tokens x the query heads that share a kv head) and a tile of 128 positions,
 // S = Q K^T goes to tensor memory, 128 threads take a row each, write P back, and O += P V
-// accumulates in tensor memory. The maximum that p is taken against lags
-// the true one by up to 2^8, so that O is rescaled a few times a row and not every tile;
-// the factor cancels in o and in l.
+// accumulates in tensor memory. The maximum that p is taken against lags the true one by up
+// to 2^8, so that O is rescaled a few times a row and not every tile; the factor cancels in
+// o and in l.
 //
 // The matrix instruction takes P in the cache's 16-bit type. A weight rounded to it once is off by
 // as much as a 16-bit result is by its own rounding (the whole error is 1.37 times that); two
@@ -40,13 +40,13 @@
 // The copying warp walks the range and publishes each piece; the rest follow it.
 //
 // What bounds it, as measured (GB300; 32 query and 8 kv heads of 128 unless said):
-// * single tokens: HBM. 64 sequences of 30 to 8192 positions 184 to 189 us = 6.3 to 6.5 TB/s, 93
-//   to 96 % of the copy rate; one sequence of 131001 positions 92.5 us, 85 % (the rest is the
+// * single tokens: HBM. 64 sequences of 30 to 8192 positions 190 to 196 us = 6.1 to 6.3 TB/s, 90
+//   to 93 % of the copy rate; one sequence of 131001 positions 91.5 to 93 us, 85 % (the rest is the
 //   start, the first tile's latency and the join, about 10 us, which is all of a 520-position
-//   call, and the second term of an fp16 cache's weights).
+//   call, and the weights' second term).
 // * prompts: the chain S -> softmax -> P V -> next S of each set, about 3000 clocks a tile
-//   where the matrix instructions of both sets need 2048: 8191 tokens 406 us = 1.35 PFLOP/s,
-//   68 % of the cuBLAS bf16 rate, tensor pipe 62 % busy. At 64 dims the softmax alone (some
+//   where the matrix instructions of both sets need 2048: 8191 tokens 412 us = 1.33 PFLOP/s,
+//   67 % of the cuBLAS bf16 rate, tensor pipe 59 % busy. At 64 dims the softmax alone (some
 //   2500 clocks a tile and set) bounds it.
 //
 // Values in rows of V outside the block's positions are zeroed in shared memory before

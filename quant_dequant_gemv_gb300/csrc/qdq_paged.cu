@@ -35,10 +35,12 @@ struct AppendArgs {
 // vector. A warp takes `rows_per_warp` of one token's n_heads + 2 n_kv_heads rows: a
 // lane sits at the same place of every row, so the angles are formed once per warp.
 // Angles: position * frequency in turns, modulo one turn, is a 64-bit integer product
-// that wraps (the frequency is kept in units of 2^-64 turn), so its error is 2^-65
-// turn per position whatever the position; the fraction then goes through sincospi.
+// that wraps (the frequency is kept in units of 2^-64 turn), so the reduction is exact; the
+// frequency itself comes from doubles and is off by at most 2^-54 turn (2^-55.1 found over
+// bases 2 to 8e6), which up to position 2^28 is less than the fraction's own rounding to
+// fp32. The fraction then goes through sincospi.
 // Bound by HBM: 274 MB (7436 tokens of 32 + 2 x 8 heads of 128, fp32 in, bf16 out) in
-// 51 us = 5.34 TB/s, 79 % of the copy rate with issue slots half used; a few tokens take 2.6 us,
+// 51 us = 5.38 TB/s, 79 % of the copy rate with issue slots half used; a few tokens take 2.7 us,
 // which is the launch and three dependent loads.
 template <typename TI, typename TC, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
@@ -165,9 +167,10 @@ int launch_append_typed(const AppendArgs &a, bool interleaved, unsigned grid, cu
 
 int launch_append(AppendArgs a, bool in_f32, bool bf16, bool interleaved, int head_dim, cudaStream_t stream,
                   int sm_count) {
-    // A warp takes up to 12 steps of a token's rows (7436 tokens of 32 + 2 x 8 heads of 128: 53.2
-    // us, against 55.1 at 8, 60.6 at 4 and 55.3 with whole tokens, whose last wave of warps is
-    // ragged); with few tokens fewer, down to one, until about 16 warps per SM have work.
+    // A warp takes up to 12 steps of a token's rows (7436 tokens of 32 + 2 x 8 heads of 128, launches
+    // that wait for each other: 53.2 us, against 55.1 at 8, 60.6 at 4 and 55.3 with whole tokens,
+    // whose last wave of warps is ragged; 51 us with launches that follow one another); with few
+    // tokens fewer, down to one, until about 16 warps per SM have work.
     const int rows = a.n_heads + 2 * a.n_kv_heads, rw = 256 / head_dim;
     const int steps = (rows + rw - 1) / rw;
     const int64_t want = ((int64_t)sm_count * 16 + a.n_tokens - 1) / a.n_tokens;

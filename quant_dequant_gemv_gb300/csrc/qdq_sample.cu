@@ -28,7 +28,7 @@
 //
 // Bound by latency, not by the read: a row is some 15 dependent steps, of which a list takes
 // five. Measured (GB300, 1 x 32000 / 64 x 32000 / 256 x 131071 logits, filters mixed):
-// 10.0 / 26.0 / 166 us; a listed row of 32000 takes 15 000 clocks from its first load, one
+// 10.0 / 26 / 171 us (158 to 179 between runs); a listed row of 32000 takes 15 000 clocks from its first load, one
 // whose nucleus is a large part of the vocabulary 43 000, of which the pass that bins the
 // masses (three shared-memory atomics an entry) and the draw's pass take 7000 and 6000.
 //
