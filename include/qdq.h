@@ -347,7 +347,7 @@ void qdq_llama_destroy(qdq_llama *model);
  *                        is not written and not attended to.
  * n_seqs <= 1024, max_pages * page_size <= 2^30 (QDQ_ERR_LIMIT).
  * ------------------------------------------------------------------------- */
-enum qdq_float_type { QDQ_F32 = 1, QDQ_F16 = 2, QDQ_BF16 = 3 };
+enum qdq_float_type { QDQ_F32 = 1, QDQ_F16 = 2, QDQ_BF16 = 3, QDQ_E4M3 = 4 };
 
 typedef struct qdq_paged_config {
     int32_t type;             /* of the pools: QDQ_F16 or QDQ_BF16 */
@@ -364,11 +364,19 @@ typedef struct qdq_paged_batch {
     const int32_t *q_start, *kv_len, *page_table;
 } qdq_paged_batch;
 typedef struct qdq_paged qdq_paged;
-/* The pools must outlive the handle. Attention calls of one handle must not overlap on
+/* A cache of e4m3 values (type QDQ_E4M3) keeps each key and value in eight bits, with a
+ * scale for each 16 positions (of one page) and head: a value is its e4m3 value times
+ * 2^(b - 127), b the scale's byte, with b - 127 in -40 .. 40 (others count as the nearest of
+ * those). Pools: [n_layers][n_pages][n_kv_heads][page_size][head_dim] (a page's heads one
+ * after the other), scales [n_layers][n_pages][n_kv_heads][page_size / 16]. Queries are fp16;
+ * append takes fp32, fp16 or bf16 rows, and attention gives any of them. */
+/* The pools must outlive the handle, and so must the scales. Attention calls of one handle must not overlap on
  * the GPU (they share the workspace); use one handle per stream otherwise. If
  * qdq_get_device_status() reports QDQ_ERR_TIMEOUT after one, destroy the handle and
  * create another before the next. */
 int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, qdq_paged **out);
+int qdq_paged_create_e4m3(const qdq_paged_config *cfg, void *k_pages, void *v_pages, uint8_t *k_scales,
+                          uint8_t *v_scales, qdq_paged **out);
 void qdq_paged_destroy(qdq_paged *cache);
 
 /* qdq_paged_append: one pass over the new tokens' q, k and v rows.
@@ -381,7 +389,14 @@ void qdq_paged_destroy(qdq_paged *cache);
  *   to the pools' type and stored in `layer` of the pools (one rounding each).
  * in_type: QDQ_F32 (a GEMV's output) or the pools' type. Row strides are in
  * elements; every row 16-byte aligned. A token at a negative position (kv_len
- * below its sequence's new tokens) gets a zero q_out row and is not stored. */
+ * below its sequence's new tokens) gets a zero q_out row and is not stored.
+ * Into a cache of e4m3 values: q_out is fp16 (values beyond its range become its largest).
+ * A block of 16 positions and a head gets the least e in -40 .. 40 with |x| <= 448 * 2^e for
+ * each finite new x; where the block begins with earlier positions, not less than its own e,
+ * and if that grows, their values are rescaled (exact but for values that fall below e4m3's
+ * normal range, 2^-6 * 2^e, which are rounded again). x * 2^-e is rounded once to e4m3;
+ * infinities become 448 * 2^e of their sign, what is no number stays none. Rows of a block
+ * behind the new ones are left as they are. No two sequences of a call may write to one page. */
 int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, int in_type, const void *q,
                      int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                      const float *q_norm, const float *k_norm, float eps, void *q_out, qdq_stream_t stream);
@@ -406,10 +421,52 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * positions outside a sequence's range are never used, whatever they hold; values
  * inside it are taken to be finite (a position that only later tokens of a chunk
  * attend to has weight zero for the earlier ones, and 0 x inf is no number).
+ * Over a cache of e4m3 values the query meets the keys' e4m3 values exactly and their scales
+ * in fp32; a weight with its value's scale in it meets the values in two fp16 terms.
  * One launch; results do not depend on timing (no floating-point atomics). */
 int qdq_paged_attention(qdq_paged *cache, int layer, const qdq_paged_batch *batch, const void *q, int64_t q_stride,
                         int out_type, void *out, int64_t out_stride, float scale, int window, float *lse,
                         qdq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over a few pages of a long sequence, chosen for each token and kv head. No
+ * counterpart on the pages. Caches of any type; a page's number in these calls is its place
+ * in the sequence's page table (positions number * page_size on).
+ *
+ * qdq_paged_key_bounds: bounds of the keys of each page that holds a new token of the batch
+ * (call it after the append), over the page's positions below kv_len, for every kv head:
+ *   E the least in -100 .. 121 with |k| <= 127 * 2^E (121 where a key is infinite),
+ *   bounds[0][d] = ceil(max k_d * 2^-E), bounds[1][d] = floor(min k_d * 2^-E),
+ * bounds: int8 [n_layers][n_pages][n_kv_heads][2][head_dim], 16-byte aligned; scales: bytes
+ * E + 127, [n_layers][n_pages][n_kv_heads]; both the caller's, by page of the pool. Keys that are
+ * no number do not count. Pages without a new token keep their bounds.
+ *
+ * qdq_paged_select_pages: for each token at position p and each kv head, the numbers of
+ * n_select of the pages that hold positions up to p (those with a page in the table), in
+ * rising order, then -1: pages[n_tokens][n_kv_heads][n_select], int32. Fewer pages than
+ * n_select: all of them. The first n_first and the last n_last of the sequence's pages up to
+ * p's are taken always (n_first + n_last <= n_select), of the others those of the highest score,
+ * the lowest number first among equals. The score of a page is the largest over the kv
+ * head's query heads of
+ *   2^s * sum_d qi_d * bounds[qi_d < 0][d]    (of bounds, the largest that qi . k can be),
+ * qi = rint(q * 2^-Eq) with Eq for the head's q as E for the keys, s = Eq + E inside -100 .. 100:
+ * an integer times a power of two, so the selection is exact. It ranks pages by how large scale *
+ * q . k can be for a positive scale. q as for attention. max_pages <= 32768 (QDQ_ERR_LIMIT). Rows
+ * of no sequence are not written; a token at a negative position gets -1 throughout.
+ *
+ * qdq_paged_attention_pages: as qdq_paged_attention without a window, over the positions up to
+ * the token's own that lie in the listed pages: pages as above. An entry counts if it is not
+ * negative and larger than the one before it. A token with nothing to attend to gets a zero row
+ * and lse = -inf. The weights meet the values in two terms. Uses the handle's workspace.
+ * ------------------------------------------------------------------------- */
+int qdq_paged_key_bounds(qdq_paged *cache, int layer, const qdq_paged_batch *batch, int8_t *bounds, uint8_t *scales,
+                         qdq_stream_t stream);
+int qdq_paged_select_pages(qdq_paged *cache, int layer, const qdq_paged_batch *batch, const void *q, int64_t q_stride,
+                           const int8_t *bounds, const uint8_t *scales, int n_select, int n_first, int n_last,
+                           int32_t *pages, qdq_stream_t stream);
+int qdq_paged_attention_pages(qdq_paged *cache, int layer, const qdq_paged_batch *batch, const void *q, int64_t q_stride,
+                              const int32_t *pages, int n_select, int out_type, void *out, int64_t out_stride,
+                              float scale, float *lse, qdq_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * qdq_sample: the next token of each row of logits, from given random numbers.

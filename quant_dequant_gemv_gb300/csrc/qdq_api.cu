@@ -400,7 +400,10 @@ int qdq_get_device_status(qdq_stream_t stream) {
     const int c = take_status_attend();
     const int d = take_status_append();
     const int e = take_status_sample();
-    return a != QDQ_OK ? a : a1 != QDQ_OK ? a1 : b != QDQ_OK ? b : c != QDQ_OK ? c : d != QDQ_OK ? d : e;
+    const int more[] = {take_status_append8(), take_status_rows(), take_status_pages()};
+    int rc = a != QDQ_OK ? a : a1 != QDQ_OK ? a1 : b != QDQ_OK ? b : c != QDQ_OK ? c : d != QDQ_OK ? d : e;
+    for (int m : more) rc = rc != QDQ_OK ? rc : m;
+    return rc;
 }
 
 int qdq_selftest_wait_timeout(int64_t timeout_ns, qdq_stream_t stream) {

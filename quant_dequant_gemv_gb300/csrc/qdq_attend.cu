@@ -58,7 +58,7 @@
 #include <new>
 #include <type_traits>
 
-#include "qdq_attend_plan.h"
+#include "qdq_attend_walk.cuh"
 #include "qdq_internal.h"
 #include "qdq_paged.cuh"
 #include "qdq_tcgen05.cuh"
@@ -131,58 +131,6 @@ constexpr int kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 21, kBa
               kBarOFree = 28, kBarDrain = 30, kBarPiece = 31, kBarPieceFree = 33,
               kBarSFree = 35;
 
-struct Start {
-    long long total, item, pos, end;  // units: of all items, where the first one begins, the CTA's range
-    int seq, block, head, ctas, live;
-};
-
-// A walk over the pieces of a CTA's range, by the copying warp.
-struct Walk {
-    long long item, pos, end;  // units: where the item begins, the rest of the range
-    int seq, block, head, off, n;  // the piece: n key tiles from the item's off-th on
-    int first, count, kv, blocks;
-    const int32_t *pages;  // the sequence's page table
-    AttendBlock b;
-    QDQ_DEV void load_seq(const KernelArgs &a) {
-        seq_tokens(a.q_start, seq, a.n_tokens, first, count);
-        kv = max(a.kv_len[seq], 0);
-        blocks = seq_blocks(a.g, count);
-        pages = a.page_table + (int64_t)seq * a.max_pages;
-    }
-    QDQ_DEV Walk(const KernelArgs &a, const Start &s)
-        : item(s.item), pos(s.pos), end(s.end), seq(s.seq), block(s.block), head(s.head) {
-        load_seq(a);
-        b = block_of(a.g, count, kv, block);
-        int last;
-        piece_of(b, item, pos, end, off, last);
-        n = last - off;
-        if (n == 0) next(a);  // (the range begins past the item's tiles or ends before them)
-    }
-    QDQ_DEV bool more() const { return n > 0; }
-    QDQ_DEV int t_beg() const { return b.t0 + off; }
-    QDQ_DEV bool whole() const { return n == b.t1 - b.t0; }
-    QDQ_DEV void next(const KernelArgs &a) {
-        item += item_units(b);
-        pos = item;
-        n = 0;
-        if (item >= end) return;
-        if (++head == a.g.kv_heads) {
-            head = 0;
-            if (++block >= blocks) {
-                block = 0;
-                do {
-                    if (++seq >= a.n_seqs) return;  // (only if the batch changed under the kernel)
-                    load_seq(a);
-                } while (count == 0);
-            }
-            b = block_of(a.g, count, kv, block);
-        }
-        int last;
-        piece_of(b, item, pos, end, off, last);
-        n = last - off;  // 0 at the end of the range, where only the item's first units are left
-    }
-};
-
 // What the other warps need of a piece, in one of two places in shared memory.
 struct Piece {
     const int32_t *pages;  // the sequence's page table
@@ -214,105 +162,6 @@ QDQ_DEV float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-
-// Where the CTA's range starts: sums of key tiles per sequence, a scan, and a search.
-template <int HD>
-QDQ_DEV void find_start(const KernelArgs &a, char *smem, Start *start) {
-    using L = Shape<HD>;
-    int *cnt = reinterpret_cast<int *>(smem + L::kRing), *kvs = cnt + kMaxSeqs;
-    long long *pre = reinterpret_cast<long long *>(smem + L::kRing + 8 * kMaxSeqs);  // [n_seqs]
-    constexpr int kAlone = 8;  // blocks that one thread sums; longer sequences are summed by a warp
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    bool longer = false;
-    for (int s = tid; s < a.n_seqs; s += kThreads) {
-        int first, count;
-        seq_tokens(a.q_start, s, a.n_tokens, first, count);
-        const int kv = max(a.kv_len[s], 0), nb = seq_blocks(a.g, count);
-        cnt[s] = count;
-        kvs[s] = kv;
-        int sum = 0;
-        if (nb <= kAlone) {
-            for (int b = 0; b < nb; ++b) sum += item_units(block_of(a.g, count, kv, b));
-        } else {
-            longer = true;
-        }
-        pre[s] = (long long)sum * a.g.kv_heads;
-    }
-    if (__syncthreads_or(longer)) {
-        for (int s = warp; s < a.n_seqs; s += kThreads / 32) {
-            const int nb = seq_blocks(a.g, cnt[s]);
-            if (nb <= kAlone) continue;
-            long long sum = 0;
-            for (int b = lane; b < nb; b += 32) sum += item_units(block_of(a.g, cnt[s], kvs[s], b));
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            if (lane == 0) pre[s] = sum * a.g.kv_heads;
-        }
-        __syncthreads();
-    }
-    if (warp == 0) {
-        // a scan over lanes, each with a contiguous run of sequences
-        const int per = (a.n_seqs + 31) / 32, s0 = min(lane * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
-        long long mine = 0;
-        for (int s = s0; s < s1; ++s) mine += pre[s];
-        long long incl = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long e = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += e;
-        }
-        const long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-        const int ctas = (int)min((long long)gridDim.x, total);
-        const bool live = (int)blockIdx.x < ctas;
-        const long long x = live ? range_start(total, ctas, blockIdx.x) : 0;
-        const long long excl = incl - mine;
-        if (lane == 0) {
-            start->live = live;
-            start->ctas = ctas;
-            start->total = total;
-            start->pos = x;
-            start->end = live ? range_start(total, ctas, blockIdx.x + 1) : 0;
-        }
-        // the lane whose run of sequences holds x walks it
-        const unsigned owner = __ballot_sync(0xFFFFFFFFu, live && mine > 0 && excl <= x && x < incl);
-        int s = 0;
-        long long rem = 0;
-        if (owner && lane == __ffs(owner) - 1) {
-            rem = x - excl;
-            s = s0;
-            while (rem >= pre[s]) rem -= pre[s++];
-        }
-        if (owner) {
-            const int src = __ffs(owner) - 1;
-            s = __shfl_sync(0xFFFFFFFFu, s, src);
-            rem = __shfl_sync(0xFFFFFFFFu, rem, src);
-            // the block: 32 at a time
-            const int nb = seq_blocks(a.g, cnt[s]);
-            for (int b0 = 0; b0 < nb; b0 += 32) {
-                int n = 0;
-                if (b0 + lane < nb) n = item_units(block_of(a.g, cnt[s], kvs[s], b0 + lane));
-                long long run = (long long)n * a.g.kv_heads;
-                const long long own = run;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long e = __shfl_up_sync(0xFFFFFFFFu, run, o);
-                    if (lane >= o) run += e;
-                }
-                const unsigned m = __ballot_sync(0xFFFFFFFFu, rem < run);
-                if (m) {
-                    const int l = __ffs(m) - 1;
-                    if (lane == l) {
-                        const int r = (int)(rem - (run - own));
-                        start->seq = s;
-                        start->block = b0 + l;
-                        start->head = r / n;
-                        start->item = x - r % n;
-                    }
-                    break;
-                }
-                rem -= __shfl_sync(0xFFFFFFFFu, run, 31);
-            }
-        }
-    }
-    __syncthreads();
 }
 
 template <int HD, bool BF16, bool OUT32>
@@ -354,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(kBarDrain), 1);
         fence_mbar_init();
     }
-    find_start<HD>(a, smem, start);
+    find_start<kThreads>(a, smem + L::kRing, start);
     if (!start->live) return;
     const Start s0 = *start;
     __syncthreads();
@@ -1057,8 +906,8 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
     const cuuint64_t rows = (cuuint64_t)p.n_layers * p.n_pages * p.page_size;
     const cuuint64_t dims[4] = {64, 8, (cuuint64_t)blocks, rows / 8}, strides[3] = {row, 128, 8 * row};
     const cuuint32_t box[4] = {64, 8, (cuuint32_t)(p.head_dim / 64), (cuuint32_t)run / 8};
-    bool ok = encode(&st->k_map, p.bf16, 4, p.k_pages, dims, strides, box) &&
-              encode(&st->v_map, p.bf16, 4, p.v_pages, dims, strides, box);
+    bool ok = encode(&st->k_map, p.type == QDQ_BF16, 4, p.k_pages, dims, strides, box) &&
+              encode(&st->v_map, p.type == QDQ_BF16, 4, p.v_pages, dims, strides, box);
     st->ctas = sm_count;
     // two parts per CTA and set: 128 rows of O, a maximum and a sum; the joins' counters
     const size_t parts = (size_t)sm_count * 4, n_o = parts * 128 * p.head_dim * 4, n_s = parts * 128 * 8;
@@ -1066,7 +915,7 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
     ok = ok && cudaMalloc((void **)&st->mem, bytes) == cudaSuccess && cudaMemset(st->mem, 0, bytes) == cudaSuccess;
     for (bool out_f32 : {false, true}) {
         cudaFuncAttributes fa;  // (the kernel's shares of registers add up to its launch's)
-        const Kernel f = kernel_of(p.head_dim, p.bf16, out_f32);
+        const Kernel f = kernel_of(p.head_dim, p.type == QDQ_BF16, out_f32);
         ok = ok && cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == 168;
         ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(p.head_dim)) == cudaSuccess;
     }
@@ -1109,7 +958,7 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     k.part_o = st->part_o, k.part_ml = st->part_ml, k.counters = st->counters;
     // fp32 accumulators, both operands of the pools' type, M = 128; S: N = 128, both K-major
     // (a negative scale negates Q); O: N = head_dim, V is N-major
-    const uint32_t common = (1u << 4) | (p.bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTileM >> 4) << 24);
+    const uint32_t common = (1u << 4) | (p.type == QDQ_BF16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTileM >> 4) << 24);
     k.idesc_qk = common | ((uint32_t)(kTileN >> 3) << 17) | (a.scale < 0.0f ? 1u << 13 : 0u);
     k.idesc_pv = common | ((uint32_t)(p.head_dim >> 3) << 17) | (1u << 16);
     // Q as [token][head][dim]: a box is 64 dims of the group's heads of a tile's tokens
@@ -1118,8 +967,8 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     const cuuint64_t q_row = a.n_tokens > 1 ? (cuuint64_t)a.q_stride * 2 : (cuuint64_t)p.n_heads * p.head_dim * 2;
     const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, q_row};
     const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)k.g.tokens};
-    if (!encode(&q_map, p.bf16, 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
-    return launch_following(kernel_of(p.head_dim, p.bf16, a.out_f32), st->ctas, kThreads, smem_of(p.head_dim), 1, stream, k, q_map,
+    if (!encode(&q_map, p.type == QDQ_BF16, 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
+    return launch_following(kernel_of(p.head_dim, p.type == QDQ_BF16, a.out_type == QDQ_F32), st->ctas, kThreads, smem_of(p.head_dim), 1, stream, k, q_map,
                             st->k_map, st->v_map);
 }
 

@@ -1,8 +1,13 @@
 // qdq_attend_plan.h -- how the paged attention's work is cut, in plain integer
-// arithmetic that the kernel and a host test both compile (qdq_attend.cu).
+// arithmetic that the kernels and a host test both compile (qdq_attend.cu,
+// qdq_attend_rows.cu).
 //
 // Rows. The g query heads that share a kv head are rows of the same matrix: a tile of
-// kTileM rows holds kTileM / g whole tokens (row = token * g + head), a block two tiles.
+// kTileM rows holds kTileM / g whole tokens (row = token * g + head), a block two tiles
+// (in the kernel of few rows a block is one short tile of its own).
+// Lists. Where each token has a list of pages to attend to, a block is one token, and its
+// positions are places in the list: page after page, as many as the list can hold of those
+// up to the token's own.
 // Items. (sequence, block, kv head), in that order; an item's length is the number of
 // key tiles (kTileN positions) from the first one that any of its tokens attends to up
 // to the last.
@@ -33,6 +38,9 @@ struct AttendGeometry {
     int kv_heads;
     int window;       // 0: none
     int table_end;    // positions that the page table covers
+    int block = 0;    // tokens of a block; 0: two tiles
+    int list = 0;     // pages of a token's list; 0: none, every position is attended to
+    int page_shift = 0;  // (of a list) log2 of the page's positions
 };
 
 // One block of a sequence: its tokens i0..i1-1, the positions lo..hi-1 that some token
@@ -44,8 +52,9 @@ struct AttendBlock {
 
 QDQ_PLAN_FN int plan_min(int a, int b) { return a < b ? a : b; }
 QDQ_PLAN_FN int plan_max(int a, int b) { return a > b ? a : b; }
+QDQ_PLAN_FN int block_tokens(const AttendGeometry &g) { return g.block ? g.block : 2 * g.tokens; }
 QDQ_PLAN_FN int seq_blocks(const AttendGeometry &g, int count) {
-    const int b = 2 * g.tokens;
+    const int b = block_tokens(g);
     return count <= b ? (count > 0 ? 1 : 0) : (count + b - 1) / b;
 }
 
@@ -55,12 +64,27 @@ QDQ_PLAN_FN void span(const AttendGeometry &g, int p0, int n, int &lo, int &hi) 
     hi = plan_max(plan_min(p0 + n, g.table_end), 0);
 }
 
+// Places of the list of a token at position p: of that many of its pages, from the first on.
+QDQ_PLAN_FN int list_span(const AttendGeometry &g, int p) {
+    const int held = plan_max(plan_min(p + 1, g.table_end), 0), pages = (held + (1 << g.page_shift) - 1) >> g.page_shift;
+    return plan_min(g.list, pages) << g.page_shift;
+}
+
 // Block b of a sequence with `count` new tokens and kv positions in all.
 QDQ_PLAN_FN AttendBlock block_of(const AttendGeometry &g, int count, int kv, int b) {
     const int tq = g.tokens, base = kv - count;
     AttendBlock r;
-    r.i0 = b * 2 * tq;
-    r.i1 = plan_min(r.i0 + 2 * tq, count);
+    r.i0 = b * block_tokens(g);
+    r.i1 = plan_min(r.i0 + block_tokens(g), count);
+    if (g.list) {
+        r.lo = 0;
+        r.hi = list_span(g, base + r.i0);
+        r.t0 = 0;
+        r.t1 = plan_max((r.hi + kTileN - 1) / kTileN, 1);
+        r.tile_t0[0] = r.tile_t0[1] = r.tile_t1[1] = 0;
+        r.tile_t1[0] = r.hi > 0 ? r.t1 : 0;
+        return r;
+    }
     span(g, base + r.i0, r.i1 - r.i0, r.lo, r.hi);
     r.t0 = r.lo / kTileN;
     r.t1 = plan_max((r.hi + kTileN - 1) / kTileN, r.t0 + 1);  // a block with nothing to attend to is one empty tile

@@ -76,27 +76,73 @@ int take_status_mma();
 struct AttendPools {
     const void *k_pages, *v_pages;  // every layer
     int n_layers, n_pages, page_size, n_heads, n_kv_heads, head_dim;
-    bool bf16;
+    int type;                           // of the pools: QDQ_F16, QDQ_BF16 or QDQ_E4M3
+    const uint8_t *k_scales, *v_scales;  // of e4m3 pools
 };
 struct AttendArgs {
     const AttendPools *pools;
     int layer, n_seqs, n_tokens, max_pages;
     const int32_t *q_start, *kv_len, *page_table;
-    const void *q;      // [n_tokens][n_heads * head_dim] of the pools' type
-    void *out;          // of the pools' type, or fp32
+    const void *q;      // [n_tokens][n_heads * head_dim] of the pools' type (fp16 for e4m3 pools)
+    void *out;          // of out_type
     float *lse;         // [n_tokens][n_heads], or NULL
     int64_t q_stride, out_stride;  // elements
     float scale;
     int window;         // 0: none
-    bool out_f32;
+    int out_type;
+    const int32_t *lists = nullptr;  // [n_tokens][n_kv_heads][list] pages of each token, or NULL: every position
+    int list = 0;
 };
 struct AttendState;
 int attend_create(const AttendPools &p, int sm_count, AttendState **out);
 void attend_destroy(AttendState *st);
 int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t stream);
 int take_status_attend();
+// Attention of few rows: over e4m3 pools, and over the pages of lists (qdq_attend_rows.cu).
+struct RowsState;
+int rows_create(const AttendPools &p, int sm_count, RowsState **out);
+void rows_destroy(RowsState *st);
+int launch_rows(const RowsState *st, const AttendArgs &a, cudaStream_t stream);
+int take_status_rows();
+
+// The append to e4m3 pools (qdq_append8.cu).
+struct Append8Args {
+    int n_seqs, n_tokens, max_pages;
+    const int32_t *q_start, *kv_len, *page_table;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements
+    const float *q_norm, *k_norm;
+    const uint64_t *freq;  // turns per position of pair i, in units of 2^-64
+    void *q_out;           // fp16
+    uint8_t *k_pages, *v_pages, *k_scales, *v_scales;  // of the layer
+    float eps;
+    int n_heads, n_kv_heads, rope_dim, n_pages, page_shift;
+    int window, parts;     // tokens of a CTA, CTAs that share them (set by the launch)
+};
+int launch_append8(Append8Args a, int in_type, bool interleaved, int head_dim, cudaStream_t stream, int sm_count);
+
+// Bounds of pages' keys, and the selection of pages by them (qdq_pages.cu).
+struct PagesArgs {
+    int n_seqs, n_tokens, max_pages;
+    const int32_t *q_start, *kv_len, *page_table;
+    int n_heads, n_kv_heads, n_pages, page_shift;
+    const void *k_pages;      // of the layer, as the scales and bounds
+    const uint8_t *k_scales;
+    int8_t *bounds;
+    uint8_t *bound_scales;
+    const void *q;
+    int64_t q_stride;
+    int select, first, last;
+    int32_t *lists;
+    int window;               // tokens of a CTA (set by the launch)
+};
+int launch_bounds(PagesArgs a, int type, int head_dim, cudaStream_t stream, int sm_count);
+int launch_select(const PagesArgs &a, int type, int head_dim, cudaStream_t stream, int sm_count);
+int pages_setup();
+int take_status_pages();
 // Of the append and of sampling, which wait for nothing: what a debug build's checks recorded.
 int take_status_append();
+int take_status_append8();
 int take_status_sample();
 
 // While a caller's stream is being captured into a CUDA graph, one-time setup calls

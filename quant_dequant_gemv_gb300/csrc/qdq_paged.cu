@@ -1,6 +1,8 @@
 // qdq_paged.cu -- the paged key/value cache: the handle, its argument checks, and
-// the append of a step's new tokens (head norms, rotation and the cache write in
-// one pass). The attention over the cache is in qdq_attend.cu.
+// the append of a step's new tokens to a 16-bit cache (head norms, rotation and the
+// cache write in one pass; to a cache of e4m3 values: qdq_append8.cu). The attention
+// over the cache is in qdq_attend.cu and qdq_attend_rows.cu, the selection of pages in
+// qdq_pages.cu.
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -213,15 +215,23 @@ struct qdq_paged {
     int device = -1, sm_count = 0;
     char *k_pages = nullptr, *v_pages = nullptr;
     int64_t layer_bytes = 0;
+    int64_t layer_scales = 0;  // of an e4m3 cache, as the pools
+    uint8_t *k_scales = nullptr, *v_scales = nullptr;
+    int page_shift = 0;
     uint64_t *freq = nullptr;  // [rope_dim / 2]
     AttendPools pools{};
-    AttendState *attend = nullptr;
+    AttendState *attend = nullptr;  // (of a 16-bit cache)
+    RowsState *rows = nullptr;
+    int q_type() const { return cfg.type == QDQ_E4M3 ? QDQ_F16 : cfg.type; }
+    bool takes(int type) const {  // as the type of append's rows or of attention's results
+        return type == QDQ_F32 || type == cfg.type || (cfg.type == QDQ_E4M3 && (type == QDQ_F16 || type == QDQ_BF16));
+    }
 };
 
 namespace {
 
-int check_paged_config(const qdq_paged_config *c) {
-    if (c->type != QDQ_F16 && c->type != QDQ_BF16) return QDQ_ERR_TYPE;
+int check_paged_config(const qdq_paged_config *c, bool scaled) {
+    if (scaled ? c->type != QDQ_E4M3 : c->type != QDQ_F16 && c->type != QDQ_BF16) return QDQ_ERR_TYPE;
     if (c->n_layers < 1 || c->n_pages < 1 || c->n_heads < 1 || c->n_kv_heads < 1) return QDQ_ERR_SHAPE;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return QDQ_ERR_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 128) return QDQ_ERR_SHAPE;
@@ -262,18 +272,17 @@ int check_rows(const void *p, int64_t stride, int64_t width, int size, int n_tok
     return n_tokens > 1 && (stride * size) % 16 ? QDQ_ERR_ALIGN : QDQ_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, qdq_paged **out) {
+// Both calls that create a handle: `scaled` for e4m3 pools.
+int qdq_paged_create(const qdq_paged_config *cfg, bool scaled, void *k_pages, void *v_pages, uint8_t *k_scales,
+                     uint8_t *v_scales, qdq_paged **out) {
     if (out == nullptr || cfg == nullptr) return QDQ_ERR_PTR;
     *out = nullptr;
-    int rc = check_paged_config(cfg);
+    int rc = check_paged_config(cfg, scaled);
     if (rc) return rc;
     const DeviceInfo &dev = current_device(&rc);
     if (rc) return rc;
     if ((rc = check_dev_ptr(k_pages, dev.device)) || (rc = check_dev_ptr(v_pages, dev.device))) return rc;
+    if (scaled && ((rc = check_dev_ptr(k_scales, dev.device, 1)) || (rc = check_dev_ptr(v_scales, dev.device, 1)))) return rc;
     qdq_paged *c = new (std::nothrow) qdq_paged();
     if (!c) return QDQ_ERR_CUDA;
     c->cfg = *cfg;
@@ -281,7 +290,10 @@ int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, 
     c->sm_count = dev.sm_count;
     c->k_pages = (char *)k_pages;
     c->v_pages = (char *)v_pages;
-    c->layer_bytes = (int64_t)cfg->n_pages * cfg->page_size * cfg->n_kv_heads * cfg->head_dim * 2;
+    c->layer_bytes = (int64_t)cfg->n_pages * cfg->page_size * cfg->n_kv_heads * cfg->head_dim * (scaled ? 1 : 2);
+    c->layer_scales = (int64_t)cfg->n_pages * cfg->n_kv_heads * (cfg->page_size / 16);
+    c->k_scales = k_scales, c->v_scales = v_scales;
+    while ((1 << c->page_shift) < cfg->page_size) ++c->page_shift;
     // pair i turns by base^(-2i/R) radians a position: that over 2 pi turns, in units of
     // 2^-64 turn (below one sixth of a turn, so it fits; a double's 53 bits of it are kept)
     uint64_t freq[64] = {};
@@ -294,8 +306,10 @@ int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, 
         return QDQ_ERR_CUDA;
     }
     c->pools = {k_pages, v_pages, cfg->n_layers, cfg->n_pages, cfg->page_size, cfg->n_heads, cfg->n_kv_heads,
-                cfg->head_dim, cfg->type == QDQ_BF16};
-    rc = attend_create(c->pools, c->sm_count, &c->attend);
+                cfg->head_dim, cfg->type, k_scales, v_scales};
+    rc = scaled ? QDQ_OK : attend_create(c->pools, c->sm_count, &c->attend);
+    if (!rc) rc = rows_create(c->pools, c->sm_count, &c->rows);
+    if (!rc) rc = pages_setup();
     // The table's copy and the counters' clearing are asynchronous and in the default stream,
     // which non-blocking streams do not follow: both are done before the handle is used.
     if (!rc && cudaStreamSynchronize(nullptr) != cudaSuccess) {
@@ -310,10 +324,68 @@ int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, 
     return QDQ_OK;
 }
 
+// The checks of attention, over every position and over lists; fills `a` where there is work.
+int check_attention(const qdq_paged *c, int layer, const qdq_paged_batch *b, const void *q, int64_t q_stride, int out_type,
+                    void *out, int64_t out_stride, float scale, int window, float *lse, AttendArgs *a, bool *work) {
+    int rc = check_paged_call(c, layer, b, work);
+    if (rc) return rc;
+    const qdq_paged_config &g = c->cfg;
+    if (!c->takes(out_type) || out_type == QDQ_E4M3) return QDQ_ERR_TYPE;
+    // (the kernel takes scale * log2(e) as fp32)
+    if (!std::isfinite((float)(scale * 1.4426950408889634)) || window < 0) return QDQ_ERR_SHAPE;
+    if (!*work) return QDQ_OK;
+    const int n = b->n_tokens;
+    const int64_t width = (int64_t)g.n_heads * g.head_dim;
+    if ((rc = check_rows(q, q_stride, width, 2, n, c->device)) ||
+        (rc = check_rows(out, out_stride, width, out_type == QDQ_F32 ? 4 : 2, n, c->device)) ||
+        (lse && (rc = check_dev_ptr(lse, c->device, 4))))
+        return rc;
+    a->pools = &c->pools;
+    a->layer = layer;
+    a->n_seqs = b->n_seqs, a->n_tokens = n, a->max_pages = b->max_pages;
+    a->q_start = b->q_start, a->kv_len = b->kv_len, a->page_table = b->page_table;
+    a->q = q, a->out = out, a->lse = lse;
+    a->q_stride = q_stride, a->out_stride = out_stride;
+    a->scale = scale, a->window = window, a->out_type = out_type;
+    return QDQ_OK;
+}
+
+// Those of the bounds and the selection.
+int check_pages(const qdq_paged *c, int layer, const qdq_paged_batch *b, int8_t *bounds, uint8_t *scales, PagesArgs *a,
+                bool *work) {
+    int rc = check_paged_call(c, layer, b, work);
+    if (rc || !*work) return rc;
+    if ((rc = check_dev_ptr(bounds, c->device)) || (rc = check_dev_ptr(scales, c->device, 1))) return rc;
+    const qdq_paged_config &g = c->cfg;
+    a->n_seqs = b->n_seqs, a->n_tokens = b->n_tokens, a->max_pages = b->max_pages;
+    a->q_start = b->q_start, a->kv_len = b->kv_len, a->page_table = b->page_table;
+    a->n_heads = g.n_heads, a->n_kv_heads = g.n_kv_heads, a->n_pages = g.n_pages, a->page_shift = c->page_shift;
+    a->k_pages = c->k_pages + layer * c->layer_bytes;
+    if (c->k_scales) a->k_scales = c->k_scales + layer * c->layer_scales;
+    const int64_t units = (int64_t)layer * g.n_pages * g.n_kv_heads;
+    a->bounds = bounds + units * 2 * g.head_dim;
+    a->bound_scales = scales + units;
+    return QDQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int qdq_paged_create(const qdq_paged_config *cfg, void *k_pages, void *v_pages, qdq_paged **out) {
+    return qdq_paged_create(cfg, false, k_pages, v_pages, nullptr, nullptr, out);
+}
+
+int qdq_paged_create_e4m3(const qdq_paged_config *cfg, void *k_pages, void *v_pages, uint8_t *k_scales,
+                          uint8_t *v_scales, qdq_paged **out) {
+    return qdq_paged_create(cfg, true, k_pages, v_pages, k_scales, v_scales, out);
+}
+
 void qdq_paged_destroy(qdq_paged *c) {
     if (c == nullptr) return;
     if (c->freq) cudaFree(c->freq);
     attend_destroy(c->attend);
+    rows_destroy(c->rows);
     delete c;
 }
 
@@ -324,7 +396,7 @@ int qdq_paged_append(qdq_paged *c, int layer, const qdq_paged_batch *b, int in_t
     int rc = check_paged_call(c, layer, b, &work);
     if (rc) return rc;
     const qdq_paged_config &g = c->cfg;
-    if (in_type != QDQ_F32 && in_type != g.type) return QDQ_ERR_TYPE;
+    if (!c->takes(in_type) || in_type == QDQ_E4M3) return QDQ_ERR_TYPE;
     if (!(eps >= 0.0f) || eps > 1.0f) return QDQ_ERR_SHAPE;
     if (!work) return QDQ_OK;
     const int size = in_type == QDQ_F32 ? 4 : 2, n = b->n_tokens, kv = g.n_kv_heads * g.head_dim;
@@ -333,6 +405,21 @@ int qdq_paged_append(qdq_paged *c, int layer, const qdq_paged_batch *b, int in_t
         (rc = check_rows(v, v_stride, kv, size, n, c->device)) || (rc = check_dev_ptr(q_out, c->device)) ||
         (q_norm && (rc = check_dev_ptr(q_norm, c->device, 4))) || (k_norm && (rc = check_dev_ptr(k_norm, c->device, 4))))
         return rc;
+    if (g.type == QDQ_E4M3) {
+        Append8Args e = {};
+        e.n_seqs = b->n_seqs, e.n_tokens = n, e.max_pages = b->max_pages;
+        e.q_start = b->q_start, e.kv_len = b->kv_len, e.page_table = b->page_table;
+        e.q = q, e.k = k, e.v = v;
+        e.q_stride = q_stride, e.k_stride = k_stride, e.v_stride = v_stride;
+        e.q_norm = q_norm, e.k_norm = k_norm, e.eps = eps;
+        e.freq = c->freq;
+        e.q_out = q_out;
+        e.k_pages = (uint8_t *)c->k_pages + layer * c->layer_bytes, e.v_pages = (uint8_t *)c->v_pages + layer * c->layer_bytes;
+        e.k_scales = c->k_scales + layer * c->layer_scales, e.v_scales = c->v_scales + layer * c->layer_scales;
+        e.n_heads = g.n_heads, e.n_kv_heads = g.n_kv_heads, e.rope_dim = g.rope_dim, e.n_pages = g.n_pages;
+        e.page_shift = c->page_shift;
+        return launch_append8(e, in_type, g.rope_interleaved != 0, g.head_dim, (cudaStream_t)stream, c->sm_count);
+    }
     AppendArgs a = {};
     a.n_seqs = b->n_seqs, a.n_tokens = n, a.max_pages = b->max_pages;
     a.q_start = b->q_start, a.kv_len = b->kv_len, a.page_table = b->page_table;
@@ -344,8 +431,7 @@ int qdq_paged_append(qdq_paged *c, int layer, const qdq_paged_batch *b, int in_t
     a.k_pages = c->k_pages + layer * c->layer_bytes;
     a.v_pages = c->v_pages + layer * c->layer_bytes;
     a.n_heads = g.n_heads, a.n_kv_heads = g.n_kv_heads, a.rope_dim = g.rope_dim, a.n_pages = g.n_pages;
-    a.page_shift = 0;
-    while ((1 << a.page_shift) < g.page_size) ++a.page_shift;
+    a.page_shift = c->page_shift;
     return launch_append(a, in_type == QDQ_F32, g.type == QDQ_BF16, g.rope_interleaved != 0, g.head_dim,
                          (cudaStream_t)stream, c->sm_count);
 }
@@ -353,29 +439,52 @@ int qdq_paged_append(qdq_paged *c, int layer, const qdq_paged_batch *b, int in_t
 int qdq_paged_attention(qdq_paged *c, int layer, const qdq_paged_batch *b, const void *q, int64_t q_stride,
                         int out_type, void *out, int64_t out_stride, float scale, int window, float *lse,
                         qdq_stream_t stream) {
-    bool work;
-    int rc = check_paged_call(c, layer, b, &work);
-    if (rc) return rc;
-    const qdq_paged_config &g = c->cfg;
-    if (out_type != QDQ_F32 && out_type != g.type) return QDQ_ERR_TYPE;
-    // (the kernel takes scale * log2(e) as fp32)
-    if (!std::isfinite((float)(scale * 1.4426950408889634)) || window < 0) return QDQ_ERR_SHAPE;
-    if (!work) return QDQ_OK;
-    const int n = b->n_tokens;
-    const int64_t width = (int64_t)g.n_heads * g.head_dim;
-    if ((rc = check_rows(q, q_stride, width, 2, n, c->device)) ||
-        (rc = check_rows(out, out_stride, width, out_type == QDQ_F32 ? 4 : 2, n, c->device)) ||
-        (lse && (rc = check_dev_ptr(lse, c->device, 4))))
-        return rc;
     AttendArgs a = {};
-    a.pools = &c->pools;
-    a.layer = layer;
-    a.n_seqs = b->n_seqs, a.n_tokens = n, a.max_pages = b->max_pages;
-    a.q_start = b->q_start, a.kv_len = b->kv_len, a.page_table = b->page_table;
-    a.q = q, a.out = out, a.lse = lse;
-    a.q_stride = q_stride, a.out_stride = out_stride;
-    a.scale = scale, a.window = window, a.out_f32 = out_type == QDQ_F32;
-    return launch_attend(c->attend, a, (cudaStream_t)stream);
+    bool work;
+    const int rc = check_attention(c, layer, b, q, q_stride, out_type, out, out_stride, scale, window, lse, &a, &work);
+    if (rc || !work) return rc;
+    return c->cfg.type == QDQ_E4M3 ? launch_rows(c->rows, a, (cudaStream_t)stream) : launch_attend(c->attend, a, (cudaStream_t)stream);
+}
+
+int qdq_paged_attention_pages(qdq_paged *c, int layer, const qdq_paged_batch *b, const void *q, int64_t q_stride,
+                              const int32_t *pages, int n_select, int out_type, void *out, int64_t out_stride,
+                              float scale, float *lse, qdq_stream_t stream) {
+    AttendArgs a = {};
+    bool work;
+    if (n_select < 1) return QDQ_ERR_SHAPE;
+    int rc = check_attention(c, layer, b, q, q_stride, out_type, out, out_stride, scale, 0, lse, &a, &work);
+    if (rc || !work) return rc;
+    if ((rc = check_dev_ptr(pages, c->device, 4))) return rc;
+    a.lists = pages, a.list = n_select;
+    return launch_rows(c->rows, a, (cudaStream_t)stream);
+}
+
+int qdq_paged_key_bounds(qdq_paged *c, int layer, const qdq_paged_batch *b, int8_t *bounds, uint8_t *scales,
+                         qdq_stream_t stream) {
+    PagesArgs a = {};
+    bool work;
+    const int rc = check_pages(c, layer, b, bounds, scales, &a, &work);
+    if (rc || !work) return rc;
+    return launch_bounds(a, c->cfg.type, c->cfg.head_dim, (cudaStream_t)stream, c->sm_count);
+}
+
+int qdq_paged_select_pages(qdq_paged *c, int layer, const qdq_paged_batch *b, const void *q, int64_t q_stride,
+                           const int8_t *bounds, const uint8_t *scales, int n_select, int n_first, int n_last,
+                           int32_t *pages, qdq_stream_t stream) {
+    PagesArgs a = {};
+    bool work;
+    if (n_select < 1 || n_first < 0 || n_last < 0 || n_first > n_select || n_last > n_select - n_first) return QDQ_ERR_SHAPE;
+    int rc = check_pages(c, layer, b, const_cast<int8_t *>(bounds), const_cast<uint8_t *>(scales), &a, &work);
+    if (rc) return rc;
+    if (b->max_pages > 32768) return QDQ_ERR_LIMIT;
+    if (!work) return QDQ_OK;
+    if ((rc = check_rows(q, q_stride, (int64_t)c->cfg.n_heads * c->cfg.head_dim, 2, b->n_tokens, c->device)) ||
+        (rc = check_dev_ptr(pages, c->device, 4)))
+        return rc;
+    a.q = q, a.q_stride = q_stride;
+    a.select = n_select, a.first = n_first, a.last = n_last;
+    a.lists = pages;
+    return launch_select(a, c->cfg.type, c->cfg.head_dim, (cudaStream_t)stream, c->sm_count);
 }
 
 }  // extern "C"

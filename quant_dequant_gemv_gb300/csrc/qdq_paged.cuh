@@ -67,6 +67,34 @@ struct Float16<__nv_bfloat16> {
     static QDQ_DEV float2 unpack(uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)); }
 };
 
+// ---- the cache of e4m3 values -------------------------------------------------------------
+// A value is 2^e times its e4m3 value; blocks of kScaleBlock positions of a head share e, which is
+// kept as the byte e + 127 and lies in -kMostExponent .. kMostExponent.
+constexpr int kScaleBlock = 16, kMostExponent = 40;
+
+QDQ_DEV int exponent_of(uint8_t scale) { return min(max((int)scale - 127, -kMostExponent), kMostExponent); }
+QDQ_DEV float power_of_two(int e) { return __int_as_float((127 + e) << 23); }  // e in -126 .. 127
+
+// Four e4m3 values as two pairs of fp16, exactly.
+QDQ_DEV void e4m3x4_to_f16(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
+// Four values as e4m3, rounded to nearest; beyond 448 (and infinite) they become 448 of their sign.
+QDQ_DEV uint32_t f32_to_e4m3x4(float a, float b, float c, float d) {
+    uint32_t v;
+    asm("{ .reg .b16 x, y; cvt.rn.satfinite.e4m3x2.f32 x, %2, %1; cvt.rn.satfinite.e4m3x2.f32 y, %4, %3; mov.b32 %0, {x, y}; }"
+        : "=r"(v)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return v;
+}
+// The least e with amax <= 448 * 2^e, inside its range (amax finite).
+QDQ_DEV int least_exponent(float amax) {
+    const int bits = __float_as_int(amax);  // 448 = 1.75 * 2^8
+    return min(max((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000), -kMostExponent), kMostExponent);
+}
+
 // Four consecutive values, read once, as floats.
 template <typename TI>
 QDQ_DEV void load4(const TI *p, float *x) {

@@ -1,0 +1,454 @@
+// qdq_pages.cu -- for attention over a few of a sequence's pages: bounds of each page's keys, and the
+// pages that a cheap score over those bounds selects.
+//
+// Bounds. For each page and kv head, per dim the largest and the smallest key in units of 2^E,
+//   mx = ceil(max k * 2^-E), mn = floor(min k * 2^-E),  E the least with max |k| <= 127 * 2^E,
+// as signed bytes: all of max k * 2^-E is exact, so the bounds are the same whatever the order.
+// Score. A query head is rounded to bytes qi in units of 2^Eq in the same way; a page's score is
+//   max over the group's heads of 2^(Eq + E) * sum_d (qi_d < 0 ? qi_d * mn_d : qi_d * mx_d),
+// no less than 2^E * 2^Eq * qi . k 2^-E for any key of the page. The sum is an integer below 2^21 and
+// the scale a power of two, so a score is exact and the selection does not depend on any order.
+#include <algorithm>
+
+#include "qdq_internal.h"
+#include "qdq_paged.cuh"
+
+namespace qdq {
+namespace {
+
+#ifdef QDQ_DEBUG
+__device__ int g_pages_status;
+#endif
+
+constexpr int kLeastBound = -100, kMostBound = 121;  // of E and Eq
+constexpr int kMostWindow = 16;
+
+// The least E with amax <= 127 * 2^E (= 1.984375 * 2^(6 + E)), inside its range.
+QDQ_DEV int bound_exponent(float amax) {
+    const int bits = __float_as_int(amax);
+    return min(max((bits >> 23) - 127 - 6 + ((bits & 0x7FFFFF) > 0x7E0000), kLeastBound), kMostBound);
+}
+
+template <int TYPE>
+struct Pair;  // two values in 32 bits
+template <>
+struct Pair<QDQ_F16> {
+    using T = __half2;
+    static QDQ_DEV uint32_t infinity() { return 0x7C007C00u; }
+    static QDQ_DEV float2 unpack(uint32_t v) { return Float16<__half>::unpack(v); }
+};
+template <>
+struct Pair<QDQ_BF16> {
+    using T = __nv_bfloat162;
+    static QDQ_DEV uint32_t infinity() { return 0x7F807F80u; }
+    static QDQ_DEV float2 unpack(uint32_t v) { return Float16<__nv_bfloat16>::unpack(v); }
+};
+template <>
+struct Pair<QDQ_E4M3> : Pair<QDQ_F16> {};
+
+template <typename T>
+QDQ_DEV uint32_t least(uint32_t a, uint32_t b) {
+    T r = __hmin2(*reinterpret_cast<T *>(&a), *reinterpret_cast<T *>(&b));
+    return *reinterpret_cast<uint32_t *>(&r);
+}
+template <typename T>
+QDQ_DEV uint32_t most(uint32_t a, uint32_t b) {
+    T r = __hmax2(*reinterpret_cast<T *>(&a), *reinterpret_cast<T *>(&b));
+    return *reinterpret_cast<uint32_t *>(&r);
+}
+
+// A CTA takes one kv head of the pages that a window of tokens is the first new one of; its four
+// warps take the page's blocks of 16 positions in turn, 16 bytes of a row a lane, and join at the end.
+template <int TYPE, int D>
+__global__ void __launch_bounds__(128) bounds_kernel(const PagesArgs a) {
+    using P = Pair<TYPE>;
+    using T = typename P::T;
+    constexpr int kSize = TYPE == QDQ_E4M3 ? 1 : 2, kValues = 16 / kSize;  // of a lane's 16 bytes
+    constexpr int kLanes = D * kSize / 16, kRows = 32 / kLanes, kSteps = 16 / kRows;  // a row's lanes, rows a step
+    __shared__ float s_most[4][D], s_least[4][D];
+    __shared__ float s_top[4];
+    follow_last_kernel();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % kLanes, sub = lane / kLanes;
+    const int head = blockIdx.x % a.n_kv_heads, t0 = (int)(blockIdx.x / a.n_kv_heads) * a.window;
+    const int page_size = 1 << a.page_shift;
+    int s = find_seq(a.q_start, a.n_seqs, t0);
+    if (s < 0) return;
+    for (int t = t0; t < min(t0 + a.window, a.n_tokens);) {
+        while (s + 1 < a.n_seqs && a.q_start[s + 1] <= t) ++s;
+        int first, count;
+        seq_tokens(a.q_start, s, a.n_tokens, first, count);
+        if (t < first || t >= first + count) return;  // rows of no sequence: the batch's last
+        const int kv = max(a.kv_len[s], 0), p = kv - count + (t - first);
+        const int in_page = p & (page_size - 1);
+        const int next = p < 0 ? -p : page_size - in_page;  // tokens to the next page's first
+        const bool lead = p >= 0 && (t == first || in_page == 0);
+        t = min(t + next, first + count);
+        if (!lead) continue;
+        const int logical = p >> a.page_shift;
+        const int page = logical < a.max_pages ? a.page_table[(int64_t)s * a.max_pages + logical] : -1;
+        if (page < 0 || page >= a.n_pages) continue;
+        const int held = min(page_size, kv - (logical << a.page_shift));
+
+        float hi[kValues], lo[kValues];
+#pragma unroll
+        for (int i = 0; i < kValues; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
+        for (int b = warp; 16 * b < held; b += 4) {
+            uint4 x[kSteps];
+            float scale = 1.0f;
+            if (TYPE == QDQ_E4M3)
+                scale = power_of_two(exponent_of(a.k_scales[(((int64_t)page * a.n_kv_heads + head) << (a.page_shift - 4)) + b]));
+#pragma unroll
+            for (int y = 0; y < kSteps; ++y) {
+                const int row = 16 * b + y * kRows + sub;
+                x[y] = make_uint4(0, 0, 0, 0);
+                // (e4m3 pools hold a page's heads one after the other, the others its positions)
+                const int64_t r = TYPE == QDQ_E4M3 ? (((int64_t)page * a.n_kv_heads + head) << a.page_shift) + row
+                                                   : (((int64_t)page << a.page_shift) + row) * a.n_kv_heads + head;
+                if (row < held && QDQ_CHECK(&g_pages_status, page < a.n_pages && row < page_size))
+                    x[y] = __ldg(reinterpret_cast<const uint4 *>((const char *)a.k_pages + r * D * kSize) + at);
+            }
+            uint32_t u_hi[kValues / 2], u_lo[kValues / 2];
+#pragma unroll
+            for (int i = 0; i < kValues / 2; ++i) u_lo[i] = P::infinity(), u_hi[i] = P::infinity() | 0x80008000u;
+#pragma unroll
+            for (int y = 0; y < kSteps; ++y) {
+                if (16 * b + y * kRows + sub >= held) continue;
+                const uint32_t v[4] = {x[y].x, x[y].y, x[y].z, x[y].w};
+#pragma unroll
+                for (int i = 0; i < kValues / 2; ++i) {
+                    uint32_t w[2];
+                    if constexpr (TYPE == QDQ_E4M3) e4m3x4_to_f16(v[i / 2], w[0], w[1]);
+                    else w[0] = w[1] = v[i];
+                    u_hi[i] = most<T>(u_hi[i], w[i & 1]);
+                    u_lo[i] = least<T>(u_lo[i], w[i & 1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kValues / 2; ++i) {
+                const float2 h = P::unpack(u_hi[i]), l = P::unpack(u_lo[i]);
+                hi[2 * i] = fmaxf(hi[2 * i], h.x * scale), hi[2 * i + 1] = fmaxf(hi[2 * i + 1], h.y * scale);
+                lo[2 * i] = fminf(lo[2 * i], l.x * scale), lo[2 * i + 1] = fminf(lo[2 * i + 1], l.y * scale);
+            }
+        }
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < kValues; ++i) {
+                hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], o));
+                lo[i] = fminf(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], o));
+            }
+        if (sub == 0) {
+#pragma unroll
+            for (int i = 0; i < kValues; ++i) s_most[warp][at * kValues + i] = hi[i], s_least[warp][at * kValues + i] = lo[i];
+        }
+        __syncthreads();
+        const int d = threadIdx.x;
+        float mx = 0.0f, mn = 0.0f, top = 0.0f;
+        if (d < D) {
+            mx = fmaxf(fmaxf(s_most[0][d], s_most[1][d]), fmaxf(s_most[2][d], s_most[3][d]));
+            mn = fminf(fminf(s_least[0][d], s_least[1][d]), fminf(s_least[2][d], s_least[3][d]));
+            if (mx < mn) mx = mn = 0.0f;  // (no key here is a number)
+            top = fmaxf(fabsf(mx), fabsf(mn));
+        }
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (lane == 0) s_top[warp] = top;
+        __syncthreads();
+        const int e = bound_exponent(fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3])));
+        const int64_t unit = (int64_t)page * a.n_kv_heads + head;
+        if (d < D) {
+            // (2^-e in two steps: it may lie below fp32's normal range)
+            const float f0 = power_of_two(-e / 2), f1 = power_of_two(-e - -e / 2);
+            a.bounds[unit * 2 * D + d] = (int8_t)fminf(fmaxf(ceilf(mx * f0 * f1), -127.0f), 127.0f);
+            a.bounds[unit * 2 * D + D + d] = (int8_t)fminf(fmaxf(floorf(mn * f0 * f1), -127.0f), 127.0f);
+        }
+        if (d == 0) a.bound_scales[unit] = (uint8_t)(e + 127);
+        __syncthreads();
+    }
+}
+
+// ---- selection --------------------------------------------------------------------------------
+constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32, kMostGroup = 32, kBins = 2048;
+constexpr int kMostPages = 32768;
+
+QDQ_DEV uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+QDQ_DEV uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+QDQ_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+QDQ_DEV void store_to_rank0(uint32_t addr, uint32_t v) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(addr));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
+QDQ_DEV uint32_t bytes4(float a, float b, float c, float d) {
+    return ((uint32_t)(int)a & 0xFF) | ((uint32_t)(int)b & 0xFF) << 8 | ((uint32_t)(int)c & 0xFF) << 16 | (uint32_t)(int)d << 24;
+}
+
+// Sums `v` over the CTA's threads before this one; total in every thread. `room`: kSelectWarps words.
+QDQ_DEV uint32_t scan(uint32_t v, uint32_t *room, uint32_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t e = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += e;
+    }
+    __syncthreads();
+    if (lane == 31) room[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kSelectWarps; ++w) {
+        if (w < warp) before += room[w];
+        total += room[w];
+    }
+    return before + incl - v;
+}
+
+// A cluster takes a token and kv head. Its CTAs score a share of the pages each (a page's bounds are
+// read once, by D / 8 lanes, for all the group's heads) and send the scores, as integers in their
+// order, to the first CTA's shared memory, which selects: it narrows the range of the k-th largest
+// by 2048 bins at a time, and then writes what lies above it and the first of its equals, in order.
+template <int TYPE, int D>
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs a) {
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a page, pages of a warp step
+    extern __shared__ __align__(16) char smem[];
+    uint32_t *keys = reinterpret_cast<uint32_t *>(smem);  // [max_pages], the first CTA's
+    __shared__ __align__(16) uint32_t s_q[2][kMostGroup][D / 4];  // max(q, 0) and min(q, 0)
+    __shared__ int s_eq[kMostGroup];
+    __shared__ uint32_t s_bins[kBins], s_room[kSelectWarps], s_pick[3];
+    __shared__ uint32_t s_range[2][kSelectWarps];
+    follow_last_kernel();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = cluster_rank(), size = cluster_size(), item = blockIdx.x / size;
+    const int t = item / a.n_kv_heads, head = item - t * a.n_kv_heads, group = a.n_heads / a.n_kv_heads;
+
+    const int s = find_seq(a.q_start, a.n_seqs, t);
+    int first = 0, count = 0;
+    if (s >= 0) seq_tokens(a.q_start, s, a.n_tokens, first, count);
+    const bool live = s >= 0 && t >= first && t < first + count;
+    const int p = live ? max(a.kv_len[s], 0) - count + (t - first) : -1;
+    const int newest = p >= 0 ? p >> a.page_shift : -1, pages = min(newest + 1, a.max_pages);
+    const int32_t *table = a.page_table + (int64_t)max(s, 0) * a.max_pages;
+
+    // the group's query heads as bytes
+    for (int h = warp; h < group; h += kSelectWarps) {
+        constexpr int kEach = D / 32;
+        float v[4] = {};
+        if (live) {
+            const uint16_t *q = (const uint16_t *)a.q + (int64_t)t * a.q_stride + (int64_t)(head * group + h) * D + lane * kEach;
+#pragma unroll
+            for (int i = 0; i < kEach; i += 2) {
+                const float2 x = Pair<TYPE>::unpack(*reinterpret_cast<const uint32_t *>(q + i));
+                v[i] = x.x, v[i + 1] = x.y;
+            }
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const int e = bound_exponent(top);
+        const float f0 = power_of_two(-e / 2), f1 = power_of_two(-e - -e / 2);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i] = fminf(fmaxf(rintf(v[i] * f0 * f1), -127.0f), 127.0f);
+        uint32_t over = bytes4(fmaxf(v[0], 0.0f), fmaxf(v[1], 0.0f), fmaxf(v[2], 0.0f), fmaxf(v[3], 0.0f));
+        uint32_t under = bytes4(fminf(v[0], 0.0f), fminf(v[1], 0.0f), fminf(v[2], 0.0f), fminf(v[3], 0.0f));
+        if (kEach == 4) {
+            s_q[0][h][lane] = over, s_q[1][h][lane] = under;
+        } else {  // two dims a lane
+            over |= __shfl_down_sync(0xFFFFFFFFu, over, 1) << 16, under = (under & 0xFFFFu) | __shfl_down_sync(0xFFFFFFFFu, under, 1) << 16;
+            if (lane % 2 == 0) s_q[0][h][lane / 2] = over, s_q[1][h][lane / 2] = under;
+        }
+        if (lane == 0) s_eq[h] = e;
+    }
+    cluster_sync();  // (and the first CTA is known to run before anything is sent to it)
+
+    // scores of this CTA's pages
+    {
+        const int sub = lane / kLanes, at = lane % kLanes, which = at / (kLanes / 2), chunk = at % (kLanes / 2);
+        const int stride = size * kSelectWarps * kAtOnce;
+        constexpr int kDeep = 4;  // steps whose loads are in flight
+        for (int j0 = (rank * kSelectWarps + warp) * kAtOnce; j0 < pages; j0 += kDeep * stride) {
+            int page[kDeep], e[kDeep];
+            uint4 b[kDeep];
+#pragma unroll
+            for (int y = 0; y < kDeep; ++y) {
+                const int j = j0 + y * stride + sub;
+                page[y] = j < pages ? table[j] : -1;
+                if ((unsigned)page[y] >= (unsigned)a.n_pages) page[y] = -1;
+            }
+#pragma unroll
+            for (int y = 0; y < kDeep; ++y) {
+                b[y] = make_uint4(0, 0, 0, 0);
+                e[y] = 0;
+                if (page[y] >= 0) {
+                    const int64_t unit = (int64_t)page[y] * a.n_kv_heads + head;
+                    b[y] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + unit * 2 * D) + at);
+                    e[y] = a.bound_scales[unit] - 127;
+                }
+            }
+#pragma unroll
+            for (int y = 0; y < kDeep; ++y) {
+                const int j = j0 + y * stride + sub;
+                if (j0 + y * stride >= pages) break;
+                float best = -INFINITY;
+                for (int h = 0; h < group; ++h) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(&s_q[which][h][4 * chunk]);
+                    int sum = __dp4a((int)b[y].x, (int)q.x, 0);
+                    sum = __dp4a((int)b[y].y, (int)q.y, sum);
+                    sum = __dp4a((int)b[y].z, (int)q.z, sum);
+                    sum = __dp4a((int)b[y].w, (int)q.w, sum);
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                    best = fmaxf(best, (float)sum * power_of_two(min(max(s_eq[h] + e[y], -100), 100)));
+                }
+                if (at == 0 && j < pages) {
+                    const uint32_t bits = __float_as_uint(best);
+                    uint32_t key = bits & 0x80000000u ? ~bits : bits | 0x80000000u;  // (finite: neither 0 nor the largest)
+                    if (j < a.first || j > newest - a.last) key = 0xFFFFFFFFu;       // always taken
+                    if (page[y] < 0) key = 0;                                        // never
+                    if (QDQ_CHECK(&g_pages_status, j >= 0 && j < a.max_pages)) store_to_rank0(smem_u32(keys + j), key);
+                }
+            }
+        }
+    }
+    cluster_sync();
+    if (rank != 0 || !live) return;
+
+    // ---- the first CTA selects -------------------------------------------------------------------
+    // a thread has a run of consecutive pages
+    const int tid = threadIdx.x, per = (pages + kSelectThreads - 1) / kSelectThreads;
+    const int j0 = min(tid * per, pages), j1 = min(j0 + per, pages);
+    uint32_t valid = 0, least_key = 0xFFFFFFFFu, most_key = 0;
+    for (int j = tid; j < pages; j += kSelectThreads) {
+        const uint32_t k = keys[j];
+        if (k) ++valid, least_key = min(least_key, k), most_key = max(most_key, k);
+    }
+    uint32_t all;
+    scan(valid, s_room, all);
+    uint32_t threshold = 1, equals = 0xFFFFFFFFu;  // taken: above the threshold, and of its equals the first so many
+    if (all > (uint32_t)a.select) {
+        least_key = __reduce_min_sync(0xFFFFFFFFu, least_key);
+        most_key = __reduce_max_sync(0xFFFFFFFFu, most_key);
+        if (lane == 0) s_range[0][warp] = least_key, s_range[1][warp] = most_key;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSelectWarps; ++w) least_key = min(least_key, s_range[0][w]), most_key = max(most_key, s_range[1][w]);
+        uint32_t want = a.select, from = least_key, width = most_key - least_key;  // the want-th largest lies in from .. from + width
+        while (true) {
+            const int bits = 32 - __clz(width), shift = max(bits - 11, 0);
+            for (int i = tid; i < kBins; i += kSelectThreads) s_bins[i] = 0;
+            __syncthreads();
+            for (int j = tid; j < pages; j += kSelectThreads) {
+                const uint32_t k = keys[j];
+                if (k >= from && k - from <= width) atomicAdd(&s_bins[(k - from) >> shift], 1u);
+            }
+            __syncthreads();
+            // from the top: thread i has bins kBins - 8 i - 8 .. kBins - 8 i - 1
+            constexpr int kEach = kBins / kSelectThreads;
+            uint32_t mine = 0, total;
+            for (int i = 0; i < kEach; ++i) mine += s_bins[kBins - 1 - kEach * tid - i];
+            uint32_t above = scan(mine, s_room, total);
+            if (above < want && want <= above + mine) {
+                int bin = kBins - 1 - kEach * tid;
+                while (above + s_bins[bin] < want) above += s_bins[bin--];
+                s_pick[0] = bin, s_pick[1] = want - above, s_pick[2] = s_bins[bin];
+            }
+            __syncthreads();
+            const uint32_t bin = s_pick[0], here = s_pick[2];
+            want = s_pick[1];
+            from += bin << shift;
+            // (the last bin may reach past the range)
+            width = min((1u << shift) - 1, width - (bin << shift));
+            __syncthreads();
+            if (shift == 0 || here == want) {  // one value, or the whole bin
+                threshold = from;
+                if (shift == 0) equals = want;
+                break;
+            }
+        }
+    }
+    const bool exact = equals != 0xFFFFFFFFu;
+    uint32_t over = 0, same = 0;
+    for (int j = j0; j < j1; ++j) {
+        const uint32_t k = keys[j];
+        if (exact ? k > threshold : k >= threshold) ++over;
+        else if (exact && k == threshold) ++same;
+    }
+    uint32_t total;
+    uint32_t rank_same = scan(same, s_room, total);
+    // entries before this thread's: those over, and of the equals the first `equals`
+    const uint32_t taken_same = exact ? (rank_same >= equals ? 0 : min(same, equals - rank_same)) : 0;
+    uint32_t to = scan(over + taken_same, s_room, total);
+    int32_t *out = a.lists + ((int64_t)t * a.n_kv_heads + head) * a.select;
+    for (int j = j0; j < j1; ++j) {
+        const uint32_t k = keys[j];
+        const bool is_same = exact && k == threshold;
+        const bool take = is_same ? rank_same < equals : k >= threshold && k != 0;
+        rank_same += is_same;
+        if (take && to < (uint32_t)a.select) out[to++] = j;
+    }
+    for (int j = (int)total + tid; j < a.select; j += kSelectThreads) out[j] = -1;
+}
+
+using Kernel = void (*)(PagesArgs);
+#define QDQ_BY_TYPE(NAME, D) (type == QDQ_E4M3 ? NAME<QDQ_E4M3, D> : type == QDQ_BF16 ? NAME<QDQ_BF16, D> : NAME<QDQ_F16, D>)
+Kernel select_of(int type, int head_dim) { return head_dim == 64 ? QDQ_BY_TYPE(select_kernel, 64) : QDQ_BY_TYPE(select_kernel, 128); }
+
+}  // namespace
+
+int launch_bounds(PagesArgs a, int type, int head_dim, cudaStream_t stream, int sm_count) {
+    // Many tokens are mostly ones that begin no page: a window of them is one CTA's.
+    a.window = (int64_t)a.n_tokens * a.n_kv_heads >= (int64_t)sm_count * 64 ? kMostWindow : 1;
+    const int64_t grid = ((int64_t)a.n_tokens + a.window - 1) / a.window * a.n_kv_heads;
+    if (grid > 0x7FFFFFFF) return QDQ_ERR_LIMIT;
+    const Kernel k = head_dim == 64 ? QDQ_BY_TYPE(bounds_kernel, 64) : QDQ_BY_TYPE(bounds_kernel, 128);
+    return launch_following(k, (unsigned)grid, 128, 0, 1, stream, a);
+}
+
+int launch_select(const PagesArgs &a, int type, int head_dim, cudaStream_t stream, int sm_count) {
+    // CTAs of a cluster: as many as the SMs have room for beside the other items, up to 8, with 64 pages
+    // each at least.
+    const int64_t items = (int64_t)a.n_tokens * a.n_kv_heads;
+    unsigned size = 1;
+    while (size < 8 && items * size * 2 <= (int64_t)sm_count * 2 && a.max_pages >= 128 * (int)size) size *= 2;
+    if (items * size > 0x7FFFFFFF) return QDQ_ERR_LIMIT;
+    return launch_following(select_of(type, head_dim), (unsigned)(items * size), kSelectThreads, (size_t)a.max_pages * 4, size,
+                            stream, a);
+}
+
+// The selection's shared memory, for every handle: called where one is created.
+int pages_setup() {
+    for (int type : {QDQ_F16, QDQ_BF16, QDQ_E4M3})
+        for (int dim : {64, 128})
+            if (cudaFuncSetAttribute(select_of(type, dim), cudaFuncAttributeMaxDynamicSharedMemorySize, kMostPages * 4) != cudaSuccess) {
+                cudaGetLastError();
+                return QDQ_ERR_CUDA;
+            }
+    return QDQ_OK;
+}
+
+int take_status_pages() {
+    int v = 0;
+#ifdef QDQ_DEBUG
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_pages_status, sizeof(int)) != cudaSuccess ||
+        (v && cudaMemcpyToSymbol(g_pages_status, &zero, sizeof(int)) != cudaSuccess)) {
+        cudaGetLastError();
+        return QDQ_ERR_CUDA;
+    }
+#endif
+    return v;
+}
+
+}  // namespace qdq

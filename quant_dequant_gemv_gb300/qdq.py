@@ -55,7 +55,7 @@ class LlamaLayer(ctypes.Structure):
 
 
 # qdq_float_type: element types of the serving calls
-F32, F16, BF16 = 1, 2, 3
+F32, F16, BF16, E4M3 = 1, 2, 3, 4
 
 
 class PagedConfig(ctypes.Structure):
@@ -118,6 +118,11 @@ def lib() -> ctypes.CDLL:
             "qdq_paged_append": (_INT, [_P, _INT, _P, _INT, _P, _I64, _P, _I64, _P, _I64, _P, _P, ctypes.c_float,
                                         _P, _P]),
             "qdq_paged_attention": (_INT, [_P, _INT, _P, _P, _I64, _INT, _P, _I64, ctypes.c_float, _INT, _P, _P]),
+            "qdq_paged_create_e4m3": (_INT, [ctypes.POINTER(PagedConfig), _P, _P, _P, _P, ctypes.POINTER(_P)]),
+            "qdq_paged_key_bounds": (_INT, [_P, _INT, _P, _P, _P, _P]),
+            "qdq_paged_select_pages": (_INT, [_P, _INT, _P, _P, _I64, _P, _P, _INT, _INT, _INT, _P, _P]),
+            "qdq_paged_attention_pages": (_INT, [_P, _INT, _P, _P, _I64, _P, _INT, _INT, _P, _I64, ctypes.c_float, _P,
+                                                 _P]),
             "qdq_sample": (_INT, [_INT, _P, _I64, _INT, _INT, _P, _P, _P, _P, _P, _P, _P, _P]),
             "qdq_quantize": (_INT, [_INT, _P, _I64, _P, _P]),
             "qdq_gguf_parse": (_INT, [_P, _I64, ctypes.POINTER(GgufTensor), _INT, ctypes.POINTER(_INT),
@@ -142,7 +147,8 @@ EXPORTS = ["qdq_block_bytes", "qdq_block_weights", "qdq_status_string", "qdq_dev
            "qdq_gemv_levels_noalloc", "qdq_rope_attention", "qdq_llama_create", "qdq_llama_forward",
            "qdq_llama_buffers", "qdq_llama_launches", "qdq_llama_destroy", "qdq_quantize", "qdq_gguf_parse",
            "qdq_gguf_find_kv", "qdq_paged_create", "qdq_paged_destroy", "qdq_paged_append", "qdq_paged_attention",
-           "qdq_sample"]
+           "qdq_sample", "qdq_paged_create_e4m3", "qdq_paged_key_bounds", "qdq_paged_select_pages",
+           "qdq_paged_attention_pages"]
 
 
 def _ptr(t) -> int:
@@ -353,11 +359,16 @@ class Llama:
 _float_types: dict = {}
 
 
+def _float16():
+    import torch
+    return torch.float16
+
+
 def _float_type(t) -> int:
     """The qdq_float_type of a torch tensor (0, which every call refuses, for another type)."""
     if not _float_types:
         import torch
-        _float_types.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+        _float_types.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3})
     return _float_types.get(t.dtype, 0)
 
 
@@ -404,23 +415,43 @@ class PagedBatch:
 class PagedCache:
     """A paged key/value cache (qdq_paged_*): k_pages and v_pages are fp16 or bf16
     tensors [n_layers, n_pages, page_size, n_kv_heads, head_dim] of the caller's,
-    which must outlive the cache."""
+    which must outlive the cache. Of e4m3 values (torch.float8_e4m3fn): tensors
+    [n_layers, n_pages, n_kv_heads, page_size, head_dim] and their scales k_scales,
+    v_scales [n_layers, n_pages, n_kv_heads, page_size / 16] (float8_e8m0fnu or uint8);
+    queries are then fp16. `q_dtype` is the queries' type."""
 
     def __init__(self, k_pages, v_pages, n_heads: int, rope_dim: int | None = None, interleaved: bool = True,
-                 rope_base: float = 10000.0):
+                 rope_base: float = 10000.0, k_scales=None, v_scales=None):
         if k_pages.dim() != 5 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or \
                 not k_pages.is_contiguous() or not v_pages.is_contiguous():
             raise ValueError("k_pages, v_pages: two contiguous tensors [n_layers, n_pages, page_size, n_kv_heads, "
                              "head_dim] of one type are needed")
+        kind = _float_type(k_pages)
+        scaled = kind == E4M3
         layers, pages, page, kv, dim = k_pages.shape
-        self._keep = (k_pages, v_pages)
+        if scaled:
+            page, kv = kv, page
+        for s in (k_scales, v_scales):
+            if (s is not None) != scaled:
+                raise ValueError("k_scales, v_scales: needed for e4m3 pools, and for these alone")
+            if scaled and (tuple(s.shape) != (layers, pages, kv, page // 16) or not s.is_contiguous() or
+                           s.element_size() != 1):
+                raise ValueError("k_scales, v_scales: contiguous tensors [n_layers, n_pages, n_kv_heads, page_size / 16] "
+                                 "of bytes are needed")
+        self._keep = (k_pages, v_pages, k_scales, v_scales)
         self.dtype = k_pages.dtype
+        self.q_dtype = _float16() if scaled else k_pages.dtype
         self.n_heads, self.n_kv_heads, self.head_dim = n_heads, kv, dim
-        self.cfg = PagedConfig(_float_type(k_pages), layers, pages, page, n_heads, kv, dim,
-                               dim if rope_dim is None else rope_dim, int(interleaved), rope_base)
+        self._pool = (layers, pages)
+        self.cfg = PagedConfig(kind, layers, pages, page, n_heads, kv, dim, dim if rope_dim is None else rope_dim,
+                               int(interleaved), rope_base)
         h = _P()
-        _check(lib().qdq_paged_create(ctypes.byref(self.cfg), _ptr(k_pages), _ptr(v_pages), ctypes.byref(h)),
-               "qdq_paged_create")
+        if scaled:
+            _check(lib().qdq_paged_create_e4m3(ctypes.byref(self.cfg), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales),
+                                               _ptr(v_scales), ctypes.byref(h)), "qdq_paged_create_e4m3")
+        else:
+            _check(lib().qdq_paged_create(ctypes.byref(self.cfg), _ptr(k_pages), _ptr(v_pages), ctypes.byref(h)),
+                   "qdq_paged_create")
         self._h = h
 
     def _width(self, t, n_tokens: int, heads: int, what: str) -> int:
@@ -433,10 +464,11 @@ class PagedCache:
                stream=None) -> None:
         """Head norms, rotation and the cache write of the batch's new tokens (qdq_paged_append).
         q, k, v: [n_tokens, heads * head_dim] rows (views of a wider row are fine), fp32 or the
-        cache's type; q_out: contiguous, of the cache's type."""
+        cache's type (any of fp32, fp16, bf16 for an e4m3 cache); q_out: contiguous, of the
+        queries' type."""
         n = batch.n_tokens
-        if k.dtype != q.dtype or v.dtype != q.dtype or q_out.dtype != self.dtype:
-            raise ValueError("q, k and v need one type, q_out the cache's")
+        if k.dtype != q.dtype or v.dtype != q.dtype or q_out.dtype != self.q_dtype:
+            raise ValueError("q, k and v need one type, q_out the queries'")
         if self._width(q_out, n, self.n_heads, "q_out") != self.n_heads * self.head_dim and n > 1:
             raise ValueError("q_out: contiguous rows are needed")
         _check(lib().qdq_paged_append(self._h, layer, batch._ref, _float_type(q), q.data_ptr(),
@@ -450,16 +482,65 @@ class PagedCache:
     def attention(self, layer: int, batch: PagedBatch, q, out, scale: float | None = None, window: int = 0, lse=None,
                   stream=None) -> None:
         """Causal attention of the batch's new tokens over the cache (qdq_paged_attention).
-        scale defaults to 1 / sqrt(head_dim); out: the cache's type or fp32."""
+        scale defaults to 1 / sqrt(head_dim); out: the cache's type or fp32 (any of fp32, fp16,
+        bf16 for an e4m3 cache)."""
         n = batch.n_tokens
-        if q.dtype != self.dtype:
-            raise ValueError("q: the cache's type is needed")
+        if q.dtype != self.q_dtype:
+            raise ValueError("q: the queries' type is needed")
         _check(lib().qdq_paged_attention(self._h, layer, batch._ref, q.data_ptr(),
                                          self._width(q, n, self.n_heads, "q"), _float_type(out), out.data_ptr(),
                                          self._width(out, n, self.n_heads, "out"),
                                          self.head_dim ** -0.5 if scale is None else scale, window,
                                          _vector(lse, n * self.n_heads, "float32", "lse"), _stream(stream)),
                "qdq_paged_attention")
+
+    def _bounds(self, bounds, scales) -> tuple[int, int]:
+        layers, pages = self._pool
+        units = layers * pages * self.n_kv_heads
+        if scales.element_size() != 1 or not scales.is_contiguous() or scales.numel() < units:
+            raise ValueError(f"scales: a contiguous tensor of {units} bytes is needed")
+        return _vector(bounds, units * 2 * self.head_dim, "int8", "bounds"), scales.data_ptr()
+
+    def key_bounds(self, layer: int, batch: PagedBatch, bounds, scales, stream=None) -> None:
+        """Bounds of the keys of the pages that hold the batch's new tokens (qdq_paged_key_bounds).
+        bounds: int8 [n_layers, n_pages, n_kv_heads, 2, head_dim]; scales: bytes (float8_e8m0fnu or
+        uint8) [n_layers, n_pages, n_kv_heads]."""
+        _check(lib().qdq_paged_key_bounds(self._h, layer, batch._ref, *self._bounds(bounds, scales), _stream(stream)),
+               "qdq_paged_key_bounds")
+
+    def _lists(self, pages, n_tokens: int) -> tuple[int, int]:
+        if pages.dim() != 3 or pages.shape[0] < n_tokens or pages.shape[1] != self.n_kv_heads:
+            raise ValueError(f"pages: [{n_tokens}, {self.n_kv_heads}, n_select] is needed")
+        return _vector(pages, 0, "int32", "pages"), pages.shape[2]
+
+    def select_pages(self, layer: int, batch: PagedBatch, q, bounds, scales, pages, first: int = 1, last: int = 1,
+                     stream=None) -> None:
+        """The numbers of the n_select pages of each token's sequence that its queries may weigh most,
+        for each kv head, the first and last ones always (qdq_paged_select_pages). pages: int32
+        [n_tokens, n_kv_heads, n_select]; bounds and scales as key_bounds keeps them."""
+        n = batch.n_tokens
+        if q.dtype != self.q_dtype:
+            raise ValueError("q: the queries' type is needed")
+        to, n_select = self._lists(pages, n)
+        _check(lib().qdq_paged_select_pages(self._h, layer, batch._ref, q.data_ptr(),
+                                            self._width(q, n, self.n_heads, "q"), *self._bounds(bounds, scales),
+                                            n_select, first, last, to, _stream(stream)), "qdq_paged_select_pages")
+
+    def attention_pages(self, layer: int, batch: PagedBatch, q, pages, out, scale: float | None = None, lse=None,
+                        stream=None) -> None:
+        """Attention of the batch's new tokens over the pages of their lists
+        (qdq_paged_attention_pages). pages: int32 [n_tokens, n_kv_heads, n_select], rising, as
+        select_pages writes them; the rest as for attention."""
+        n = batch.n_tokens
+        if q.dtype != self.q_dtype:
+            raise ValueError("q: the queries' type is needed")
+        lists, n_select = self._lists(pages, n)
+        _check(lib().qdq_paged_attention_pages(self._h, layer, batch._ref, q.data_ptr(),
+                                               self._width(q, n, self.n_heads, "q"), lists, n_select, _float_type(out),
+                                               out.data_ptr(), self._width(out, n, self.n_heads, "out"),
+                                               self.head_dim ** -0.5 if scale is None else scale,
+                                               _vector(lse, n * self.n_heads, "float32", "lse"), _stream(stream)),
+               "qdq_paged_attention_pages")
 
     def close(self) -> None:
         if getattr(self, "_h", None) is not None and self._h.value:
