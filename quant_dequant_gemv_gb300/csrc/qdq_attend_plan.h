@@ -11,7 +11,7 @@
 // Items. (sequence, block, kv head), in that order; an item's length is the number of
 // key tiles (kTileN positions) from the first one that any of its tokens attends to up
 // to the last.
-// Work. An item is kItemUnits units (its queries, its output), then one for each key
+// Work. An item is kItemUnits (or the geometry's `item`) units (its queries, its output), then one for each key
 // tile. The items' units, laid end to end, are dealt to the CTAs in equal contiguous
 // ranges, so whatever the lengths, every CTA has the same work; a key tile belongs to the
 // CTA that holds its unit, and an item whose tiles belong to several is joined from its
@@ -38,6 +38,7 @@ struct AttendGeometry {
     int kv_heads;
     int window;       // 0: none
     int table_end;    // positions that the page table covers
+    int item = kItemUnits;
     int block = 0;    // tokens of a block; 0: two tiles
     int list = 0;     // pages of a token's list; 0: none, every position is attended to
     int page_shift = 0;  // (of a list) log2 of the page's positions
@@ -116,10 +117,11 @@ QDQ_PLAN_FN int range_owner(int64_t total, int n, int64_t x) {
     return total < (1 << 22) && n < 512 ? (int)((((uint32_t)x + 1) * (uint32_t)n - 1) / (uint32_t)total)
                                         : (int)(((x + 1) * n - 1) / total);
 }
-QDQ_PLAN_FN int item_units(const AttendBlock &b) { return kItemUnits + b.t1 - b.t0; }
+QDQ_PLAN_FN int item_units(const AttendBlock &b, int own = kItemUnits) { return own + b.t1 - b.t0; }
 // Of an item whose units begin at `item`, the key tiles [first, last) of the range [x, end).
-QDQ_PLAN_FN void piece_of(const AttendBlock &b, int64_t item, int64_t x, int64_t end, int &first, int &last) {
-    const int64_t tile0 = item + kItemUnits, n = b.t1 - b.t0;
+QDQ_PLAN_FN void piece_of(const AttendBlock &b, int64_t item, int64_t x, int64_t end, int &first, int &last,
+                         int own = kItemUnits) {
+    const int64_t tile0 = item + own, n = b.t1 - b.t0;
     const int64_t f = x > tile0 ? x - tile0 : 0, l = end - tile0 < n ? end - tile0 : n;
     first = (int)f;
     last = l > f ? (int)l : (int)f;

@@ -18,9 +18,9 @@
 // from registers, where the e4m3 values are widened on their way (a matrix unit that reads shared
 // memory would want them written back there), and any 8 rows fill it. A CTA has eight working warps,
 // each with 16 of a tile's 128 positions (one block of scales), a maximum, a sum and an accumulator
-// of its own, and one warp that issues the copies: whole runs of a page's rows by tensor copies
-// with a swizzle, into a ring of stages of a tile's keys and values. The warps' states are joined at
-// the item's end.
+// of its own; one warp that issues the copies, whole runs of a page's rows by tensor copies with a
+// swizzle into a ring of stages of a tile's keys and values, and the queries of the next items; and
+// three that join the working warps' states at an item's end, while those go on with the next.
 //
 // Operands. The contraction may take its terms in any order, so a lane reads 16 consecutive bytes of
 // a key and its query fragments are loaded in that order. Of the values a lane reads 16 consecutive
@@ -54,7 +54,7 @@ namespace {
 
 __device__ int g_rows_status;
 
-constexpr int kWarps = 8, kThreads = (kWarps + 1) * 32, kMostRows = 32;
+constexpr int kWarps = 8, kJoiners = 3, kThreads = (kWarps + 1 + kJoiners) * 32, kMostRows = 32;
 constexpr float kLag = 8.0f;  // log2 of how far the running maximum may lag
 
 enum Kind { kF16, kBf16, kE4m3 };
@@ -78,22 +78,33 @@ struct RowsArgs {
     unsigned *counters;
 };
 
-template <int HD, int KIND>
+struct RowsPiece {
+    int n, t0;               // key tiles (0 ends the walk), the first
+    int lo, hi;              // positions that the block attends to
+    int tokens, token0, p0;  // the block's tokens, the row of the first, its position
+    int head;
+    int whole, c_first, c_last;
+};
+
+template <int HD, int KIND, int MODE>
 struct Shape {
+    static constexpr int kRows = 8 << MODE;
     static constexpr uint32_t kRow = HD * (KIND == kE4m3 ? 1 : 2);  // bytes of a position
     static constexpr uint32_t kHalf = kTileN * kRow;                // keys (or values) of a stage
     static constexpr uint32_t kStage = 2 * kHalf;
-    static constexpr int kStages = kStage == 65536 ? 3 : kStage == 32768 ? 5 : 10;
-    static constexpr uint32_t kMerge = kStages * kStage;              // [warp][8 rows][HD + 4]
-    static constexpr uint32_t kPitch = (HD + 4) * 4;
-    static constexpr uint32_t kState = kMerge + kWarps * 8 * kPitch;  // [warp][8 rows] maximum and sum
-    static constexpr uint32_t kMeta = kState + kWarps * 8 * 8;  // [stage] Meta
+    static constexpr int kStages = (int)(131072 / kStage);
+    static constexpr int kPieces = MODE == 0 ? 8 : MODE == 1 ? 4 : 2;  // items that the copies may be ahead
+    static constexpr uint32_t kMerge = kStages * kStage;                  // [2][warp][8 rows][HD + 4]
+    static constexpr uint32_t kPitch = (HD + 4) * 4, kMergeSize = kWarps * 8 * kPitch;
+    static constexpr uint32_t kState = kMerge + 2 * kMergeSize;           // [2][warp][8 rows] maximum and sum
+    static constexpr uint32_t kQ = kState + 2 * kWarps * 64, kQSize = kRows * HD * 2;  // [piece][row][HD]
+    static constexpr uint32_t kMeta = kQ + kPieces * kQSize;              // [stage] Meta
     static constexpr uint32_t kBars = kMeta + kStages * 64;
-    static constexpr uint32_t kStart = kBars + (2 * kStages + 4) * 8;
-    static constexpr uint32_t kPieces = kStart + 64;
-    static constexpr uint32_t kTotal = kPieces + 192;
-    static_assert(kMeta % 16 == 0 && kBars % 8 == 0 && kStart % 8 == 0 && kPieces % 8 == 0 && kTotal <= 232448, "shared memory");
-    static_assert(kStages * kStage >= 16 * kMaxSeqs, "find_start's room");
+    static constexpr uint32_t kStart = kBars + (2 * kStages + 2 * kPieces + 4) * 8;
+    static constexpr uint32_t kPiece = kStart + 64;
+    static constexpr uint32_t kTotal = kPiece + kPieces * sizeof(RowsPiece);
+    static_assert(kQ % 16 == 0 && kMeta % 16 == 0 && kBars % 8 == 0 && kStart % 8 == 0 && kTotal <= 232448, "shared memory");
+    static_assert(kStages * kStage >= 16 * kMaxSeqs && sizeof(Start) <= 64, "find_start's room, Shape::kPiece");
 };
 
 // Of each block of 16 positions of a stage: its first position (-1: absent) and its scales' exponents.
@@ -102,15 +113,6 @@ struct Meta {
     int8_t ek[8], ev[8];
 };
 static_assert(sizeof(Meta) <= 64, "Shape::kBars");
-
-struct RowsPiece {
-    int n, t0;               // key tiles (0 ends the walk), the first
-    int lo, hi;              // positions that the block attends to
-    int tokens, token0, p0;  // the block's tokens, the row of the first, its position
-    int head;
-    int whole, c_first, c_last;
-};
-static_assert(2 * sizeof(RowsPiece) <= 192 && sizeof(Start) <= 64, "Shape::kPieces");
 
 template <int KIND>
 QDQ_DEV void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -135,7 +137,7 @@ QDQ_DEV void tma_rows(uint32_t dst, const CUtensorMap *map, int y, int z, uint32
 template <int HD, int KIND, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     rows_kernel(const RowsArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using L = Shape<HD, KIND>;
+    using L = Shape<HD, KIND, MODE>;
     using F16 = Float16<typename std::conditional<KIND == kBf16, __nv_bfloat16, __half>::type>;
     constexpr bool kPacked = MODE == 0;          // a weight's second term in rows 8..15
     constexpr int kHalves = MODE == 2 ? 2 : 1;   // 32 rows: even and odd warps have 16 each, and two blocks of positions
@@ -147,11 +149,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *status = &g_rows_status;
     Start *start = reinterpret_cast<Start *>(smem + L::kStart);
-    RowsPiece *pieces = reinterpret_cast<RowsPiece *>(smem + L::kPieces);
+    RowsPiece *pieces = reinterpret_cast<RowsPiece *>(smem + L::kPiece);
     auto full = [&](int i) { return sb + L::kBars + 8u * i; };
     auto empty = [&](int i) { return sb + L::kBars + 8u * (L::kStages + i); };
     auto piece_full = [&](int i) { return sb + L::kBars + 8u * (2 * L::kStages + i); };
-    auto piece_free = [&](int i) { return sb + L::kBars + 8u * (2 * L::kStages + 2 + i); };
+    auto piece_free = [&](int i) { return sb + L::kBars + 8u * (2 * L::kStages + L::kPieces + i); };
+    auto merge_full = [&](int i) { return sb + L::kBars + 8u * (2 * L::kStages + 2 * L::kPieces + i); };
+    auto merge_free = [&](int i) { return sb + L::kBars + 8u * (2 * L::kStages + 2 * L::kPieces + 2 + i); };
+    auto piece_at = [](uint32_t items) { return (int)(items % L::kPieces); };
+    auto piece_phase = [](uint32_t items) { return (items / L::kPieces) & 1; };
     follow_last_kernel();
 
     if (threadIdx.x == 0) {
@@ -159,9 +165,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(full(i), 1);
             mbar_init(empty(i), kWarps);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::kPieces; ++i) {
             mbar_init(piece_full(i), 1);
-            mbar_init(piece_free(i), kWarps);
+            mbar_init(piece_free(i), kWarps + kJoiners);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(merge_full(i), kWarps);
+            mbar_init(merge_free(i), kJoiners);
         }
         fence_mbar_init();
     }
@@ -174,71 +184,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int run_shift = min(a.page_shift, 7);  // log2 of the positions of one copy
     if (warp == kWarps) {
         // ---- copies ---------------------------------------------------------------------------
-        const uint32_t run_bytes = L::kRow << run_shift;
+        const uint32_t run_bytes = L::kRow << run_shift, q_bytes = a.g.group * HD * 2;
         const int blocks_shift = a.page_shift - 4;  // log2 of a page's blocks of scales
         uint32_t stage_no = 0, items = 0;
-        for (Walk w(a, s0);; w.next(a), ++items) {
-            RowsPiece &piece = pieces[items & 1];
-            mbar_wait(piece_free(items & 1), ((items >> 1) & 1) ^ 1, status);
-            const int t0 = w.t_beg(), p0 = w.kv - w.count + w.b.i0, token0 = w.first + w.b.i0;
+        // An item's piece, with what its positions are found by.
+        struct Source {
+            const int32_t *list;  // the token's pages, or NULL
+            int t0, lo, hi, token0, p0;
+        };
+        auto source = [&](const Walk &w) {
+            Source f;
+            f.token0 = w.first + w.b.i0, f.p0 = w.kv - w.count + w.b.i0, f.t0 = w.t_beg();
+            // (of a list the positions are those of its pages up to the token's own)
+            f.list = a.g.list ? a.lists + ((int64_t)f.token0 * a.g.kv_heads + w.head) * a.g.list : nullptr;
+            f.lo = a.g.list ? 0 : w.b.lo;
+            f.hi = a.g.list ? max(min(f.p0 + 1, a.g.table_end), 0) : w.b.hi;
+            return f;
+        };
+        // Four tiles at a time, a lane has one block of 16 positions (block lane % 8 of tile lane / 8): its
+        // first position and its page, or -1 where there is none, and its scales. The next four's pages, and
+        // the next piece's first, are on their way while these four are copied.
+        auto entry = [&](const Walk &w, const Source &f, int j, int &position, int &page) {
+            position = page = -1;
+            const int place = (f.t0 + j + (lane >> 3)) * kTileN + ((lane & 7) << 4);
+            if (j + (lane >> 3) >= w.n || place >= w.b.hi) return;
+            int at = place >> a.page_shift;
+            if (f.list) {
+                const int e = f.list[at], last = at ? f.list[at - 1] : -1;
+                if (e < 0 || (at && e <= last) || e >= a.max_pages) return;
+                at = e;
+            }
+            position = (at << a.page_shift) + (place & ((1 << a.page_shift) - 1));
+            // (a page's run is copied whole if any of it is attended to)
+            const int run = position & ~((1 << run_shift) - 1);
+            if (run < f.hi && run + (1 << run_shift) > f.lo && QDQ_CHECK(status, at >= 0 && at < a.max_pages)) page = w.pages[at];
+        };
+        auto scale = [&](const Walk &w, int position, int &page, int &e) {
+            if ((unsigned)page >= (unsigned)a.n_pages) page = -1;
+            if (KIND != kE4m3 || page < 0) return;
+            const int64_t at = (((int64_t)page * a.g.kv_heads + w.head) << blocks_shift) + ((position & ((1 << a.page_shift) - 1)) >> 4);
+            e = exponent_of(a.k_scales[at]) << 16 | (exponent_of(a.v_scales[at]) & 0xFFFF);
+        };
+        Walk w(a, s0), ahead = w;
+        Source f = source(w), f_ahead = f;
+        int position = -1, page = -1, e = 0, next_position = -1, next_page = -1, first_position = -1, first_page = -1;
+        if (w.more()) {
+            entry(w, f, 0, position, page);
+            entry(w, f, 4, next_position, next_page);
+        }
+        for (;; ++items) {
+            const int at = piece_at(items);
+            RowsPiece &piece = pieces[at];
+            mbar_wait(piece_free(at), piece_phase(items) ^ 1, status);
             if (lane == 0) {
                 piece.n = w.n;
                 if (w.n) {
-                    piece.t0 = t0;
-                    // (of a list the positions are those of its pages up to the token's own)
-                    piece.lo = a.g.list ? 0 : w.b.lo;
-                    piece.hi = a.g.list ? max(min(p0 + 1, a.g.table_end), 0) : w.b.hi;
-                    piece.tokens = w.b.i1 - w.b.i0, piece.token0 = token0, piece.p0 = p0;
+                    piece.t0 = f.t0;
+                    piece.lo = f.lo, piece.hi = f.hi;
+                    piece.tokens = w.b.i1 - w.b.i0, piece.token0 = f.token0, piece.p0 = f.p0;
                     piece.head = w.head;
                     piece.whole = w.whole();
                     if (!w.whole()) {
-                        piece.c_first = range_owner(s0.total, s0.ctas, w.item + kItemUnits);
-                        piece.c_last = range_owner(s0.total, s0.ctas, w.item + item_units(w.b) - 1);
+                        piece.c_first = range_owner(s0.total, s0.ctas, w.item + a.g.item);
+                        piece.c_last = range_owner(s0.total, s0.ctas, w.item + item_units(w.b, a.g.item) - 1);
                     }
                 }
-                mbar_arrive(piece_full(items & 1));
+                // (the group's heads of a token lie one behind the other)
+                mbar_arrive_expect_tx(piece_full(at), w.n ? piece.tokens * q_bytes : 0u);
             }
             __syncwarp();
             if (!w.more()) break;
-            const int32_t *list = a.g.list ? a.lists + ((int64_t)token0 * a.g.kv_heads + w.head) * a.g.list : nullptr;
-            const int hi = a.g.list ? max(min(p0 + 1, a.g.table_end), 0) : w.b.hi, lo = a.g.list ? 0 : w.b.lo;
-            // The lane's run of positions of tile j: its first position and its page, or -1 for either.
-            // (lanes past the tile's runs have none)
-            auto entry = [&](int j, int &position, int &page) {
-                position = page = -1;
-                const int place = j * kTileN + (lane << run_shift);
-                if (lane >= (kTileN >> run_shift) || place >= w.b.hi) return;
-                int at = place >> a.page_shift;
-                if (list) {
-                    const int e = list[at], last = at ? list[at - 1] : -1;
-                    if (e < 0 || (at && e <= last) || e >= a.max_pages) return;
-                    at = e;
-                }
-                position = (at << a.page_shift) + (place & ((1 << a.page_shift) - 1));
-                if (position < hi && position + (1 << run_shift) > lo &&
-                    QDQ_CHECK(status, at >= 0 && at < a.max_pages))
-                    page = w.pages[at];
-            };
-            int position, page, next_position = -1, next_page = -1;
-            entry(t0, position, page);
+            if (lane < w.b.i1 - w.b.i0 && QDQ_CHECK(status, f.token0 + lane < a.n_tokens && (lane + 1) * q_bytes <= L::kQSize))
+                bulk_g2s(sb + L::kQ + at * L::kQSize + lane * q_bytes,
+                         a.q + (int64_t)(f.token0 + lane) * a.q_stride + (int64_t)w.head * a.g.group * HD, q_bytes, piece_full(at));
+            scale(w, position, page, e);
             for (int j = 0; j < w.n; ++j, ++stage_no) {
-                if (j + 1 < w.n) entry(t0 + j + 1, next_position, next_page);
-                const int here = (unsigned)page < (unsigned)a.n_pages ? page : -1;
+                const int y = j & 3;
+                if (y == 0 && j) {
+                    position = next_position, page = next_page;
+                    scale(w, position, page, e);
+                    entry(w, f, j + 4, next_position, next_page);
+                }
+                // lane r issues the copies of the tile's run r
+                const int from = y * 8 + ((lane << run_shift) >> 4);
+                const int run_page = __shfl_sync(0xFFFFFFFFu, page, from & 31), run_position = __shfl_sync(0xFFFFFFFFu, position, from & 31);
+                const int here = lane < (kTileN >> run_shift) ? run_page : -1;
                 const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, here >= 0)) * run_bytes * 2;
                 const int stage = stage_no % L::kStages;
                 mbar_wait(empty(stage), ((stage_no / L::kStages) & 1) ^ 1, status);
-                // the scales of block `lane` of the tile, which lies in run lane * 16 >> run_shift
-                const int run = ((lane & 7) << 4) >> run_shift;
-                const int run_page = __shfl_sync(0xFFFFFFFFu, here, run), run_pos = __shfl_sync(0xFFFFFFFFu, position, run);
-                const int base = run_page < 0 ? -1 : run_pos + (((lane & 7) << 4) & ((1 << run_shift) - 1));
-                int ek = 0, ev = 0;
-                if (KIND == kE4m3 && base >= 0 && lane < 8) {
-                    const int64_t at = (((int64_t)run_page * a.g.kv_heads + w.head) << blocks_shift) +
-                                       ((base & ((1 << a.page_shift) - 1)) >> 4);
-                    ek = a.k_scales[at], ev = a.v_scales[at];
-                }
                 if (here >= 0) {
-                    const int in_page = position & ((1 << a.page_shift) - 1);
+                    const int in_page = run_position & ((1 << a.page_shift) - 1);
                     const uint32_t to = sb + stage * L::kStage + lane * run_bytes;
                     if (QDQ_CHECK(status, w.head < a.g.kv_heads && lane * run_bytes + run_bytes <= L::kHalf && here < a.n_pages)) {
                         if constexpr (KIND == kE4m3) {
@@ -252,32 +287,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (lane < 8) {
+                if (lane >> 3 == y) {
                     Meta *m = reinterpret_cast<Meta *>(smem + L::kMeta + stage * 64);
-                    m->base[lane] = base;
-                    m->ek[lane] = (int8_t)min(max(ek - 127, -40), 40);
-                    m->ev[lane] = (int8_t)min(max(ev - 127, -40), 40);
+                    m->base[lane & 7] = page < 0 ? -1 : position;
+                    m->ek[lane & 7] = (int8_t)(e >> 16);
+                    m->ev[lane & 7] = (int8_t)e;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(full(stage), bytes);
-                position = next_position, page = next_page;
+                if (j == 0) {
+                    ahead.next(a);
+                    if (ahead.more()) {
+                        f_ahead = source(ahead);
+                        entry(ahead, f_ahead, 0, first_position, first_page);
+                    }
+                }
             }
+            w = ahead, f = f_ahead;
+            position = first_position, page = first_page;
+            if (w.more()) entry(w, f, 4, next_position, next_page);
         }
         // every copy has landed before the CTA can end, also after a wait that ran out
         for (uint32_t i = stage_no < (uint32_t)L::kStages ? 0 : stage_no - L::kStages; i < stage_no; ++i)
             mbar_wait(full(i % L::kStages), (i / L::kStages) & 1, status);
+        for (uint32_t i = items < (uint32_t)L::kPieces ? 0 : items - L::kPieces + 1; i < items; ++i)
+            mbar_wait(piece_full(piece_at(i)), piece_phase(i), status);
         return;
     }
 
+    if (warp < kWarps) {
     // ---- the working warps -----------------------------------------------------------------------
     const int g = lane >> 2, c = lane & 3, half = warp % kHalves;
-    const float ln2 = 0.6931471805599453f;
-    uint32_t stage_no = 0;
+    uint32_t stage_no = 0, merges = 0;
     for (uint32_t items = 0;; ++items) {
-        mbar_wait(piece_full(items & 1), (items >> 1) & 1, status);
-        const RowsPiece w = pieces[items & 1];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(piece_free(items & 1));
+        const int at = piece_at(items);
+        mbar_wait(piece_full(at), piece_phase(items), status);
+        const RowsPiece w = pieces[at];
         if (w.n == 0) break;
         const int rows = w.tokens * a.g.group;
 
@@ -289,15 +334,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int z = 0; z < kGroups; ++z) {
             const int r = 16 * half + 8 * z + g, tok = r / a.g.group;
             const bool live = r < rows;
-            const uint16_t *q = a.q + (int64_t)(w.token0 + (live ? tok : 0)) * a.q_stride +
-                                (int64_t)(w.head * a.g.group + (live ? r - tok * a.g.group : 0)) * HD;
+            const uint32_t q = sb + L::kQ + at * L::kQSize + r * (HD * 2);
             // consecutive dims of the lane: KIND e4m3: HD / 4 from HD / 4 * c on; 16-bit: 16 from 64 h + 16 c on
             constexpr int kRun = KIND == kE4m3 ? HD / 4 : 16;
 #pragma unroll
             for (int k = 0; k < HD / 4; k += 8) {
                 const int dim = KIND == kE4m3 ? kRun * c + k : k / 16 * 64 + 16 * c + k % 16;
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (live) v = __ldg(reinterpret_cast<const uint4 *>(q + dim));
+                if (live) v = lds128(q + 2 * dim);
                 uint32_t *to = &qa[z][k / 2];
                 to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
             }
@@ -305,6 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             row_lo[z] = a.g.window ? max(p - a.g.window + 1, 0) : 0;
             row_hi[z] = live ? min(p + 1, w.hi) : 0;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_free(at));
         // positions that every row attends to
         const int all_lo = a.g.window ? max(w.p0 + w.tokens - a.g.window, 0) : 0, all_hi = min(w.p0 + 1, w.hi);
 
@@ -462,9 +508,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(empty(stage));
         }
 
-        // ---- the piece's end: the warps' states are joined, eight rows of each at a time -----------------------
-        float2 *state = reinterpret_cast<float2 *>(smem + L::kState);
-        const int part = (blockIdx.x * 2 + (!w.whole && (int)blockIdx.x == w.c_first ? 1 : 0));
+        // ---- the piece's end: the warp's state, eight rows at a time --------------------------------------
+#pragma unroll
+        for (int z = 0; z < kGroups; ++z) {
+            if (8 * z >= rows) break;
+            const int room = merges & 1, mine = 16 * half + 8 * z + g;
+            mbar_wait(merge_free(room), ((merges >> 1) & 1) ^ 1, status);
+            ++merges;
+            l[z] += __shfl_xor_sync(0xFFFFFFFFu, l[z], 1);
+            l[z] += __shfl_xor_sync(0xFFFFFFFFu, l[z], 2);
+            if (c == 0) reinterpret_cast<float2 *>(smem + L::kState)[(room * kWarps + warp) * 8 + g] = make_float2(m[z], l[z]);
+            // the lane's columns 2 c and 2 c + 1, kN dims each
+            if (mine < rows) {
+                float *to = reinterpret_cast<float *>(smem + L::kMerge + room * L::kMergeSize + (warp * 8 + g) * L::kPitch);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int n = 0; n < kN; n += 4) {
+                        float e[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            e[y] = kPacked ? o[n + y][x] + o[n + y][2 + x] : o[n + y][2 * z + x];
+                        const int dim = KIND == kE4m3 || HD == 64 ? (2 * c + x) * kN + n : n / 8 * 64 + (2 * c + x) * 8 + n % 8;
+                        *reinterpret_cast<float4 *>(to + dim) = make_float4(e[0], e[1], e[2], e[3]);
+                    }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(merge_full(room));
+        }
+    }
+    return;
+    }
+
+    // ---- the joining warps --------------------------------------------------------------------------
+    const int tid = threadIdx.x - (kWarps + 1) * 32;
+    constexpr int kJoin = kJoiners * 32;
+    const float ln2 = 0.6931471805599453f;
+    int *flag = reinterpret_cast<int *>(smem + L::kStart);
+    uint32_t merges = 0;
+    for (uint32_t items = 0;; ++items) {
+        const int piece_no = piece_at(items);
+        mbar_wait(piece_full(piece_no), piece_phase(items), status);
+        const RowsPiece w = pieces[piece_no];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(piece_free(piece_no));
+        if (w.n == 0) break;
+        const int rows = w.tokens * a.g.group;
+        const int part = blockIdx.x * 2 + (!w.whole && (int)blockIdx.x == w.c_first ? 1 : 0);
         auto store = [&](int row, int dim, float4 v) {
             const int tok = row / a.g.group;
             const int64_t at = (int64_t)(w.token0 + tok) * a.out_stride + (int64_t)(w.head * a.g.group + row - tok * a.g.group) * HD + dim;
@@ -485,31 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 a.lse[(int64_t)(w.token0 + tok) * a.n_heads + w.head * a.g.group + row - tok * a.g.group] =
                     sum != 0.0f ? (top - kLift + log2f(sum)) * ln2 : -INFINITY;
         };
-        named_bar_sync(1, kWarps * 32);  // (the last piece's states have been read)
-#pragma unroll
-        for (int z = 0; z < kGroups; ++z) {
-            if (8 * z >= rows) break;
-            const int mine = 16 * half + 8 * z + g;
-            l[z] += __shfl_xor_sync(0xFFFFFFFFu, l[z], 1);
-            l[z] += __shfl_xor_sync(0xFFFFFFFFu, l[z], 2);
-            if (c == 0) state[warp * 8 + g] = make_float2(m[z], l[z]);
-            // the lane's columns 2 c and 2 c + 1, kN dims each
-            if (mine < rows) {
-                float *to = reinterpret_cast<float *>(smem + L::kMerge + (warp * 8 + g) * L::kPitch);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-#pragma unroll
-                    for (int n = 0; n < kN; n += 4) {
-                        float e[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            e[y] = kPacked ? o[n + y][x] + o[n + y][2 + x] : o[n + y][2 * z + x];
-                        const int dim = KIND == kE4m3 || HD == 64 ? (2 * c + x) * kN + n : n / 8 * 64 + (2 * c + x) * 8 + n % 8;
-                        *reinterpret_cast<float4 *>(to + dim) = make_float4(e[0], e[1], e[2], e[3]);
-                    }
-            }
-            named_bar_sync(1, kWarps * 32);
-            for (int x = threadIdx.x; x < kHalves * 8 * (HD / 4); x += kWarps * 32) {
+        for (int z = 0; z < kGroups && 8 * z < rows; ++z, ++merges) {
+            const int room = merges & 1;
+            mbar_wait(merge_full(room), (merges >> 1) & 1, status);
+            const float2 *state = reinterpret_cast<const float2 *>(smem + L::kState) + room * kWarps * 8;
+            for (int x = tid; x < kHalves * 8 * (HD / 4); x += kJoin) {
                 const int i = x / (HD / 4), dim = x % (HD / 4) * 4, r = i % 8, h = i / 8, row = 16 * h + 8 * z + r;
                 if (row >= rows) continue;
                 float top = -INFINITY, sum = 0.0f;
@@ -520,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int y = h; y < kWarps; y += kHalves) {
                     const float2 ml = state[y * 8 + r];
                     const float f = ml.y != 0.0f ? ex2(ml.x - top) : 0.0f;  // (a sum that is no number stays none)
-                    const float4 v = *reinterpret_cast<const float4 *>(smem + L::kMerge + (y * 8 + r) * L::kPitch + dim * 4);
+                    const float4 v = *reinterpret_cast<const float4 *>(smem + L::kMerge + room * L::kMergeSize + (y * 8 + r) * L::kPitch + dim * 4);
                     sum = fmaf(ml.y, f, sum);
                     acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
                 }
@@ -533,15 +603,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (dim == 0) __stcg(a.part_ml + part * kMostRows + row, make_float2(top, sum));
                 }
             }
-            if (z + 1 < kGroups) named_bar_sync(1, kWarps * 32);  // (the merge's room is used again)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(merge_free(room));
         }
         if (w.whole) continue;
 
         // ---- the last of an item's parts joins them all, in CTA order ---------------------------------------
-        int *flag = reinterpret_cast<int *>(smem + L::kStart);
-        named_bar_sync(1, kWarps * 32);
-        if (threadIdx.x == 0) {
-            // (the fence covers the whole CTA's stores, which the barrier has shown this thread; the count
+        named_bar_sync(1, kJoin);
+        if (tid == 0) {
+            // (the fence covers the warps' stores, which the barrier has shown this thread; the count
             // goes back to zero by itself)
             __threadfence();
             const unsigned others = (unsigned)(w.c_last - w.c_first);
@@ -549,13 +619,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             *flag = atomicInc(counter, others) == others;
             __threadfence();
         }
-        named_bar_sync(1, kWarps * 32);
-        if (!*flag) continue;
-        for (int x = threadIdx.x; x < rows * (HD / 4); x += kWarps * 32) {
+        named_bar_sync(1, kJoin);
+        const bool last = *flag != 0;
+        named_bar_sync(1, kJoin);
+        if (!last) continue;
+        for (int x = tid; x < rows * (HD / 4); x += kJoin) {
             const int row = x / (HD / 4), dim = x % (HD / 4) * 4;
             float top = -INFINITY, sum = 0.0f;
             float4 acc = make_float4(0, 0, 0, 0);
-            constexpr int kAtOnce = 4;
+            constexpr int kAtOnce = 8;
             for (int cta = w.c_first; cta <= w.c_last; cta += kAtOnce) {
                 float2 ml[kAtOnce];
                 float4 v[kAtOnce];
@@ -600,7 +672,10 @@ struct Choice {
     uint32_t smem;
 };
 Choice choose(int head_dim, int type, int mode) {
-#define QDQ_ROWS(HD, KIND) Choice{kernel_of<HD, KIND>(mode), Shape<HD, KIND>::kTotal}
+#define QDQ_ROWS(HD, KIND)                                                                      \
+    Choice{kernel_of<HD, KIND>(mode), mode == 0   ? Shape<HD, KIND, 0>::kTotal                  \
+                                      : mode == 1 ? Shape<HD, KIND, 1>::kTotal                  \
+                                                  : Shape<HD, KIND, 2>::kTotal}
     if (head_dim == 64) return type == QDQ_E4M3 ? QDQ_ROWS(64, kE4m3) : type == QDQ_BF16 ? QDQ_ROWS(64, kBf16) : QDQ_ROWS(64, kF16);
     return type == QDQ_E4M3 ? QDQ_ROWS(128, kE4m3) : type == QDQ_BF16 ? QDQ_ROWS(128, kBf16) : QDQ_ROWS(128, kF16);
 #undef QDQ_ROWS
@@ -691,6 +766,7 @@ int launch_rows(const RowsState *st, const AttendArgs &a, cudaStream_t stream) {
     k.g.window = a.window < INT32_MAX - a.n_tokens ? a.window : INT32_MAX - a.n_tokens;
     k.g.table_end = a.max_pages * p.page_size;
     k.g.list = a.lists ? a.list : 0;
+    k.g.item = 2;
     k.g.page_shift = k.page_shift;
     k.part_o = st->part_o, k.part_ml = st->part_ml, k.counters = st->counters;
     const Choice c = choose(p.head_dim, p.type, mode);

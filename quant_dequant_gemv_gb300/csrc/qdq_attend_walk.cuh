@@ -32,7 +32,7 @@ struct Walk {
         load_seq(a);
         b = block_of(a.g, count, kv, block);
         int last;
-        piece_of(b, item, pos, end, off, last);
+        piece_of(b, item, pos, end, off, last, a.g.item);
         n = last - off;
         if (n == 0) next(a);  // (the range begins past the item's tiles or ends before them)
     }
@@ -41,7 +41,7 @@ struct Walk {
     QDQ_DEV bool whole() const { return n == b.t1 - b.t0; }
     template <typename A>
     QDQ_DEV void next(const A &a) {
-        item += item_units(b);
+        item += item_units(b, a.g.item);
         pos = item;
         n = 0;
         if (item >= end) return;
@@ -57,7 +57,7 @@ struct Walk {
             b = block_of(a.g, count, kv, block);
         }
         int last;
-        piece_of(b, item, pos, end, off, last);
+        piece_of(b, item, pos, end, off, last, a.g.item);
         n = last - off;  // 0 at the end of the range, where only the item's first units are left
     }
 };
@@ -79,7 +79,7 @@ QDQ_DEV void find_start(const A &a, char *room, Start *start) {
         kvs[s] = kv;
         int sum = 0;
         if (nb <= kAlone) {
-            for (int b = 0; b < nb; ++b) sum += item_units(block_of(a.g, count, kv, b));
+            for (int b = 0; b < nb; ++b) sum += item_units(block_of(a.g, count, kv, b), a.g.item);
         } else {
             longer = true;
         }
@@ -90,7 +90,7 @@ QDQ_DEV void find_start(const A &a, char *room, Start *start) {
             const int nb = seq_blocks(a.g, cnt[s]);
             if (nb <= kAlone) continue;
             long long sum = 0;
-            for (int b = lane; b < nb; b += 32) sum += item_units(block_of(a.g, cnt[s], kvs[s], b));
+            for (int b = lane; b < nb; b += 32) sum += item_units(block_of(a.g, cnt[s], kvs[s], b), a.g.item);
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
             if (lane == 0) pre[s] = sum * a.g.kv_heads;
         }
@@ -135,7 +135,7 @@ QDQ_DEV void find_start(const A &a, char *room, Start *start) {
             const int nb = seq_blocks(a.g, cnt[s]);
             for (int b0 = 0; b0 < nb; b0 += 32) {
                 int n = 0;
-                if (b0 + lane < nb) n = item_units(block_of(a.g, cnt[s], kvs[s], b0 + lane));
+                if (b0 + lane < nb) n = item_units(block_of(a.g, cnt[s], kvs[s], b0 + lane), a.g.item);
                 long long run = (long long)n * a.g.kv_heads;
                 const long long own = run;
                 for (int o = 1; o < 32; o <<= 1) {
