@@ -406,7 +406,7 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  *   out[t][h] = sum_j a_j v_j,  a = softmax_j(scale * q . k_j),
  * over the sequence's positions j <= p, and j > p - window when window > 0.
  * scale: of either sign, or 0 (the mean of the values); scale * log2(e) has to be
- * finite in fp32 (QDQ_ERR_SHAPE).
+ * finite in fp32, over a cache of e4m3 values times 2^40 too (QDQ_ERR_SHAPE).
  * q: [n_tokens][n_heads * head_dim] of the pools' type (append's q_out), out: of
  * the pools' type or QDQ_F32; row strides in elements, rows 16-byte aligned.
  * lse (NULL or fp32 [n_tokens][n_heads]): log sum_j exp(scale * q . k_j).
@@ -422,7 +422,9 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * inside it are taken to be finite (a position that only later tokens of a chunk
  * attend to has weight zero for the earlier ones, and 0 x inf is no number).
  * Over a cache of e4m3 values the query meets the keys' e4m3 values exactly and their scales
- * in fp32; a weight with its value's scale in it meets the values in two fp16 terms.
+ * in fp32; a weight, with its value's scale in it, meets the values in two fp16 terms, or in
+ * one, rounded once, for a 16-bit out where a step has more than 32 rows (tokens x query
+ * heads of a kv head) a sequence on average.
  * One launch; results do not depend on timing (no floating-point atomics). */
 int qdq_paged_attention(qdq_paged *cache, int layer, const qdq_paged_batch *batch, const void *q, int64_t q_stride,
                         int out_type, void *out, int64_t out_stride, float scale, int window, float *lse,

@@ -52,6 +52,13 @@
 // Values in rows of V outside the block's positions are zeroed in shared memory before
 // their product (their weights are zero, but 0 x NaN is not), scores there are replaced
 // by -inf whatever K held.
+//
+// A cache of e4m3 values (KV8): two of the third warpgroup's warps widen the copied bytes to fp16,
+// which holds them exactly, into the ring that the matrix instructions read (and leave out the rows
+// outside the block's positions there). The scales of 16 positions stay out of the products: 2^ek
+// goes into the scores' factor, and with 2^ev the weight that meets the values is 2^(t + ev - m),
+// m the maximum of t + ev, l the sum of those weights times 2^-ev (as in qdq_attend_rows.cu, which
+// takes the batches of few rows).
 #include <cmath>
 #include <cuda.h>
 #include <limits>
@@ -99,6 +106,8 @@ struct KernelArgs {
     float scale_log2;  // |scale| * log2(e); a negative scale negates Q in the instruction
     uint32_t idesc_qk, idesc_pv;
     int n_pages, page_shift, row8_layer;  // row8_layer: first group of 8 rows of the layer
+    int page0, out_bf16;                  // KV8: the layer's first page; whether 16-bit results are bf16
+    const uint8_t *k_scales, *v_scales;   // KV8: of the layer
     int n_heads;
     AttendGeometry g;
     float *part_o;
@@ -106,16 +115,22 @@ struct KernelArgs {
     unsigned *counters;
 };
 
-template <int HD>
+template <int HD, bool KV8>
 struct Shape {
     static constexpr int kHalves = HD / 64;
     static constexpr uint32_t kQTile = 128u * HD * 2u;
     static constexpr uint32_t kSlot = (uint32_t)kTileN * HD * 2u;
-    static constexpr int kSlots = HD == 128 ? 5 : 10;
+    static constexpr int kSlots = KV8 ? (HD == 128 ? 3 : 6) : HD == 128 ? 5 : 10;
     static constexpr uint32_t kGroup8 = (uint32_t)kHalves * 1024u;  // 8 positions of a slot
     static constexpr uint32_t kQ = 0, kRing = 2 * kQTile;
-    static constexpr uint32_t kBars = kRing + kSlots * kSlot;
-    static constexpr uint32_t kScratch = kBars + 304;        // a state handed from set to set, a join's flag
+    // KV8: the ring of bytes as they are copied, and each of kNotes tiles' scales and rows. (A tile's notes
+    // are written over when the copies are kNotes tiles on: its bytes' slots have then been taken up
+    // 2 kNotes - kRawSlots copies on, whose slots of the ring were free once its weights had been used.)
+    static constexpr int kRawSlots = KV8 ? (HD == 128 ? 4 : 8) : 0, kNotes = 8;
+    static constexpr uint32_t kRawSlot = (uint32_t)kTileN * HD, kRaw = kRing + kSlots * kSlot;
+    static_assert(!KV8 || 2 * kNotes >= kRawSlots + kSlots + 2, "kNotes");
+    static constexpr uint32_t kBars = kRaw + kRawSlots * kRawSlot;
+    static constexpr uint32_t kScratch = kBars + (KV8 ? 304 + 2 * 8 * 8 : 304);        // a state handed from set to set, a join's flag
     static constexpr uint32_t kStart = kScratch + 2 * 128 * 8;  // the CTA's first piece, tensor-memory base
     // Tensor memory: S of the two sets in columns 0..255, O from kColO on. A weight's two terms
     // lie over S, 64 columns each. One term alone has, at 64 dims, columns of its own, so that the
@@ -124,12 +139,22 @@ struct Shape {
     static constexpr int kColOne = kApart ? kColO + 2 * HD : 0, kPitchOne = kApart ? 64 : 128;
     static constexpr int kColRest = 64;  // of the second term, from the first one's
     static constexpr uint32_t kPieces = kStart + 64;
-    static constexpr uint32_t kTotal = kPieces + 192;
+    static constexpr uint32_t kNote = kPieces + 192;
+    static constexpr uint32_t kTotal = kNote + (KV8 ? kNotes * 32 : 0);
+    static_assert(kTotal <= 232448, "shared memory");
 };
+
+// KV8, of a tile's eight blocks of 16 positions: the scales' exponents, and the rows that hold a
+// position of the block.
+struct Note {
+    int8_t ek[8], ev[8];
+    uint16_t rows[8];
+};
+static_assert(sizeof(Note) == 32, "Shape::kNote");
 // barriers (8 bytes each) at kBars
 constexpr int kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 21, kBarS = 22, kBarP = 24, kBarPv = 26,
               kBarOFree = 28, kBarDrain = 30, kBarPiece = 31, kBarPieceFree = 33,
-              kBarSFree = 35;
+              kBarSFree = 35, kBarRawFull = 38, kBarRawEmpty = 46;
 
 // What the other warps need of a piece, in one of two places in shared memory.
 struct Piece {
@@ -164,11 +189,11 @@ QDQ_DEV float max3(float a, float b, float c) {
     return d;
 }
 
-template <int HD, bool BF16, bool OUT32>
+template <int HD, bool BF16, bool OUT32, bool KV8>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap q_map,
                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using L = Shape<HD>;
+    using L = Shape<HD, KV8>;
     using F16 = Float16<typename std::conditional<BF16, __nv_bfloat16, __half>::type>;
     // Whether both terms of the weights are multiplied, with the sets on alternate key tiles and on two
     // tiles of rows.
@@ -184,8 +209,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kSlots; ++i) {
-            mbar_init(bar(kBarFull + i), 1);
+            mbar_init(bar(kBarFull + i), KV8 ? 2 : 1);
             mbar_init(bar(kBarEmpty + i), 1);
+        }
+        for (int i = 0; i < L::kRawSlots; ++i) {
+            mbar_init(bar(kBarRawFull + i), 1);
+            mbar_init(bar(kBarRawEmpty + i), 2);
         }
         mbar_init(bar(kBarQFull), 1);
         mbar_init(bar(kBarQEmpty), 1);
@@ -198,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBarPiece + i), 1);
-            mbar_init(bar(kBarPieceFree + i), 9);
+            mbar_init(bar(kBarPieceFree + i), KV8 ? 11 : 9);
         }
         mbar_init(bar(kBarDrain), 1);
         fence_mbar_init();
@@ -272,6 +301,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 < n) page = tile_page(a, piece, t0 + j + 1, run_shift);
                     const unsigned have = __ballot_sync(0xFFFFFFFFu, here >= 0);
                     const uint32_t bytes = __popc(have) * run_bytes;
+                    if constexpr (KV8) {
+                        const uint32_t raw_run = (uint32_t)HD << run_shift;
+                        const int in_page = ((t0 + j) * kTileN + (lane << run_shift)) & ((1 << a.page_shift) - 1);
+                        // block `lane` of the tile lies in run lane * 16 >> run_shift
+                        const int run = ((lane & 7) << 4) >> run_shift, p0 = (t0 + j) * kTileN + ((lane & 7) << 4);
+                        const int run_page = __shfl_sync(0xFFFFFFFFu, here, run);
+                        int ek = 0, ev = 0;
+                        if (run_page >= 0 && lane < 8) {
+                            const int64_t at = (((int64_t)run_page * a.g.kv_heads + w.head) << (a.page_shift - 4)) +
+                                               ((p0 & ((1 << a.page_shift) - 1)) >> 4);
+                            ek = exponent_of(a.k_scales[at]), ev = exponent_of(a.v_scales[at]);
+                        }
+#pragma unroll
+                        for (int kv = 0; kv < 2; ++kv, ++seq_no) {
+                            const int slot = seq_no % L::kRawSlots;
+                            mbar_wait(bar(kBarRawEmpty + slot), ((seq_no / L::kRawSlots) & 1) ^ 1, status);
+                            if (here >= 0 && QDQ_CHECK(status, here < a.n_pages && w.head < a.g.kv_heads && lane * raw_run + raw_run <= L::kRawSlot))
+                                tma_load_3d(sb + L::kRaw + slot * L::kRawSlot + (uint32_t)lane * raw_run, kv ? &v_map : &k_map, 0,
+                                            (w.head << a.page_shift) + in_page, a.page0 + here, bar(kBarRawFull + slot));
+                            if (kv == 0 && lane < 8) {
+                                Note *note = reinterpret_cast<Note *>(smem + L::kNote) + (seq_no >> 1) % L::kNotes;
+                                const int b = min(max(w.b.lo - p0, 0), 16), e = min(max(w.b.hi - p0, 0), 16);
+                                note->ek[lane] = (int8_t)ek, note->ev[lane] = (int8_t)ev;
+                                note->rows[lane] = run_page >= 0 && e > b ? (uint16_t)((1u << e) - (1u << b)) : 0;
+                            }
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_expect_tx(bar(kBarRawFull + slot), __popc(have) * raw_run);
+                        }
+                        continue;
+                    }
                     // the lane's run of positions: its first group of 8 rows in the pools
                     const int in_page = ((t0 + j) * kTileN + (lane << run_shift)) & ((1 << a.page_shift) - 1);
                     const int row8 = a.row8_layer + (int)((((int64_t)here << a.page_shift) + in_page) >> 3);
@@ -290,8 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // every copy has landed before the CTA can end, also after a wait that ran out
-            for (uint32_t i = seq_no < (uint32_t)L::kSlots ? 0 : seq_no - L::kSlots; i < seq_no; ++i)
-                mbar_wait(bar(kBarFull + i % L::kSlots), (i / L::kSlots) & 1, status);
+            constexpr uint32_t kLast = KV8 ? L::kRawSlots : L::kSlots;
+            for (uint32_t i = seq_no < kLast ? 0 : seq_no - kLast; i < seq_no; ++i)
+                mbar_wait(bar((KV8 ? kBarRawFull : kBarFull) + i % kLast), (i / kLast) & 1, status);
             if (items) mbar_wait(bar(kBarQFull), (items - 1) & 1, status);
         } else if (warp == kWarpMma) {
             // ---- matrix instructions ----------------------------------------------------------
@@ -433,6 +493,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) mma_commit(bar(kBarDrain));
             __syncwarp();
             mbar_wait(bar(kBarDrain), 0, status);
+        } else if constexpr (KV8) {
+            // ---- bytes to fp16: 64 positions of a tile a warp --------------------------------------
+            // A lane takes 16 bytes of a row, which are two 16-byte pieces of the widened row; 8 lanes store
+            // to 8 different places of the swizzle at once (of 128 dims, the upper half's lanes store
+            // their second piece first).
+            constexpr int kChunks = HD / 16, kRows = 32 / kChunks;  // lanes of a row, rows at once
+            const int mine = warp - kWarpLoad - 1, chunk = lane % kChunks, sub = lane / kChunks;
+            const bool swap = HD == 128 && chunk >= 4;
+            uint32_t seq_no = 0;
+            for (uint32_t items = 0;; ++items) {
+                const Piece &w = pieces[items & 1];
+                mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
+                const int n = w.n;
+                __syncwarp();
+                if (n == 0) break;
+                if (lane == 0) mbar_arrive(bar(kBarPieceFree + (items & 1)));
+                for (int x = 0; x < 2 * n; ++x, ++seq_no) {
+                    const int raw = seq_no % L::kRawSlots, slot = seq_no % L::kSlots;
+                    mbar_wait(bar(kBarRawFull + raw), (seq_no / L::kRawSlots) & 1, status);
+                    mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
+                    const Note &note = reinterpret_cast<const Note *>(smem + L::kNote)[(seq_no >> 1) % L::kNotes];
+                    const uint32_t from = sb + L::kRaw + raw * L::kRawSlot + chunk * 16;
+                    const uint32_t to = sb + L::kRing + slot * L::kSlot + (HD == 128 ? (chunk / 4) * 1024u : 0u);
+                    constexpr int kDeep = 4;  // loads in flight
+#pragma unroll 1
+                    for (int r0 = mine * 64; r0 < mine * 64 + 64; r0 += kDeep * kRows) {
+                        uint4 v[kDeep];
+#pragma unroll
+                        for (int y = 0; y < kDeep; ++y) v[y] = lds128(from + (r0 + y * kRows + sub) * HD);
+                        const uint32_t live = note.rows[r0 / 16] | (kDeep * kRows > 16 ? (uint32_t)note.rows[r0 / 16 + 1] << 16 : 0u);
+#pragma unroll
+                        for (int y = 0; y < kDeep; ++y) {
+                            const int r = r0 + y * kRows + sub;
+                            if (!((live >> ((y * kRows + sub) % (kDeep * kRows > 16 ? 32 : 16))) & 1)) v[y] = make_uint4(0, 0, 0, 0);
+                            const uint32_t a0 = swap ? v[y].z : v[y].x, a1 = swap ? v[y].w : v[y].y;
+                            const uint32_t b0 = swap ? v[y].x : v[y].z, b1 = swap ? v[y].y : v[y].w;
+                            uint4 f, g;
+                            e4m3x4_to_f16(a0, f.x, f.y);
+                            e4m3x4_to_f16(a1, f.z, f.w);
+                            e4m3x4_to_f16(b0, g.x, g.y);
+                            e4m3x4_to_f16(b1, g.z, g.w);
+                            const uint32_t row = to + (r >> 3) * L::kGroup8 + (r & 7) * 128, c = (2 * chunk) & 7;
+                            const uint32_t first = row + (((c + (swap ? 1 : 0)) ^ (r & 7)) << 4), second = row + (((c + (swap ? 0 : 1)) ^ (r & 7)) << 4);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(second), "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
+                        }
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(kBarFull + slot));
+                        mbar_arrive(bar(kBarRawEmpty + raw));
+                    }
+                }
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -516,6 +631,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!idle) {
                     float s[4][32], mx[4];
+                    int8_t ek[KV8 ? 8 : 1], ev[KV8 ? 8 : 1];
+                    if constexpr (KV8) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::kNote + ((base >> 1) + (j - t0)) % L::kNotes * 32);
+                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) ek[y] = (int8_t)(u[y / 4] >> (8 * (y % 4))), ev[y] = (int8_t)(u[2 + y / 4] >> (8 * (y % 4)));
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tc_ld32(t_s + 32 * k, s[k]);
 #pragma unroll
@@ -524,18 +646,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mask(s[k], k);
                     }
+                    if constexpr (KV8) {
+                        // (block by block, in the units of the weights)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s[y][0], s[y][1]);
+                        for (int y = 0; y < 4; ++y) {
+                            float b[2];
 #pragma unroll
-                    for (int k = 2; k < 32; k += 2)
+                            for (int z = 0; z < 2; ++z) {
+                                b[z] = fmaxf(s[y][16 * z], s[y][16 * z + 1]);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[y][k], s[y][k + 1]);
+                                for (int k = 2; k < 16; k += 2) b[z] = max3(b[z], s[y][16 * z + k], s[y][16 * z + k + 1]);
+                                b[z] = fmaf(b[z], c * power_of_two(ek[2 * y + z]), (float)ev[2 * y + z]);
+                            }
+                            mx[y] = fmaxf(b[0], b[1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s[y][0], s[y][1]);
+#pragma unroll
+                        for (int k = 2; k < 32; k += 2)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[y][k], s[y][k + 1]);
+                    }
+                    const float unit = KV8 ? 1.0f : c;  // of the maximum, in weights' exponents
                     const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                     if (j == j0) {
                         m = mn;
-                    } else if (__any_sync(0xFFFFFFFFu, (mn - m) * c > lag)) {
+                    } else if (__any_sync(0xFFFFFFFFu, (mn - m) * unit > lag)) {
                         // raise the maximum of the warp's rows: O and l change units
-                        const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
+                        const float f = mn == -INFINITY ? 1.0f : ex2((m - mn) * unit);
                         m = mn;
                         l *= f;
                         mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
@@ -556,15 +695,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tmem_wait_st();
                     }
-                    const float mc = m == -INFINITY ? 0.0f : fmaf(m, c, -kLift<BF16>);
+                    const float mc = m == -INFINITY ? 0.0f : fmaf(m, unit, -kLift<BF16>);
                     const uint64_t mc2 = pack2(-mc, -mc);
                     uint64_t sum[2] = {};
-                    auto weights = [&](const float *s, uint32_t *to, uint32_t *left, auto rest) {
+                    auto weights = [&](const float *s, uint32_t *to, uint32_t *left, auto rest, int block) {
+                        uint64_t f2 = c2, g2 = mc2;
+                        [[maybe_unused]] uint64_t h2 = 0, part = 0;
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            const uint64_t e = ffma2(pack2(s[k], s[k + 1]), c2, mc2);
+                            if constexpr (KV8) {
+                                if (k % 16 == 0) {
+                                    const float f = c * power_of_two(ek[block + k / 16]), g = (float)ev[block + k / 16] - mc;
+                                    const float h = power_of_two(-ev[block + k / 16]);
+                                    f2 = pack2(f, f), g2 = pack2(g, g), h2 = pack2(h, h), part = 0;
+                                }
+                            }
+                            const uint64_t e = ffma2(pack2(s[k], s[k + 1]), f2, g2);
                             const float p = ex2(lo_of(e)), q = ex2(hi_of(e));
-                            sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
+                            if constexpr (KV8) {
+                                part = fadd2(part, pack2(p, q));
+                                if (k % 16 == 14) sum[(k / 16) & 1] = ffma2(part, h2, sum[(k / 16) & 1]);
+                            } else {
+                                sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
+                            }
                             to[k / 2] = F16::pack(p, q);
                             if constexpr (rest.value) {
                                 const float2 h = F16::unpack(to[k / 2]);
@@ -576,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t u[32], left[32];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            weights(s[2 * h], u, left, rest);
-                            weights(s[2 * h + 1], u + 16, left + 16, rest);
+                            weights(s[2 * h], u, left, rest, 4 * h);
+                            weights(s[2 * h + 1], u + 16, left + 16, rest, 4 * h + 2);
                             if constexpr (rest.value) {
                                 tc_st32(t_s + 32 * h, u);
                                 tc_st32(t_s + L::kColRest + 32 * h, left);
@@ -593,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t t = fadd2(sum[0], sum[1]);
                     l += lo_of(t) + hi_of(t);
                 }
-                if (dirty) {
+                if (!KV8 && dirty) {
                     // zero the rows of V that hold no position of the block (row r of the slot)
                     const uint32_t vs = base + 2 * (j - t0) + 1;
                     mbar_wait(bar(kBarFull + vs % L::kSlots), (vs / L::kSlots) & 1, status);
@@ -615,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---- the piece's end ------------------------------------------------------------
             const bool any = j1 > j0;
-            float mc = m == -INFINITY ? -INFINITY : fmaf(m, c, -kLift<BF16>), f0 = 1.0f, f1 = 0.0f;
+            float mc = m == -INFINITY ? -INFINITY : fmaf(m, KV8 ? 1.0f : c, -kLift<BF16>), f0 = 1.0f, f1 = 0.0f;
             if (any) {
                 mbar_wait_spin(bar(kBarPv + i), (npv - 1) & 1, status);
                 tc_fence_after();
@@ -676,9 +829,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     to[0] = make_float4(o[0] * f, o[1] * f, o[2] * f, o[3] * f);
                     to[1] = make_float4(o[4] * f, o[5] * f, o[6] * f, o[7] * f);
                 } else {
+                    auto pack = [&](float x, float y) {
+                        return KV8 && a.out_bf16 ? Float16<__nv_bfloat16>::pack(x, y) : F16::pack(x, y);
+                    };
                     *reinterpret_cast<uint4 *>((uint16_t *)a.out + at) =
-                        make_uint4(F16::pack(o[0] * f, o[1] * f), F16::pack(o[2] * f, o[3] * f),
-                                   F16::pack(o[4] * f, o[5] * f), F16::pack(o[6] * f, o[7] * f));
+                        make_uint4(pack(o[0] * f, o[1] * f), pack(o[2] * f, o[3] * f), pack(o[4] * f, o[5] * f), pack(o[6] * f, o[7] * f));
                 }
             };
             const float ln2 = 0.6931471805599453f;
@@ -872,26 +1027,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-bool encode(CUtensorMap *map, bool bf16, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
-            const cuuint32_t *box) {
+bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     EncodeTiled enc = encode_fn();
-    return enc && enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
-                      const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc && enc(map, type, rank, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 using Kernel = void (*)(KernelArgs, CUtensorMap, CUtensorMap, CUtensorMap);
-template <bool OUT32>
-Kernel kernel_of(int head_dim, bool bf16) {
-    if (head_dim == 64) return bf16 ? attend_kernel<64, true, OUT32> : attend_kernel<64, false, OUT32>;
-    return bf16 ? attend_kernel<128, true, OUT32> : attend_kernel<128, false, OUT32>;
+template <int HD, bool OUT32>
+Kernel kernel_of(int type) {
+    return type == QDQ_E4M3   ? attend_kernel<HD, false, OUT32, true>
+           : type == QDQ_BF16 ? attend_kernel<HD, true, OUT32, false>
+                              : attend_kernel<HD, false, OUT32, false>;
 }
-Kernel kernel_of(int head_dim, bool bf16, bool out_f32) {
-    return out_f32 ? kernel_of<true>(head_dim, bf16) : kernel_of<false>(head_dim, bf16);
+Kernel kernel_of(int head_dim, int type, bool out_f32) {
+    if (head_dim == 64) return out_f32 ? kernel_of<64, true>(type) : kernel_of<64, false>(type);
+    return out_f32 ? kernel_of<128, true>(type) : kernel_of<128, false>(type);
 }
-uint32_t smem_of(int head_dim) { return head_dim == 64 ? Shape<64>::kTotal : Shape<128>::kTotal; }
+uint32_t smem_of(int head_dim, int type) {
+    if (type == QDQ_E4M3) return head_dim == 64 ? Shape<64, true>::kTotal : Shape<128, true>::kTotal;
+    return head_dim == 64 ? Shape<64, false>::kTotal : Shape<128, false>::kTotal;
+}
+CUtensorMapDataType data_type(int type) { return type == QDQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16; }
 
 }  // namespace
 
@@ -906,8 +1065,18 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
     const cuuint64_t rows = (cuuint64_t)p.n_layers * p.n_pages * p.page_size;
     const cuuint64_t dims[4] = {64, 8, (cuuint64_t)blocks, rows / 8}, strides[3] = {row, 128, 8 * row};
     const cuuint32_t box[4] = {64, 8, (cuuint32_t)(p.head_dim / 64), (cuuint32_t)run / 8};
-    bool ok = encode(&st->k_map, p.type == QDQ_BF16, 4, p.k_pages, dims, strides, box) &&
-              encode(&st->v_map, p.type == QDQ_BF16, 4, p.v_pages, dims, strides, box);
+    bool ok;
+    if (p.type == QDQ_E4M3) {
+        // [page][head and position][head_dim]: a box is a run of positions of one kv head
+        const cuuint64_t r = (cuuint64_t)p.n_kv_heads * p.page_size, d[3] = {(cuuint64_t)p.head_dim, r, (cuuint64_t)p.n_layers * p.n_pages};
+        const cuuint64_t t[2] = {(cuuint64_t)p.head_dim, r * p.head_dim};
+        const cuuint32_t x[3] = {(cuuint32_t)p.head_dim, (cuuint32_t)run, 1};
+        ok = encode(&st->k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.k_pages, d, t, x, CU_TENSOR_MAP_SWIZZLE_NONE) &&
+             encode(&st->v_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.v_pages, d, t, x, CU_TENSOR_MAP_SWIZZLE_NONE);
+    } else {
+        ok = encode(&st->k_map, data_type(p.type), 4, p.k_pages, dims, strides, box) &&
+             encode(&st->v_map, data_type(p.type), 4, p.v_pages, dims, strides, box);
+    }
     st->ctas = sm_count;
     // two parts per CTA and set: 128 rows of O, a maximum and a sum; the joins' counters
     const size_t parts = (size_t)sm_count * 4, n_o = parts * 128 * p.head_dim * 4, n_s = parts * 128 * 8;
@@ -915,9 +1084,9 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
     ok = ok && cudaMalloc((void **)&st->mem, bytes) == cudaSuccess && cudaMemset(st->mem, 0, bytes) == cudaSuccess;
     for (bool out_f32 : {false, true}) {
         cudaFuncAttributes fa;  // (the kernel's shares of registers add up to its launch's)
-        const Kernel f = kernel_of(p.head_dim, p.type == QDQ_BF16, out_f32);
+        const Kernel f = kernel_of(p.head_dim, p.type, out_f32);
         ok = ok && cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == 168;
-        ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(p.head_dim)) == cudaSuccess;
+        ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(p.head_dim, p.type)) == cudaSuccess;
     }
     if (!ok) {
         cudaGetLastError();
@@ -944,11 +1113,19 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     k.q_start = a.q_start, k.kv_len = a.kv_len, k.page_table = a.page_table;
     k.out = a.out, k.lse = a.lse, k.out_stride = a.out_stride;
     // (masked scores are -inf and are multiplied by the scale: for a scale of 0 by the smallest number
-    // instead, which leaves them -inf and moves the weight of any finite score by less than 2^-20 of it)
-    k.scale_log2 = std::fmax((float)(std::fabs((double)a.scale) * 1.4426950408889634), std::numeric_limits<float>::denorm_min());
+    // instead, which leaves them -inf and moves the weight of any finite score by less than 2^-20 of it;
+    // times a scale of 2^-40 .. 2^40, over e4m3 values, by 2^-100, which leaves 2^-140 at least)
+    const float least = p.type == QDQ_E4M3 ? 0x1p-100f : std::numeric_limits<float>::denorm_min();
+    k.scale_log2 = std::fmax((float)(std::fabs((double)a.scale) * 1.4426950408889634), least);
     k.n_pages = p.n_pages;
     while ((1 << k.page_shift) < p.page_size) ++k.page_shift;
     k.row8_layer = (int)((int64_t)a.layer * p.n_pages * p.page_size / 8);
+    k.page0 = a.layer * p.n_pages;
+    k.out_bf16 = a.out_type == QDQ_BF16;
+    if (p.type == QDQ_E4M3) {
+        const int64_t scales = (int64_t)a.layer * p.n_pages * p.n_kv_heads * (p.page_size / 16);
+        k.k_scales = p.k_scales + scales, k.v_scales = p.v_scales + scales;
+    }
     k.n_heads = p.n_heads;
     k.g.group = p.n_heads / p.n_kv_heads;
     k.g.tokens = kTileM / k.g.group;
@@ -967,8 +1144,8 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     const cuuint64_t q_row = a.n_tokens > 1 ? (cuuint64_t)a.q_stride * 2 : (cuuint64_t)p.n_heads * p.head_dim * 2;
     const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, q_row};
     const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)k.g.tokens};
-    if (!encode(&q_map, p.type == QDQ_BF16, 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
-    return launch_following(kernel_of(p.head_dim, p.type == QDQ_BF16, a.out_type == QDQ_F32), st->ctas, kThreads, smem_of(p.head_dim), 1, stream, k, q_map,
+    if (!encode(&q_map, data_type(p.type), 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
+    return launch_following(kernel_of(p.head_dim, p.type, a.out_type == QDQ_F32), st->ctas, kThreads, smem_of(p.head_dim, p.type), 1, stream, k, q_map,
                             st->k_map, st->v_map);
 }
 

@@ -10,6 +10,9 @@
 #include "qdq_internal.h"
 #include "qdq_paged.cuh"
 
+#ifndef QDQ_FEW_ROWS
+#define QDQ_FEW_ROWS 32
+#endif
 namespace qdq {
 namespace {
 
@@ -220,7 +223,7 @@ struct qdq_paged {
     int page_shift = 0;
     uint64_t *freq = nullptr;  // [rope_dim / 2]
     AttendPools pools{};
-    AttendState *attend = nullptr;  // (of a 16-bit cache)
+    AttendState *attend = nullptr;
     RowsState *rows = nullptr;
     int q_type() const { return cfg.type == QDQ_E4M3 ? QDQ_F16 : cfg.type; }
     bool takes(int type) const {  // as the type of append's rows or of attention's results
@@ -307,7 +310,7 @@ int qdq_paged_create(const qdq_paged_config *cfg, bool scaled, void *k_pages, vo
     }
     c->pools = {k_pages, v_pages, cfg->n_layers, cfg->n_pages, cfg->page_size, cfg->n_heads, cfg->n_kv_heads,
                 cfg->head_dim, cfg->type, k_scales, v_scales};
-    rc = scaled ? QDQ_OK : attend_create(c->pools, c->sm_count, &c->attend);
+    rc = attend_create(c->pools, c->sm_count, &c->attend);
     if (!rc) rc = rows_create(c->pools, c->sm_count, &c->rows);
     if (!rc) rc = pages_setup();
     // The table's copy and the counters' clearing are asynchronous and in the default stream,
@@ -331,8 +334,9 @@ int check_attention(const qdq_paged *c, int layer, const qdq_paged_batch *b, con
     if (rc) return rc;
     const qdq_paged_config &g = c->cfg;
     if (!c->takes(out_type) || out_type == QDQ_E4M3) return QDQ_ERR_TYPE;
-    // (the kernel takes scale * log2(e) as fp32)
-    if (!std::isfinite((float)(scale * 1.4426950408889634)) || window < 0) return QDQ_ERR_SHAPE;
+    // (the kernels take scale * log2(e) as fp32, and times an e4m3 block's scale)
+    const double most = g.type == QDQ_E4M3 ? std::ldexp(1.4426950408889634, kMostExponent) : 1.4426950408889634;
+    if (!std::isfinite((float)(scale * most)) || window < 0) return QDQ_ERR_SHAPE;
     if (!*work) return QDQ_OK;
     const int n = b->n_tokens;
     const int64_t width = (int64_t)g.n_heads * g.head_dim;
@@ -443,7 +447,9 @@ int qdq_paged_attention(qdq_paged *c, int layer, const qdq_paged_batch *b, const
     bool work;
     const int rc = check_attention(c, layer, b, q, q_stride, out_type, out, out_stride, scale, window, lse, &a, &work);
     if (rc || !work) return rc;
-    return c->cfg.type == QDQ_E4M3 ? launch_rows(c->rows, a, (cudaStream_t)stream) : launch_attend(c->attend, a, (cudaStream_t)stream);
+    const int64_t rows = ((int64_t)a.n_tokens + a.n_seqs - 1) / a.n_seqs * (c->cfg.n_heads / c->cfg.n_kv_heads);
+    return c->cfg.type == QDQ_E4M3 && rows <= QDQ_FEW_ROWS ? launch_rows(c->rows, a, (cudaStream_t)stream)
+                                                       : launch_attend(c->attend, a, (cudaStream_t)stream);
 }
 
 int qdq_paged_attention_pages(qdq_paged *c, int layer, const qdq_paged_batch *b, const void *q, int64_t q_stride,

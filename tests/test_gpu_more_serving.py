@@ -5,8 +5,9 @@
   error of a power of two's border (then one exponent either way). A stored value is off by half a
   step: 2^-4 of it, or half e4m3's smallest step, 2^-10 * 2^e; the fp32 arithmetic before that by
   what tests/test_gpu_serving.py derives. Earlier rows of a block are rescaled to the bit.
-* Attention. As there, with the weights in two fp16 terms: each is off by 2^-22 of itself and
-  2^-32 of the row's largest (its value's scale in it), which meets at most 448 * 2^e; t = s * c + e
+* Attention. As there, with the weights in two fp16 terms (one, where blocks of many rows have a
+  16-bit result): each is off by 2^-22 (2^-11) of itself and 2^-32 of the row's largest (its
+  value's scale in it), which meets at most 448 * 2^e; t = s * c + e
   is rounded with |e| in it, which is counted as 4 * 2^-24 * |e| beside the scores' own error.
 * Bounds and selections are whole numbers: equal.
 """
@@ -231,6 +232,10 @@ def check_attention(qdq, b, window=0, scale=None, layer=0, out_dtype="f32", q_sc
         v_max = np.nanmax(np.abs(V), initial=0.0, where=np.isfinite(V))
     # two terms: 16 bits of a weight in bf16, 22 in fp16, whose smallest step counts too
     weight, least = (2.0 ** -17, 0.0) if b["q_dtype"] == "bf16" else (2.0 ** -22, 2.0 ** -32)
+    if lists is None and out_dtype != "f32" and -(-T // len(b["kv_len"])) * (H // b["kv"]) > 32:
+        # blocks of many rows with a 16-bit result: one fp16 term, rounded to nearest, off by 2^-11 of itself
+        # (fp16's smallest step, 2^-24, is 2^-31 of the row's largest weight, which is kept times 2^7: half of it, 2^-32)
+        weight = 2.0 ** -11
     ds = 2 * D * 2.0 ** -24 * reach + 4 * 2.0 ** -24 * e
     tol = half_out * np.abs(ref) + (weight + 2 * ds[..., None] + 2.0 ** -20 + n * 2.0 ** -24) * spread + n * least * v_max + 1e-30
     if out_dtype == "f16":
