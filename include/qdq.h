@@ -423,7 +423,7 @@ int qdq_paged_append(qdq_paged *cache, int layer, const qdq_paged_batch *batch, 
  * attend to has weight zero for the earlier ones, and 0 x inf is no number).
  * Over a cache of e4m3 values the query meets the keys' e4m3 values exactly and their scales
  * in fp32; a weight, with its value's scale in it, meets the values in two fp16 terms, or in
- * one, rounded once, for a 16-bit out where a step has more than 32 rows (tokens x query
+ * one, rounded once, for a 16-bit out where a step has more than 16 rows (tokens x query
  * heads of a kv head) a sequence on average.
  * One launch; results do not depend on timing (no floating-point atomics). */
 int qdq_paged_attention(qdq_paged *cache, int layer, const qdq_paged_batch *batch, const void *q, int64_t q_stride,

@@ -53,12 +53,14 @@
 // their product (their weights are zero, but 0 x NaN is not), scores there are replaced
 // by -inf whatever K held.
 //
-// A cache of e4m3 values (KV8): two of the third warpgroup's warps widen the copied bytes to fp16,
-// which holds them exactly, into the ring that the matrix instructions read (and leave out the rows
-// outside the block's positions there). The scales of 16 positions stay out of the products: 2^ek
-// goes into the scores' factor, and with 2^ev the weight that meets the values is 2^(t + ev - m),
-// m the maximum of t + ev, l the sum of those weights times 2^-ev (as in qdq_attend_rows.cu, which
-// takes the batches of few rows).
+// A cache of e4m3 values (KV8): two of the third warpgroup's warps widen the copied bytes to fp16
+// into the ring that the matrix instructions read (and leave out the rows outside the block's
+// positions there), in units of a power of two for each tile and kind, 2^-7 of the largest scale of
+// its blocks: exactly where a block's scale is 2^-22 of the largest or more, else off by less than
+// 2^-31 of the tile's largest values. The units stay out of the products: the keys'
+// goes into the scores' factor, and with the values' 2^e the weight that meets them is 2^(t + e - m),
+// m the maximum of t + e, l the sum of those weights times 2^-e. (Block by block in the softmax, as in
+// qdq_attend_rows.cu, which takes the batches of few rows, the 8191 tokens took 530 us.)
 #include <cmath>
 #include <cuda.h>
 #include <limits>
@@ -115,6 +117,15 @@ struct KernelArgs {
     unsigned *counters;
 };
 
+// KV8, of a tile: the scores' factor and the values' unit, and of its eight blocks of 16 positions the
+// rows that hold a position of the block and what brings them to the tile's units.
+struct Note {
+    float f, e, h;       // scale * log2(e) * the keys' unit; log2 of the values', and its inverse
+    uint32_t reserved;
+    uint16_t rows[8];
+    uint16_t times[2][8];  // fp16: keys, values
+};
+
 template <int HD, bool KV8>
 struct Shape {
     static constexpr int kHalves = HD / 64;
@@ -126,7 +137,7 @@ struct Shape {
     // KV8: the ring of bytes as they are copied, and each of kNotes tiles' scales and rows. (A tile's notes
     // are written over when the copies are kNotes tiles on: its bytes' slots have then been taken up
     // 2 kNotes - kRawSlots copies on, whose slots of the ring were free once its weights had been used.)
-    static constexpr int kRawSlots = KV8 ? (HD == 128 ? 4 : 8) : 0, kNotes = 8;
+    static constexpr int kRawSlots = KV8 ? (HD == 128 ? 3 : 8) : 0, kNotes = 8;
     static constexpr uint32_t kRawSlot = (uint32_t)kTileN * HD, kRaw = kRing + kSlots * kSlot;
     static_assert(!KV8 || 2 * kNotes >= kRawSlots + kSlots + 2, "kNotes");
     static constexpr uint32_t kBars = kRaw + kRawSlots * kRawSlot;
@@ -139,18 +150,11 @@ struct Shape {
     static constexpr int kColOne = kApart ? kColO + 2 * HD : 0, kPitchOne = kApart ? 64 : 128;
     static constexpr int kColRest = 64;  // of the second term, from the first one's
     static constexpr uint32_t kPieces = kStart + 64;
-    static constexpr uint32_t kNote = kPieces + 192;
-    static constexpr uint32_t kTotal = kNote + (KV8 ? kNotes * 32 : 0);
+    static constexpr uint32_t kNote = (kPieces + 192 + 15) / 16 * 16;
+    static constexpr uint32_t kTotal = kNote + (KV8 ? kNotes * sizeof(Note) : 0);
     static_assert(kTotal <= 232448, "shared memory");
 };
 
-// KV8, of a tile's eight blocks of 16 positions: the scales' exponents, and the rows that hold a
-// position of the block.
-struct Note {
-    int8_t ek[8], ev[8];
-    uint16_t rows[8];
-};
-static_assert(sizeof(Note) == 32, "Shape::kNote");
 // barriers (8 bytes each) at kBars
 constexpr int kBarFull = 0, kBarEmpty = 10, kBarQFull = 20, kBarQEmpty = 21, kBarS = 22, kBarP = 24, kBarPv = 26,
               kBarOFree = 28, kBarDrain = 30, kBarPiece = 31, kBarPieceFree = 33,
@@ -307,12 +311,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // block `lane` of the tile lies in run lane * 16 >> run_shift
                         const int run = ((lane & 7) << 4) >> run_shift, p0 = (t0 + j) * kTileN + ((lane & 7) << 4);
                         const int run_page = __shfl_sync(0xFFFFFFFFu, here, run);
-                        int ek = 0, ev = 0;
+                        constexpr int kNone = -1000;
+                        int ek = kNone, ev = kNone;
                         if (run_page >= 0 && lane < 8) {
                             const int64_t at = (((int64_t)run_page * a.g.kv_heads + w.head) << (a.page_shift - 4)) +
                                                ((p0 & ((1 << a.page_shift) - 1)) >> 4);
                             ek = exponent_of(a.k_scales[at]), ev = exponent_of(a.v_scales[at]);
                         }
+                        const int all_k = __reduce_max_sync(0xFFFFFFFFu, ek), all_v = __reduce_max_sync(0xFFFFFFFFu, ev);
+                        const int unit_k = all_k == kNone ? 0 : all_k - 7, unit_v = all_v == kNone ? 0 : all_v - 7;
+                        // 2^d in fp16, d at most 7
+                        auto half_power = [](int d) { return (uint16_t)(d >= -14 ? (15 + d) << 10 : d >= -24 ? 1 << (24 + d) : 0); };
 #pragma unroll
                         for (int kv = 0; kv < 2; ++kv, ++seq_no) {
                             const int slot = seq_no % L::kRawSlots;
@@ -323,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (kv == 0 && lane < 8) {
                                 Note *note = reinterpret_cast<Note *>(smem + L::kNote) + (seq_no >> 1) % L::kNotes;
                                 const int b = min(max(w.b.lo - p0, 0), 16), e = min(max(w.b.hi - p0, 0), 16);
-                                note->ek[lane] = (int8_t)ek, note->ev[lane] = (int8_t)ev;
+                                if (lane == 0) note->f = a.scale_log2 * power_of_two(unit_k), note->e = (float)unit_v, note->h = power_of_two(-unit_v);
+                                note->times[0][lane] = half_power(ek - unit_k), note->times[1][lane] = half_power(ev - unit_v);
                                 note->rows[lane] = run_page >= 0 && e > b ? (uint16_t)((1u << e) - (1u << b)) : 0;
                             }
                             __syncwarp();
@@ -522,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint4 v[kDeep];
 #pragma unroll
                         for (int y = 0; y < kDeep; ++y) v[y] = lds128(from + (r0 + y * kRows + sub) * HD);
+                        const uint16_t *times = note.times[seq_no & 1];
                         const uint32_t live = note.rows[r0 / 16] | (kDeep * kRows > 16 ? (uint32_t)note.rows[r0 / 16 + 1] << 16 : 0u);
 #pragma unroll
                         for (int y = 0; y < kDeep; ++y) {
@@ -534,6 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             e4m3x4_to_f16(a1, f.z, f.w);
                             e4m3x4_to_f16(b0, g.x, g.y);
                             e4m3x4_to_f16(b1, g.z, g.w);
+                            const __half2 by = __half2half2(__ushort_as_half(times[r0 / 16 + (y * kRows) / 16]));
+                            for (uint32_t *u : {&f.x, &f.y, &f.z, &f.w, &g.x, &g.y, &g.z, &g.w})
+                                *reinterpret_cast<__half2 *>(u) = __hmul2(*reinterpret_cast<__half2 *>(u), by);
                             const uint32_t row = to + (r >> 3) * L::kGroup8 + (r & 7) * 128, c = (2 * chunk) & 7;
                             const uint32_t first = row + (((c + (swap ? 1 : 0)) ^ (r & 7)) << 4), second = row + (((c + (swap ? 0 : 1)) ^ (r & 7)) << 4);
                             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
@@ -631,12 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!idle) {
                     float s[4][32], mx[4];
-                    int8_t ek[KV8 ? 8 : 1], ev[KV8 ? 8 : 1];
+                    float f_tile = c, e_tile = 0.0f, h_tile = 1.0f;
                     if constexpr (KV8) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::kNote + ((base >> 1) + (j - t0)) % L::kNotes * 32);
-                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) ek[y] = (int8_t)(u[y / 4] >> (8 * (y % 4))), ev[y] = (int8_t)(u[2 + y / 4] >> (8 * (y % 4)));
+                        const uint4 x = lds128(sb + L::kNote + ((base >> 1) + (j - t0)) % L::kNotes * (uint32_t)sizeof(Note));
+                        f_tile = __uint_as_float(x.x), e_tile = __uint_as_float(x.y), h_tile = __uint_as_float(x.z);
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tc_ld32(t_s + 32 * k, s[k]);
@@ -646,30 +658,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mask(s[k], k);
                     }
-                    if constexpr (KV8) {
-                        // (block by block, in the units of the weights)
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            float b[2];
+                    for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s[y][0], s[y][1]);
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                b[z] = fmaxf(s[y][16 * z], s[y][16 * z + 1]);
+                    for (int k = 2; k < 32; k += 2)
 #pragma unroll
-                                for (int k = 2; k < 16; k += 2) b[z] = max3(b[z], s[y][16 * z + k], s[y][16 * z + k + 1]);
-                                b[z] = fmaf(b[z], c * power_of_two(ek[2 * y + z]), (float)ev[2 * y + z]);
-                            }
-                            mx[y] = fmaxf(b[0], b[1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) mx[y] = fmaxf(s[y][0], s[y][1]);
-#pragma unroll
-                        for (int k = 2; k < 32; k += 2)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[y][k], s[y][k + 1]);
-                    }
+                        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[y][k], s[y][k + 1]);
                     const float unit = KV8 ? 1.0f : c;  // of the maximum, in weights' exponents
-                    const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float mn = fmaxf(m, KV8 ? fmaf(top, f_tile, e_tile) : top);
                     if (j == j0) {
                         m = mn;
                     } else if (__any_sync(0xFFFFFFFFu, (mn - m) * unit > lag)) {
@@ -696,28 +693,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_st();
                     }
                     const float mc = m == -INFINITY ? 0.0f : fmaf(m, unit, -kLift<BF16>);
-                    const uint64_t mc2 = pack2(-mc, -mc);
+                    const uint64_t mc2 = KV8 ? pack2(e_tile - mc, e_tile - mc) : pack2(-mc, -mc), f2 = KV8 ? pack2(f_tile, f_tile) : c2;
                     uint64_t sum[2] = {};
-                    auto weights = [&](const float *s, uint32_t *to, uint32_t *left, auto rest, int block) {
-                        uint64_t f2 = c2, g2 = mc2;
-                        [[maybe_unused]] uint64_t h2 = 0, part = 0;
+                    auto weights = [&](const float *s, uint32_t *to, uint32_t *left, auto rest) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
-                            if constexpr (KV8) {
-                                if (k % 16 == 0) {
-                                    const float f = c * power_of_two(ek[block + k / 16]), g = (float)ev[block + k / 16] - mc;
-                                    const float h = power_of_two(-ev[block + k / 16]);
-                                    f2 = pack2(f, f), g2 = pack2(g, g), h2 = pack2(h, h), part = 0;
-                                }
-                            }
-                            const uint64_t e = ffma2(pack2(s[k], s[k + 1]), f2, g2);
+                            const uint64_t e = ffma2(pack2(s[k], s[k + 1]), f2, mc2);
                             const float p = ex2(lo_of(e)), q = ex2(hi_of(e));
-                            if constexpr (KV8) {
-                                part = fadd2(part, pack2(p, q));
-                                if (k % 16 == 14) sum[(k / 16) & 1] = ffma2(part, h2, sum[(k / 16) & 1]);
-                            } else {
-                                sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
-                            }
+                            sum[(k / 2) & 1] = fadd2(sum[(k / 2) & 1], pack2(p, q));
                             to[k / 2] = F16::pack(p, q);
                             if constexpr (rest.value) {
                                 const float2 h = F16::unpack(to[k / 2]);
@@ -729,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t u[32], left[32];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            weights(s[2 * h], u, left, rest, 4 * h);
-                            weights(s[2 * h + 1], u + 16, left + 16, rest, 4 * h + 2);
+                            weights(s[2 * h], u, left, rest);
+                            weights(s[2 * h + 1], u + 16, left + 16, rest);
                             if constexpr (rest.value) {
                                 tc_st32(t_s + 32 * h, u);
                                 tc_st32(t_s + L::kColRest + 32 * h, left);
@@ -744,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!alt) store(TwoTiles());
                     else store(TwoAlternate());
                     const uint64_t t = fadd2(sum[0], sum[1]);
-                    l += lo_of(t) + hi_of(t);
+                    l = KV8 ? fmaf(lo_of(t) + hi_of(t), h_tile, l) : l + (lo_of(t) + hi_of(t));
                 }
                 if (!KV8 && dirty) {
                     // zero the rows of V that hold no position of the block (row r of the slot)

@@ -10,9 +10,6 @@
 #include "qdq_internal.h"
 #include "qdq_paged.cuh"
 
-#ifndef QDQ_FEW_ROWS
-#define QDQ_FEW_ROWS 32
-#endif
 namespace qdq {
 namespace {
 
@@ -447,9 +444,12 @@ int qdq_paged_attention(qdq_paged *c, int layer, const qdq_paged_batch *b, const
     bool work;
     const int rc = check_attention(c, layer, b, q, q_stride, out_type, out, out_stride, scale, window, lse, &a, &work);
     if (rc || !work) return rc;
+    // Over e4m3 values, by the rows (tokens x heads of a kv head) that a sequence has on average: up to 16 are
+    // one pass of the kernel of few rows (32 + 8 heads of 128, 16 sequences over 4000 positions: 4 tokens
+    // each 49.5 us there and 67.4 on the tcgen05 tensor cores; 8 tokens, two passes, 87 and 67.8).
     const int64_t rows = ((int64_t)a.n_tokens + a.n_seqs - 1) / a.n_seqs * (c->cfg.n_heads / c->cfg.n_kv_heads);
-    return c->cfg.type == QDQ_E4M3 && rows <= QDQ_FEW_ROWS ? launch_rows(c->rows, a, (cudaStream_t)stream)
-                                                       : launch_attend(c->attend, a, (cudaStream_t)stream);
+    return c->cfg.type == QDQ_E4M3 && rows <= 16 ? launch_rows(c->rows, a, (cudaStream_t)stream)
+                                                 : launch_attend(c->attend, a, (cudaStream_t)stream);
 }
 
 int qdq_paged_attention_pages(qdq_paged *c, int layer, const qdq_paged_batch *b, const void *q, int64_t q_stride,

@@ -232,7 +232,7 @@ def check_attention(qdq, b, window=0, scale=None, layer=0, out_dtype="f32", q_sc
         v_max = np.nanmax(np.abs(V), initial=0.0, where=np.isfinite(V))
     # two terms: 16 bits of a weight in bf16, 22 in fp16, whose smallest step counts too
     weight, least = (2.0 ** -17, 0.0) if b["q_dtype"] == "bf16" else (2.0 ** -22, 2.0 ** -32)
-    if lists is None and out_dtype != "f32" and -(-T // len(b["kv_len"])) * (H // b["kv"]) > 32:
+    if lists is None and out_dtype != "f32" and -(-T // len(b["kv_len"])) * (H // b["kv"]) > 16:
         # blocks of many rows with a 16-bit result: one fp16 term, rounded to nearest, off by 2^-11 of itself
         # (fp16's smallest step, 2^-24, is 2^-31 of the row's largest weight, which is kept times 2^7: half of it, 2^-32)
         weight = 2.0 ** -11
