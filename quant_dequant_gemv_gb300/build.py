@@ -30,11 +30,12 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 # Kernels that move registers between their warps: the shares add up to what the launch has only
 # with this many a thread, and a kernel that asked for more would wait for ever.
 REGISTERS = {"qdq_attend.cu": ("attend_kernel", 168)}
+REGISTERS_E4M3 = {"qdq_attend.cu": ("attend8_kernel", 128)}
 
 
-def check_registers(src: str, ptxas: str) -> None:
-    """Raises if a kernel of REGISTERS[src] was given another number of registers (ptxas -v's report)."""
-    name, want = REGISTERS[src]
+def check_registers(src: str, ptxas: str, registers: dict = REGISTERS) -> None:
+    """Raises if a kernel of registers[src] was given another number of registers (ptxas -v's report)."""
+    name, want = registers[src]
     got = re.findall(r"Compiling entry function '(\w*%s\w*)'.*?Used (\d+) registers" % name, ptxas, re.S)
     bad = sorted({int(n) for _, n in got if int(n) != want})
     if not got or bad:
@@ -76,6 +77,7 @@ def build(verbose: bool = False, force: bool = False) -> Path:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         if src in REGISTERS:
             check_registers(src, r.stdout + r.stderr)
+            check_registers(src, r.stdout + r.stderr, REGISTERS_E4M3)
         if verbose and r.stderr:
             print(r.stderr)
         return obj

@@ -53,7 +53,7 @@
 // their product (their weights are zero, but 0 x NaN is not), scores there are replaced
 // by -inf whatever K held.
 //
-// A cache of e4m3 values (KV8): two of the third warpgroup's warps widen the copied bytes to fp16
+// A cache of e4m3 values (KV8): four further warps widen the copied bytes to fp16
 // into the ring that the matrix instructions read (and leave out the rows outside the block's
 // positions there), in units of a power of two for each tile and kind, 2^-7 of the largest scale of
 // its blocks: exactly where a block's scale is 2^-22 of the largest or more, else off by less than
@@ -89,7 +89,10 @@ namespace {
 
 __device__ int g_attend_status;
 
-constexpr int kWarpMma = 8, kWarpLoad = 9, kThreads = 384;
+constexpr int kWarpMma = 8, kWarpLoad = 9;
+constexpr int kWiden = 4;  // KV8: warps that widen the bytes, behind these
+template <bool KV8>
+constexpr int kThreadsOf = KV8 ? 512 : 384;
 constexpr float kLag = 8.0f;  // log2 of how far the running maximum may lag
 constexpr int kColO = 256;
 // log2 of what weights are kept times. fp16's last step below 2^-14 is 2^-24: with the largest weight
@@ -193,11 +196,73 @@ QDQ_DEV float max3(float a, float b, float c) {
     return d;
 }
 
+// KV8, bytes to fp16: the warp's kTileN / kWiden positions of each tile. A lane takes 16 bytes of a row, which
+// are two 16-byte pieces of the widened row; 8 lanes store to 8 different places of the swizzle at once
+// (of 128 dims, the upper half's lanes store their second piece first).
+template <int HD>
+QDQ_DEV void widen(char *smem, const Piece *pieces, int mine, int *status) {
+    using L = Shape<HD, true>;
+    constexpr int kChunks = HD / 16, kRows = 32 / kChunks;  // lanes of a row, rows at once
+    constexpr int kDeep = 2;                                 // loads in flight
+    const uint32_t sb = smem_u32(smem);
+    auto bar = [&](int i) { return sb + L::kBars + 8u * i; };
+    const int lane = threadIdx.x & 31, chunk = lane % kChunks, sub = lane / kChunks;
+    const bool swap = HD == 128 && chunk >= 4;
+    const uint32_t c = (2 * chunk) & 7, c_first = c + (swap ? 1 : 0), c_second = c + (swap ? 0 : 1);
+    uint32_t seq_no = 0;
+    for (uint32_t items = 0;; ++items) {
+        mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
+        const int n = pieces[items & 1].n;
+        __syncwarp();
+        if (n == 0) break;
+        if (lane == 0) mbar_arrive(bar(kBarPieceFree + (items & 1)));
+        for (int x = 0; x < 2 * n; ++x, ++seq_no) {
+            const int raw = seq_no % L::kRawSlots, slot = seq_no % L::kSlots;
+            mbar_wait(bar(kBarRawFull + raw), (seq_no / L::kRawSlots) & 1, status);
+            mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
+            const Note &note = reinterpret_cast<const Note *>(smem + L::kNote)[(seq_no >> 1) % L::kNotes];
+            const uint16_t *times = note.times[seq_no & 1];
+            const uint32_t from = sb + L::kRaw + raw * L::kRawSlot + chunk * 16;
+            const uint32_t to = sb + L::kRing + slot * L::kSlot + (HD == 128 ? (chunk / 4) * 1024u : 0u);
+#pragma unroll 1
+            for (int r0 = mine * (kTileN / kWiden); r0 < (mine + 1) * (kTileN / kWiden); r0 += kDeep * kRows) {
+                uint4 v[kDeep];
+#pragma unroll
+                for (int y = 0; y < kDeep; ++y) v[y] = lds128(from + (r0 + y * kRows + sub) * HD);
+                const __half2 by = __half2half2(__ushort_as_half(times[r0 / 16]));
+                const uint32_t live = note.rows[r0 / 16] >> (r0 % 16);
+                static_assert(16 % (kDeep * kRows) == 0, "one block at a time");
+#pragma unroll
+                for (int y = 0; y < kDeep; ++y) {
+                    const int r = r0 + y * kRows + sub;
+                    if (!((live >> (y * kRows + sub)) & 1)) v[y] = make_uint4(0, 0, 0, 0);
+                    uint4 f, g;
+                    e4m3x4_to_f16(swap ? v[y].z : v[y].x, f.x, f.y);
+                    e4m3x4_to_f16(swap ? v[y].w : v[y].y, f.z, f.w);
+                    e4m3x4_to_f16(swap ? v[y].x : v[y].z, g.x, g.y);
+                    e4m3x4_to_f16(swap ? v[y].y : v[y].w, g.z, g.w);
+                    auto scaled = [&](uint32_t &u) { *reinterpret_cast<__half2 *>(&u) = __hmul2(*reinterpret_cast<__half2 *>(&u), by); };
+                    scaled(f.x), scaled(f.y), scaled(f.z), scaled(f.w), scaled(g.x), scaled(g.y), scaled(g.z), scaled(g.w);
+                    const uint32_t row = to + (r >> 3) * L::kGroup8 + (r & 7) * 128;
+                    const uint32_t first = row + ((c_first ^ (r & 7)) << 4), second = row + ((c_second ^ (r & 7)) << 4);
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(second), "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(kBarFull + slot));
+                mbar_arrive(bar(kBarRawEmpty + raw));
+            }
+        }
+    }
+}
+
 template <int HD, bool BF16, bool OUT32, bool KV8>
-__global__ void __launch_bounds__(kThreads, 1)
-    attend_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap q_map,
-                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+QDQ_DEV void attend(const KernelArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map, const CUtensorMap &v_map) {
     using L = Shape<HD, KV8>;
+    constexpr int kThreads = kThreadsOf<KV8>;
     using F16 = Float16<typename std::conditional<BF16, __nv_bfloat16, __half>::type>;
     // Whether both terms of the weights are multiplied, with the sets on alternate key tiles and on two
     // tiles of rows.
@@ -213,12 +278,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::kSlots; ++i) {
-            mbar_init(bar(kBarFull + i), KV8 ? 2 : 1);
+            mbar_init(bar(kBarFull + i), KV8 ? kWiden : 1);
             mbar_init(bar(kBarEmpty + i), 1);
         }
         for (int i = 0; i < L::kRawSlots; ++i) {
             mbar_init(bar(kBarRawFull + i), 1);
-            mbar_init(bar(kBarRawEmpty + i), 2);
+            mbar_init(bar(kBarRawEmpty + i), kWiden);
         }
         mbar_init(bar(kBarQFull), 1);
         mbar_init(bar(kBarQEmpty), 1);
@@ -231,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBarPiece + i), 1);
-            mbar_init(bar(kBarPieceFree + i), KV8 ? 11 : 9);
+            mbar_init(bar(kBarPieceFree + i), 9 + (KV8 ? kWiden : 0));
         }
         mbar_init(bar(kBarDrain), 1);
         fence_mbar_init();
@@ -257,9 +322,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Registers: launched with 168 a thread, three warpgroups of them; the softmax groups go
     // up to 216, which holds a row's 128 scores without spilling, and the third, of which two
     // warps work, comes down to 72: 2 x 216 + 72 = 3 x 168 (the build refuses to make a library
-    // with another number, attend_create to run one).
+    // with another number, attend_create to run one). KV8: launched with 128 a thread, four warpgroups,
+    // 2 x 208 + 2 x 48 = 4 x 128.
     if (warp >= kWarpMma) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (!KV8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == kWarpLoad) {
             // ---- copies ---------------------------------------------------------------------
             const uint32_t q_rows = (uint32_t)(tq * a.g.group), run_bytes = (L::kGroup8 << run_shift) >> 3;
@@ -504,67 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             mbar_wait(bar(kBarDrain), 0, status);
         } else if constexpr (KV8) {
-            // ---- bytes to fp16: 64 positions of a tile a warp --------------------------------------
-            // A lane takes 16 bytes of a row, which are two 16-byte pieces of the widened row; 8 lanes store
-            // to 8 different places of the swizzle at once (of 128 dims, the upper half's lanes store
-            // their second piece first).
-            constexpr int kChunks = HD / 16, kRows = 32 / kChunks;  // lanes of a row, rows at once
-            const int mine = warp - kWarpLoad - 1, chunk = lane % kChunks, sub = lane / kChunks;
-            const bool swap = HD == 128 && chunk >= 4;
-            uint32_t seq_no = 0;
-            for (uint32_t items = 0;; ++items) {
-                const Piece &w = pieces[items & 1];
-                mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
-                const int n = w.n;
-                __syncwarp();
-                if (n == 0) break;
-                if (lane == 0) mbar_arrive(bar(kBarPieceFree + (items & 1)));
-                for (int x = 0; x < 2 * n; ++x, ++seq_no) {
-                    const int raw = seq_no % L::kRawSlots, slot = seq_no % L::kSlots;
-                    mbar_wait(bar(kBarRawFull + raw), (seq_no / L::kRawSlots) & 1, status);
-                    mbar_wait(bar(kBarEmpty + slot), ((seq_no / L::kSlots) & 1) ^ 1, status);
-                    const Note &note = reinterpret_cast<const Note *>(smem + L::kNote)[(seq_no >> 1) % L::kNotes];
-                    const uint32_t from = sb + L::kRaw + raw * L::kRawSlot + chunk * 16;
-                    const uint32_t to = sb + L::kRing + slot * L::kSlot + (HD == 128 ? (chunk / 4) * 1024u : 0u);
-                    constexpr int kDeep = 4;  // loads in flight
-#pragma unroll 1
-                    for (int r0 = mine * 64; r0 < mine * 64 + 64; r0 += kDeep * kRows) {
-                        uint4 v[kDeep];
-#pragma unroll
-                        for (int y = 0; y < kDeep; ++y) v[y] = lds128(from + (r0 + y * kRows + sub) * HD);
-                        const uint16_t *times = note.times[seq_no & 1];
-                        const uint32_t live = note.rows[r0 / 16] | (kDeep * kRows > 16 ? (uint32_t)note.rows[r0 / 16 + 1] << 16 : 0u);
-#pragma unroll
-                        for (int y = 0; y < kDeep; ++y) {
-                            const int r = r0 + y * kRows + sub;
-                            if (!((live >> ((y * kRows + sub) % (kDeep * kRows > 16 ? 32 : 16))) & 1)) v[y] = make_uint4(0, 0, 0, 0);
-                            const uint32_t a0 = swap ? v[y].z : v[y].x, a1 = swap ? v[y].w : v[y].y;
-                            const uint32_t b0 = swap ? v[y].x : v[y].z, b1 = swap ? v[y].y : v[y].w;
-                            uint4 f, g;
-                            e4m3x4_to_f16(a0, f.x, f.y);
-                            e4m3x4_to_f16(a1, f.z, f.w);
-                            e4m3x4_to_f16(b0, g.x, g.y);
-                            e4m3x4_to_f16(b1, g.z, g.w);
-                            const __half2 by = __half2half2(__ushort_as_half(times[r0 / 16 + (y * kRows) / 16]));
-                            for (uint32_t *u : {&f.x, &f.y, &f.z, &f.w, &g.x, &g.y, &g.z, &g.w})
-                                *reinterpret_cast<__half2 *>(u) = __hmul2(*reinterpret_cast<__half2 *>(u), by);
-                            const uint32_t row = to + (r >> 3) * L::kGroup8 + (r & 7) * 128, c = (2 * chunk) & 7;
-                            const uint32_t first = row + (((c + (swap ? 1 : 0)) ^ (r & 7)) << 4), second = row + (((c + (swap ? 0 : 1)) ^ (r & 7)) << 4);
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(second), "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
-                        }
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(kBarFull + slot));
-                        mbar_arrive(bar(kBarRawEmpty + raw));
-                    }
-                }
-            }
+            if (warp <= kWarpLoad + kWiden) widen<HD>(smem, pieces, warp - kWarpLoad - 1, status);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (!KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- softmax, output ----------------------------------------------------------------
         const int i = warp >> 2, r = threadIdx.x & 127;  // set; row = tensor-memory lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -1010,6 +1021,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+template <int HD, bool BF16, bool OUT32>
+__global__ void __launch_bounds__(kThreadsOf<false>, 1)
+    attend_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap q_map,
+                  const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    attend<HD, BF16, OUT32, false>(a, q_map, k_map, v_map);
+}
+template <int HD, bool OUT32>
+__global__ void __launch_bounds__(kThreadsOf<true>, 1)
+    attend8_kernel(const KernelArgs a, const __grid_constant__ CUtensorMap q_map,
+                   const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    attend<HD, false, OUT32, true>(a, q_map, k_map, v_map);
+}
+
 bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
             const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
@@ -1021,9 +1045,9 @@ bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *ba
 using Kernel = void (*)(KernelArgs, CUtensorMap, CUtensorMap, CUtensorMap);
 template <int HD, bool OUT32>
 Kernel kernel_of(int type) {
-    return type == QDQ_E4M3   ? attend_kernel<HD, false, OUT32, true>
-           : type == QDQ_BF16 ? attend_kernel<HD, true, OUT32, false>
-                              : attend_kernel<HD, false, OUT32, false>;
+    return type == QDQ_E4M3   ? attend8_kernel<HD, OUT32>
+           : type == QDQ_BF16 ? attend_kernel<HD, true, OUT32>
+                              : attend_kernel<HD, false, OUT32>;
 }
 Kernel kernel_of(int head_dim, int type, bool out_f32) {
     if (head_dim == 64) return out_f32 ? kernel_of<64, true>(type) : kernel_of<64, false>(type);
@@ -1068,7 +1092,7 @@ int attend_create(const AttendPools &p, int sm_count, AttendState **out) {
     for (bool out_f32 : {false, true}) {
         cudaFuncAttributes fa;  // (the kernel's shares of registers add up to its launch's)
         const Kernel f = kernel_of(p.head_dim, p.type, out_f32);
-        ok = ok && cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == 168;
+        ok = ok && cudaFuncGetAttributes(&fa, f) == cudaSuccess && fa.numRegs == (p.type == QDQ_E4M3 ? 128 : 168);
         ok = ok && cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(p.head_dim, p.type)) == cudaSuccess;
     }
     if (!ok) {
@@ -1128,7 +1152,7 @@ int launch_attend(const AttendState *st, const AttendArgs &a, cudaStream_t strea
     const cuuint64_t strides[2] = {(cuuint64_t)p.head_dim * 2, q_row};
     const cuuint32_t box[3] = {64, (cuuint32_t)k.g.group, (cuuint32_t)k.g.tokens};
     if (!encode(&q_map, data_type(p.type), 3, a.q, dims, strides, box)) return QDQ_ERR_CUDA;
-    return launch_following(kernel_of(p.head_dim, p.type, a.out_type == QDQ_F32), st->ctas, kThreads, smem_of(p.head_dim, p.type), 1, stream, k, q_map,
+    return launch_following(kernel_of(p.head_dim, p.type, a.out_type == QDQ_F32), st->ctas, p.type == QDQ_E4M3 ? kThreadsOf<true> : kThreadsOf<false>, smem_of(p.head_dim, p.type), 1, stream, k, q_map,
                             st->k_map, st->v_map);
 }
 

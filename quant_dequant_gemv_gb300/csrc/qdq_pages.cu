@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(128) bounds_kernel(const PagesArgs a) {
 // ---- selection --------------------------------------------------------------------------------
 constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32, kMostGroup = 32, kBins = 2048;
 constexpr int kMostPages = 32768;
+constexpr uint32_t kForced = 0xFFFFFFFFu;  // above the key of any score
 
 QDQ_DEV uint32_t cluster_rank() {
     uint32_t r;
@@ -187,6 +188,12 @@ QDQ_DEV void store_to_rank0(uint32_t addr, uint32_t v) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(addr));
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
+// c (16 x 8) += a (16 x 32 signed bytes) x b (32 x 8).
+QDQ_DEV void mma_s8(int *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 QDQ_DEV uint32_t bytes4(float a, float b, float c, float d) {
     return ((uint32_t)(int)a & 0xFF) | ((uint32_t)(int)b & 0xFF) << 8 | ((uint32_t)(int)c & 0xFF) << 16 | (uint32_t)(int)d << 24;
@@ -214,16 +221,18 @@ QDQ_DEV uint32_t scan(uint32_t v, uint32_t *room, uint32_t &total) {
     return before + incl - v;
 }
 
-// A cluster takes a token and kv head. Its CTAs score a share of the pages each (a page's bounds are
-// read once, by D / 8 lanes, for all the group's heads) and send the scores, as integers in their
-// order, to the first CTA's shared memory, which selects: it narrows the range of the k-th largest
-// by 2048 bins at a time, and then writes what lies above it and the first of its equals, in order.
+// A cluster takes a token and kv head. Its CTAs score a share of the pages each, 16 a warp and step, by
+// the integer matrix instruction (16 pages x 8 heads x 32 dims; a lane's operands are 16 consecutive bytes
+// of a page's bounds, and the query's in the same order: a sum may take its terms in any), and send the
+// scores, as integers in their order, to the first CTA's shared memory. That one selects: it narrows the
+// range of the k-th largest by 2048 bins at a time, and then writes what lies above it and the first of
+// its equals, in order.
 template <int TYPE, int D>
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs a) {
-    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a page, pages of a warp step
+    constexpr int kAtOnce = 16;  // pages of a warp step
     extern __shared__ __align__(16) char smem[];
     uint32_t *keys = reinterpret_cast<uint32_t *>(smem);  // [max_pages], the first CTA's
-    __shared__ __align__(16) uint32_t s_q[2][kMostGroup][D / 4];  // max(q, 0) and min(q, 0)
+    __shared__ __align__(16) uint32_t s_q[2][kMostGroup][D == 128 ? 48 : 16];  // max(q, 0) and min(q, 0)
     __shared__ int s_eq[kMostGroup];
     __shared__ uint32_t s_bins[kBins], s_room[kSelectWarps], s_pick[3];
     __shared__ uint32_t s_range[2][kSelectWarps];
@@ -275,47 +284,67 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
 
     // scores of this CTA's pages
     {
-        const int sub = lane / kLanes, at = lane % kLanes, which = at / (kLanes / 2), chunk = at % (kLanes / 2);
+        constexpr int kLoads = D / 64;  // 16-byte pieces of each bound that a lane reads
+        const int g = lane >> 2, c = lane & 3;
         const int stride = size * kSelectWarps * kAtOnce;
-        constexpr int kDeep = 4;  // steps whose loads are in flight
-        for (int j0 = (rank * kSelectWarps + warp) * kAtOnce; j0 < pages; j0 += kDeep * stride) {
-            int page[kDeep], e[kDeep];
-            uint4 b[kDeep];
+        // the lane's rows g and g + 8 of the step at j0: pages, and of these those of the table
+        auto pages_at = [&](int j0, int *page) {
 #pragma unroll
-            for (int y = 0; y < kDeep; ++y) {
-                const int j = j0 + y * stride + sub;
+            for (int y = 0; y < 2; ++y) {
+                const int j = j0 + 8 * y + g;
                 page[y] = j < pages ? table[j] : -1;
-                if ((unsigned)page[y] >= (unsigned)a.n_pages) page[y] = -1;
             }
+        };
+        int page[2], next[2];
+        int j0 = (rank * kSelectWarps + warp) * kAtOnce;
+        pages_at(j0, next);
+        for (; j0 < pages; j0 += stride) {
+            uint4 b[2][2][kLoads];  // [row][largest, smallest][piece]
+            int e[2];
 #pragma unroll
-            for (int y = 0; y < kDeep; ++y) {
-                b[y] = make_uint4(0, 0, 0, 0);
+            for (int y = 0; y < 2; ++y) {
+                page[y] = (unsigned)next[y] < (unsigned)a.n_pages ? next[y] : -1;
                 e[y] = 0;
-                if (page[y] >= 0) {
-                    const int64_t unit = (int64_t)page[y] * a.n_kv_heads + head;
-                    b[y] = __ldg(reinterpret_cast<const uint4 *>(a.bounds + unit * 2 * D) + at);
-                    e[y] = a.bound_scales[unit] - 127;
+                const int64_t unit = (int64_t)max(page[y], 0) * a.n_kv_heads + head;
+                const int8_t *from = a.bounds + unit * 2 * D + 16 * c;
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) b[y][z][i] = __ldg(reinterpret_cast<const uint4 *>(from + z * D + 64 * i));
+                e[y] = a.bound_scales[unit] - 127;
+            }
+            pages_at(j0 + stride, next);
+            float best[2] = {-INFINITY, -INFINITY};
+            for (int h0 = 0; h0 < group; h0 += 8) {
+                int sum[4] = {};
+                const int h = min(h0 + g, group - 1);  // (column g of the product)
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        const uint4 q = *reinterpret_cast<const uint4 *>(&s_q[z][h][16 * i + 4 * c]);
+                        mma_s8(sum, b[0][z][i].x, b[1][z][i].x, b[0][z][i].y, b[1][z][i].y, q.x, q.y);
+                        mma_s8(sum, b[0][z][i].z, b[1][z][i].z, b[0][z][i].w, b[1][z][i].w, q.z, q.w);
+                    }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {  // heads h0 + 2 c and the next
+                    const int eq = s_eq[min(h0 + 2 * c + x, group - 1)];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float v = (float)sum[2 * y + x] * power_of_two(min(max(eq + e[y], -100), 100));
+                        best[y] = fmaxf(best[y], v);  // (the last head once more, past the group's end)
+                    }
                 }
             }
 #pragma unroll
-            for (int y = 0; y < kDeep; ++y) {
-                const int j = j0 + y * stride + sub;
-                if (j0 + y * stride >= pages) break;
-                float best = -INFINITY;
-                for (int h = 0; h < group; ++h) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(&s_q[which][h][4 * chunk]);
-                    int sum = __dp4a((int)b[y].x, (int)q.x, 0);
-                    sum = __dp4a((int)b[y].y, (int)q.y, sum);
-                    sum = __dp4a((int)b[y].z, (int)q.z, sum);
-                    sum = __dp4a((int)b[y].w, (int)q.w, sum);
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                    best = fmaxf(best, (float)sum * power_of_two(min(max(s_eq[h] + e[y], -100), 100)));
-                }
-                if (at == 0 && j < pages) {
-                    const uint32_t bits = __float_as_uint(best);
+            for (int y = 0; y < 2; ++y) {
+                best[y] = fmaxf(best[y], __shfl_xor_sync(0xFFFFFFFFu, best[y], 1));
+                best[y] = fmaxf(best[y], __shfl_xor_sync(0xFFFFFFFFu, best[y], 2));
+                const int j = j0 + 8 * y + g;
+                if (c == 0 && j < pages) {
+                    const uint32_t bits = __float_as_uint(best[y]);
                     uint32_t key = bits & 0x80000000u ? ~bits : bits | 0x80000000u;  // (finite: neither 0 nor the largest)
-                    if (j < a.first || j > newest - a.last) key = 0xFFFFFFFFu;       // always taken
+                    if (j < a.first || j > newest - a.last) key = kForced;           // always taken
                     if (page[y] < 0) key = 0;                                        // never
                     if (QDQ_CHECK(&g_pages_status, j >= 0 && j < a.max_pages)) store_to_rank0(smem_u32(keys + j), key);
                 }
@@ -326,16 +355,20 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
     if (rank != 0 || !live) return;
 
     // ---- the first CTA selects -------------------------------------------------------------------
-    // a thread has a run of consecutive pages
-    const int tid = threadIdx.x, per = (pages + kSelectThreads - 1) / kSelectThreads;
+    // a thread has a run of consecutive pages (an odd number, which are in other banks than its neighbours')
+    const int tid = threadIdx.x, per = ((pages + kSelectThreads - 1) / kSelectThreads) | 1;
     const int j0 = min(tid * per, pages), j1 = min(j0 + per, pages);
-    uint32_t valid = 0, least_key = 0xFFFFFFFFu, most_key = 0;
+    uint32_t valid = 0, forced = 0, least_key = 0xFFFFFFFFu, most_key = 0;
     for (int j = tid; j < pages; j += kSelectThreads) {
         const uint32_t k = keys[j];
-        if (k) ++valid, least_key = min(least_key, k), most_key = max(most_key, k);
+        if (k == 0) continue;
+        ++valid;
+        if (k == kForced) ++forced;
+        else least_key = min(least_key, k), most_key = max(most_key, k);
     }
     uint32_t all;
-    scan(valid, s_room, all);
+    scan(valid | forced << 16, s_room, all);
+    forced = all >> 16, all &= 0xFFFFu;
     uint32_t threshold = 1, equals = 0xFFFFFFFFu;  // taken: above the threshold, and of its equals the first so many
     if (all > (uint32_t)a.select) {
         least_key = __reduce_min_sync(0xFFFFFFFFu, least_key);
@@ -344,8 +377,10 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kSelectWarps; ++w) least_key = min(least_key, s_range[0][w]), most_key = max(most_key, s_range[1][w]);
-        uint32_t want = a.select, from = least_key, width = most_key - least_key;  // the want-th largest lies in from .. from + width
-        while (true) {
+        // the want-th largest of the scores lies in from .. from + width
+        uint32_t want = a.select - forced, from = least_key, width = most_key - least_key;
+        if (want == 0) threshold = kForced;
+        while (want) {
             const int bits = 32 - __clz(width), shift = max(bits - 11, 0);
             for (int i = tid; i < kBins; i += kSelectThreads) s_bins[i] = 0;
             __syncthreads();
