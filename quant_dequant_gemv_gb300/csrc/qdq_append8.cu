@@ -20,19 +20,27 @@ __device__ int g_append8_status;
 constexpr int kThreads = 256, kMostWindow = 16;
 constexpr int kSpan = kMostWindow + kScaleBlock - 1;  // tokens that a window's blocks reach
 
+// Two values as fp16; beyond its range they become its largest, what is no number stays none.
+QDQ_DEV uint32_t pack_finite(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 // A CTA takes a window of tokens: their q rows, and the keys and values of the blocks that begin
 // (or are first written to) there, which may reach past it. A block of one head, keys or values, is
-// a warp's: D/8 lanes take a row, eight values a lane, as in the 16-bit append (qdq_paged.cu), the
-// whole block in registers, so that the scale is known before anything is stored. The angles of the
+// a pair of warps', eight rows each: D/8 lanes take a row, eight values a lane, as in the 16-bit append
+// (qdq_paged.cu), all in registers, so that the scale is known before anything is stored. The angles of the
 // window's positions are formed once for all heads, in shared memory.
 template <typename TI, int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) {
+__global__ void __launch_bounds__(kThreads, 3) append8_kernel(const Append8Args a) {
     constexpr int G = D / 8, RW = 32 / G;            // lanes per row, rows per warp step
-    constexpr int kSteps = kScaleBlock / RW;         // of a block
+    constexpr int kSteps = 8 / RW;                   // of half a block
     constexpr int kBatch = 4;                        // steps of a q task
     __shared__ float2 turn[kSpan * (D / 2)];         // cosine and sine of each token's pairs
     __shared__ int s_pos[kSpan], s_rows[kSpan], s_lead[kMostWindow], s_count;
     __shared__ bool s_live[kSpan], s_turn[kSpan];
+    __shared__ float s_top[2][kThreads / 32];
     __shared__ int64_t s_block[kMostWindow];         // (page * heads) and the block's number in it, or -1
     follow_last_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane % G, sub = lane / G;
@@ -121,118 +129,126 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) 
 
     const int kv_tasks = s_count * 2 * a.n_kv_heads, per_token = (a.n_heads + kBatch * RW - 1) / (kBatch * RW);
     const int tasks = kv_tasks + in_window * per_token;
-    for (int task = warp * a.parts + part; task < tasks; task += (kThreads / 32) * a.parts) {
-        if (task < kv_tasks) {
-            // ---- a block of keys or values of one head ----------------------------------------------
-            const int at = task / (2 * a.n_kv_heads), which = task - at * 2 * a.n_kv_heads;
-            const bool is_k = which < a.n_kv_heads;
-            const int head = is_k ? which : which - a.n_kv_heads, token = s_lead[at], rows = s_rows[token];
-            const int64_t block = s_block[at];
-            const int page = (int)(block >> 32), in_page = (int)block, row0 = in_page & (kScaleBlock - 1);
-            const int64_t unit = (int64_t)page * a.n_kv_heads + head;  // a page's rows of the head
-            uint8_t *scale = (is_k ? a.k_scales : a.v_scales) + (unit << (a.page_shift - 4)) + (in_page >> 4);
-            uint8_t *code = (is_k ? a.k_pages : a.v_pages) + ((unit << a.page_shift) + in_page) * D;
-            const TI *src = (is_k ? (const TI *)a.k + (int64_t)(t0 + token) * a.k_stride : (const TI *)a.v + (int64_t)(t0 + token) * a.v_stride) + head * D;
-            const int64_t stride = is_k ? a.k_stride : a.v_stride;
-            float x[kSteps][8];
+    const int pair = warp >> 1, half = warp & 1;
+    int turn_no = 0;
+    for (int task = pair * a.parts + part; task < kv_tasks; task += (kThreads / 64) * a.parts) {
+        // ---- a block of keys or values of one head ----------------------------------------------
+        const int at = task / (2 * a.n_kv_heads), which = task - at * 2 * a.n_kv_heads;
+        const bool is_k = which < a.n_kv_heads;
+        const int head = is_k ? which : which - a.n_kv_heads, token = s_lead[at], rows = s_rows[token];
+        if (rows <= 8 && half) continue;  // (the first warp's alone)
+        const int64_t block = s_block[at];
+        const int page = (int)(block >> 32), in_page = (int)block, row0 = in_page & (kScaleBlock - 1);
+        const int64_t unit = (int64_t)page * a.n_kv_heads + head;  // a page's rows of the head
+        uint8_t *scale = (is_k ? a.k_scales : a.v_scales) + (unit << (a.page_shift - 4)) + (in_page >> 4);
+        uint8_t *code = (is_k ? a.k_pages : a.v_pages) + ((unit << a.page_shift) + in_page) * D;
+        const TI *src = (is_k ? (const TI *)a.k + (int64_t)(t0 + token) * a.k_stride : (const TI *)a.v + (int64_t)(t0 + token) * a.v_stride) + head * D;
+        const int64_t stride = is_k ? a.k_stride : a.v_stride;
+        float x[kSteps][8];
 #pragma unroll
-            for (int y = 0; y < kSteps; ++y) {
-                const int i = y * RW + sub;
+        for (int y = 0; y < kSteps; ++y) {
+            const int i = 8 * half + y * RW + sub;
 #pragma unroll
-                for (int z = 0; z < 8; ++z) x[y][z] = 0.0f;
-                if (i < rows && QDQ_CHECK(&g_append8_status, t0 + token + i < a.n_tokens && page < a.n_pages && row0 + i < kScaleBlock)) {
-                    load4(src + i * stride + c0, x[y]);
-                    load4(src + i * stride + c1, x[y] + 4);
-                }
+            for (int z = 0; z < 8; ++z) x[y][z] = 0.0f;
+            if (i < rows && QDQ_CHECK(&g_append8_status, t0 + token + i < a.n_tokens && page < a.n_pages && row0 + i < kScaleBlock)) {
+                load4(src + i * stride + c0, x[y]);
+                load4(src + i * stride + c1, x[y] + 4);
             }
-            const int before = row0 ? exponent_of(*scale) : -kMostExponent;
-            float w[8], top = 0.0f;
-            if (is_k && a.k_norm) weights(a.k_norm, w);
+        }
+        const int before = row0 ? exponent_of(*scale) : -kMostExponent;
+        float w[8], top = 0.0f;
+        if (is_k && a.k_norm) weights(a.k_norm, w);
 #pragma unroll
-            for (int y = 0; y < kSteps; ++y) {
-                if (y * RW >= rows) break;
-                if (is_k) {
-                    if (a.k_norm) norm(x[y], w);
-                    rotate(x[y], token + min(y * RW + sub, rows - 1));
-                }
-                if (y * RW + sub < rows) {
-#pragma unroll
-                    for (int z = 0; z < 8; ++z) {
-                        const float v = fabsf(x[y][z]);
-                        if (v <= 3.402823466e38f) top = fmaxf(top, v);  // (finite ones)
-                    }
-                }
+        for (int y = 0; y < kSteps; ++y) {
+            if (8 * half + y * RW >= rows) break;
+            if (is_k) {
+                if (a.k_norm) norm(x[y], w);
+                rotate(x[y], token + min(8 * half + y * RW + sub, rows - 1));
             }
+            if (8 * half + y * RW + sub < rows) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const int e = max(least_exponent(top), before);
-            const float f = power_of_two(-e);
-#pragma unroll
-            for (int y = 0; y < kSteps; ++y) {
-                const int i = y * RW + sub;
-                if (i >= rows) continue;
-                const float *v = x[y];
-                const uint32_t lo = f32_to_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
-                const uint32_t hi = f32_to_e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f);
-                uint8_t *to = code + i * D;
-                if (INTERLEAVED) {
-                    *reinterpret_cast<uint2 *>(to + c0) = make_uint2(lo, hi);
-                } else {
-                    *reinterpret_cast<uint32_t *>(to + c0) = lo;
-                    *reinterpret_cast<uint32_t *>(to + c1) = hi;
-                }
+                for (int z = 0; z < 8; ++z) top = fmaxf(top, fabsf(x[y][z]));
             }
-            if (row0 && e > before) {  // the block's earlier rows come to the new scale
-                const float g = power_of_two(before - e);
-                for (int i = sub; i < row0; i += RW) {
-                    uint2 *at8 = reinterpret_cast<uint2 *>(code + (i - row0) * D + 8 * u);
-                    const uint2 old = *at8;
-                    auto rescaled = [&](uint32_t v) {
-                        uint32_t lo, hi;
-                        e4m3x4_to_f16(v, lo, hi);
-                        const float2 p = Float16<__half>::unpack(lo), q = Float16<__half>::unpack(hi);
-                        return f32_to_e4m3x4(p.x * g, p.y * g, q.x * g, q.y * g);
-                    };
-                    *at8 = make_uint2(rescaled(old.x), rescaled(old.y));
-                }
+        }
+        if (__any_sync(0xFFFFFFFFu, top == INFINITY)) {  // (seldom: the largest of the finite ones)
+            top = 0.0f;
+#pragma unroll
+            for (int y = 0; y < kSteps; ++y)
+#pragma unroll
+                for (int z = 0; z < 8; ++z) top = fmaxf(top, 8 * half + y * RW + sub < rows && isfinite(x[y][z]) ? fabsf(x[y][z]) : 0.0f);
+        }
+        top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));  // (not negative: its bits are in its order)
+        if (rows > 8) {
+            if (lane == 0) s_top[turn_no][warp] = top;
+            named_bar_sync(1 + pair, 64);
+            top = fmaxf(top, s_top[turn_no][warp ^ 1]);
+            turn_no ^= 1;  // (the other warp may still read this place)
+        }
+        const int e = max(least_exponent(top), before);
+        const float f = power_of_two(-e);
+#pragma unroll
+        for (int y = 0; y < kSteps; ++y) {
+            const int i = 8 * half + y * RW + sub;
+            if (i >= rows) continue;
+            const float *v = x[y];
+            const uint32_t lo = f32_to_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+            const uint32_t hi = f32_to_e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f);
+            uint8_t *to = code + i * D;
+            if (INTERLEAVED) {
+                *reinterpret_cast<uint2 *>(to + c0) = make_uint2(lo, hi);
+            } else {
+                *reinterpret_cast<uint32_t *>(to + c0) = lo;
+                *reinterpret_cast<uint32_t *>(to + c1) = hi;
             }
-            // (every lane has read the old scale: the shuffles above come after it)
-            if (lane == 0) *scale = (uint8_t)(e + 127);
-        } else {
-            // ---- kBatch steps of a token's q rows ---------------------------------------------------
-            const int at = task - kv_tasks, token = at / per_token, r0 = (at - token * per_token) * kBatch * RW;
-            if (!s_live[token]) continue;
-            const TI *src = (const TI *)a.q + (int64_t)(t0 + token) * a.q_stride;
-            __half *to = (__half *)a.q_out + (int64_t)(t0 + token) * a.n_heads * D;
-            float x[kBatch][8], w[8];
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                const int r = min(r0 + y * RW + sub, a.n_heads - 1);
-                load4(src + r * D + c0, x[y]);
-                load4(src + r * D + c1, x[y] + 4);
+        }
+        if (row0 && e > before && half == 0) {  // the block's earlier rows come to the new scale
+            const float g = power_of_two(before - e);
+            for (int i = sub; i < row0; i += RW) {
+                uint2 *at8 = reinterpret_cast<uint2 *>(code + (i - row0) * D + 8 * u);
+                const uint2 old = *at8;
+                auto rescaled = [&](uint32_t v) {
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16(v, lo, hi);
+                    const float2 p = Float16<__half>::unpack(lo), q = Float16<__half>::unpack(hi);
+                    return f32_to_e4m3x4(p.x * g, p.y * g, q.x * g, q.y * g);
+                };
+                *at8 = make_uint2(rescaled(old.x), rescaled(old.y));
             }
-            if (a.q_norm) weights(a.q_norm, w);
-            const bool none = s_pos[token] < 0;
+        }
+        // (both warps have read the old scale)
+        if (lane == 0 && half == 0) *scale = (uint8_t)(e + 127);
+    }
+    for (int task = kv_tasks + warp * a.parts + part; task < tasks; task += (kThreads / 32) * a.parts) {
+        // ---- kBatch steps of a token's q rows ---------------------------------------------------
+        const int at = task - kv_tasks, token = at / per_token, r0 = (at - token * per_token) * kBatch * RW;
+        if (!s_live[token]) continue;
+        const TI *src = (const TI *)a.q + (int64_t)(t0 + token) * a.q_stride;
+        __half *to = (__half *)a.q_out + (int64_t)(t0 + token) * a.n_heads * D;
+        float x[kBatch][8], w[8];
 #pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                const int r = r0 + y * RW + sub;
-                float *v = x[y];
-                if (a.q_norm) norm(v, w);
-                if (!none) rotate(v, token);
+        for (int y = 0; y < kBatch; ++y) {
+            const int r = min(r0 + y * RW + sub, a.n_heads - 1);
+            load4(src + r * D + c0, x[y]);
+            load4(src + r * D + c1, x[y] + 4);
+        }
+        if (a.q_norm) weights(a.q_norm, w);
+        const bool none = s_pos[token] < 0;
 #pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                    // (beyond fp16's range: its largest value; what is no number stays none)
-                    v[z] = none ? 0.0f : v[z] > 65504.0f ? 65504.0f : v[z] < -65504.0f ? -65504.0f : v[z];
-                }
-                if (r >= a.n_heads) continue;
-                const uint2 lo = make_uint2(Float16<__half>::pack(v[0], v[1]), Float16<__half>::pack(v[2], v[3]));
-                const uint2 hi = make_uint2(Float16<__half>::pack(v[4], v[5]), Float16<__half>::pack(v[6], v[7]));
-                if (INTERLEAVED) {
-                    *reinterpret_cast<uint4 *>(to + r * D + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                } else {
-                    *reinterpret_cast<uint2 *>(to + r * D + c0) = lo;
-                    *reinterpret_cast<uint2 *>(to + r * D + c1) = hi;
-                }
+        for (int y = 0; y < kBatch; ++y) {
+            const int r = r0 + y * RW + sub;
+            float *v = x[y];
+            if (a.q_norm) norm(v, w);
+            if (!none) rotate(v, token);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) v[z] = none ? 0.0f : v[z];
+            if (r >= a.n_heads) continue;
+            const uint2 lo = make_uint2(pack_finite(v[0], v[1]), pack_finite(v[2], v[3]));
+            const uint2 hi = make_uint2(pack_finite(v[4], v[5]), pack_finite(v[6], v[7]));
+            if (INTERLEAVED) {
+                *reinterpret_cast<uint4 *>(to + r * D + c0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                *reinterpret_cast<uint2 *>(to + r * D + c0) = lo;
+                *reinterpret_cast<uint2 *>(to + r * D + c1) = hi;
             }
         }
     }
