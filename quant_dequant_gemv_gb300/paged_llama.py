@@ -19,11 +19,13 @@ ROWS = 8  # plans take at most eight columns
 class PagedLlama:
     """embd, output: (type, W); layers: per layer a dict of q k v o gate up down -> (type, W) and
     attn_norm, ffn_norm -> fp32 tensors (as for qdq.Llama); head dims of 64 or 128. The tensors
-    must outlive the model."""
+    must outlive the model. cache: "f16", or "e4m3" for a cache of eight-bit values with scales.
+    select: in steps of single tokens, attend to so many pages of a sequence for each kv head (the
+    first, the last two and those that bounds of their keys rank highest); 0 for all of them."""
 
     def __init__(self, dim, hidden, n_layers, n_heads, n_kv_heads, vocab, embd, layers, output_norm, output,
                  n_pages: int, page_size: int = 16, max_seqs: int = ROWS, max_pages: int = 64, rope_base=10000.0,
-                 norm_eps=1e-5):
+                 norm_eps=1e-5, cache: str = "f16", select: int = 0):
         import torch
         self.dim, self.vocab, self.embd, self.page_size, self.max_pages = dim, vocab, embd, page_size, max_pages
         kv = n_kv_heads * (dim // n_heads)
@@ -31,10 +33,24 @@ class PagedLlama:
         self.h, self.q, self.k, self.v = new(dim), new(dim), new(kv), new(kv)
         self.att, self.gate, self.up, self.logits = new(dim), new(hidden), new(hidden), new(vocab)
         self.q16 = new(dim, torch.float16)
-        pools = torch.zeros(2, n_layers, n_pages, page_size, n_kv_heads, dim // n_heads, dtype=torch.float16,
-                            device="cuda")
+        if cache not in ("f16", "e4m3") or (select and select < 3):
+            raise ValueError('cache: "f16" or "e4m3"; select: 0, or 3 pages at least')
+        head = dim // n_heads
+        if cache == "e4m3":
+            pools = torch.zeros(2, n_layers, n_pages, n_kv_heads, page_size, head, dtype=torch.uint8,
+                                device="cuda").view(torch.float8_e4m3fn)
+            self.scales = torch.zeros(2, n_layers, n_pages, n_kv_heads, page_size // 16, dtype=torch.uint8, device="cuda")
+            self.cache = qdq.PagedCache(pools[0], pools[1], n_heads, rope_base=rope_base, k_scales=self.scales[0],
+                                        v_scales=self.scales[1])
+        else:
+            pools = torch.zeros(2, n_layers, n_pages, page_size, n_kv_heads, head, dtype=torch.float16, device="cuda")
+            self.cache = qdq.PagedCache(pools[0], pools[1], n_heads, rope_base=rope_base)
         self.pools = pools
-        self.cache = qdq.PagedCache(pools[0], pools[1], n_heads, rope_base=rope_base)
+        self.select = select
+        if select:
+            self.bounds = torch.zeros(n_layers, n_pages, n_kv_heads, 2, head, dtype=torch.int8, device="cuda")
+            self.bound_scales = torch.zeros(n_layers, n_pages, n_kv_heads, dtype=torch.uint8, device="cuda")
+            self.chosen = torch.zeros(ROWS, n_kv_heads, select, dtype=torch.int32, device="cuda")
         norm = lambda w: {"x_op": qdq.X_RMSNORM, "norm_w": w, "eps": norm_eps}
         self._before, self._after = [], []
         for w in layers:
@@ -116,7 +132,13 @@ class PagedLlama:
             for l, (before, after) in enumerate(zip(self._before, self._after)):
                 before.run()
                 self.cache.append(l, self.batch, self.q, self.k, self.v, self.q16)
-                self.cache.attention(l, self.batch, self.q16, self.att)
+                if self.select:
+                    self.cache.key_bounds(l, self.batch, self.bounds, self.bound_scales)
+                if self.select and all(len(t) == 1 for t in work.values()):
+                    self.cache.select_pages(l, self.batch, self.q16, self.bounds, self.bound_scales, self.chosen, first=1, last=2)
+                    self.cache.attention_pages(l, self.batch, self.q16, self.chosen, self.att)
+                else:
+                    self.cache.attention(l, self.batch, self.q16, self.att)
                 after.run()
             self._head.run()
             qdq.sample(self.logits, u, self.tokens, logprobs=self.logprobs, **sampling)
