@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(128) bounds_kernel(const PagesArgs a) {
 }
 
 // ---- selection --------------------------------------------------------------------------------
-constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32, kMostGroup = 32, kBins = 2048;
+constexpr int kMostGroup = 32;
 constexpr int kMostPages = 32768;
 constexpr uint32_t kForced = 0xFFFFFFFFu;  // above the key of any score
 
@@ -195,11 +195,9 @@ QDQ_DEV void mma_s8(int *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, 
         : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-QDQ_DEV uint32_t bytes4(float a, float b, float c, float d) {
-    return ((uint32_t)(int)a & 0xFF) | ((uint32_t)(int)b & 0xFF) << 8 | ((uint32_t)(int)c & 0xFF) << 16 | (uint32_t)(int)d << 24;
-}
 
-// Sums `v` over the CTA's threads before this one; total in every thread. `room`: kSelectWarps words.
+// Sums `v` over the CTA's threads before this one; total in every thread. `room`: a word a warp.
+template <int kSelectWarps>
 QDQ_DEV uint32_t scan(uint32_t v, uint32_t *room, uint32_t &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t incl = v;
@@ -225,58 +223,100 @@ QDQ_DEV uint32_t scan(uint32_t v, uint32_t *room, uint32_t &total) {
 // the integer matrix instruction (16 pages x 8 heads x 32 dims; a lane's operands are 16 consecutive bytes
 // of a page's bounds, and the query's in the same order: a sum may take its terms in any), and send the
 // scores, as integers in their order, to the first CTA's shared memory. That one selects: it narrows the
-// range of the k-th largest by 2048 bins at a time, and then writes what lies above it and the first of
-// its equals, in order.
-template <int TYPE, int D>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs a) {
+// range of the k-th largest by a bin a thread at a time, and then writes what lies above it and the first of
+// its equals, in order. (The instruction takes 64 clocks, 512 for 16 pages of 128 dims; in fp16, which holds
+// the bytes and their sums exactly too, it would be 128, but the widening takes more registers than the
+// CTAs that share an SM have: 64 tokens 26 us and not 16.)
+// Few items: 512 threads, and the next step's bounds on their way while one is scored. Many: 256 threads
+// with no more registers than let three CTAs share an SM.
+template <int TYPE, int D, bool FEW>
+__global__ void __launch_bounds__(FEW ? 512 : 256, FEW ? 1 : 3) select_kernel(const PagesArgs a) {
+    constexpr int kSelectThreads = FEW ? 512 : 256, kSelectWarps = kSelectThreads / 32;
     constexpr int kAtOnce = 16;  // pages of a warp step
     extern __shared__ __align__(16) char smem[];
     uint32_t *keys = reinterpret_cast<uint32_t *>(smem);  // [max_pages], the first CTA's
     __shared__ __align__(16) uint32_t s_q[2][kMostGroup][D == 128 ? 48 : 16];  // max(q, 0) and min(q, 0)
     __shared__ int s_eq[kMostGroup];
-    __shared__ uint32_t s_bins[kBins], s_room[kSelectWarps], s_pick[3];
-    __shared__ uint32_t s_range[2][kSelectWarps];
+    __shared__ uint32_t s_bins[kSelectThreads], s_room[kSelectWarps], s_pick[3];
+    __shared__ uint32_t s_range[3][kSelectWarps];
     follow_last_kernel();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cluster_rank(), size = cluster_size(), item = blockIdx.x / size;
     const int t = item / a.n_kv_heads, head = item - t * a.n_kv_heads, group = a.n_heads / a.n_kv_heads;
 
+    // (loads that do not wait for each other come first)
+    constexpr int kEach = D / 32;  // dims of a lane
+    float v[kEach];
+    auto query = [&](int h) {
+        const uint16_t *q = (const uint16_t *)a.q + (int64_t)t * a.q_stride + (int64_t)(head * group + h) * D + lane * kEach;
+#pragma unroll
+        for (int i = 0; i < kEach; i += 2) {
+            const float2 x = Pair<TYPE>::unpack(__ldg(reinterpret_cast<const uint32_t *>(q + i)));
+            v[i] = x.x, v[i + 1] = x.y;
+        }
+    };
+    query(min(warp, group - 1));
     const int s = find_seq(a.q_start, a.n_seqs, t);
-    int first = 0, count = 0;
-    if (s >= 0) seq_tokens(a.q_start, s, a.n_tokens, first, count);
+    int first, count;
+    seq_tokens(a.q_start, max(s, 0), a.n_tokens, first, count);
+    const int kv = max(a.kv_len[max(s, 0)], 0);
     const bool live = s >= 0 && t >= first && t < first + count;
-    const int p = live ? max(a.kv_len[s], 0) - count + (t - first) : -1;
+    const int p = live ? kv - count + (t - first) : -1;
     const int newest = p >= 0 ? p >> a.page_shift : -1, pages = min(newest + 1, a.max_pages);
     const int32_t *table = a.page_table + (int64_t)max(s, 0) * a.max_pages;
 
+    // The first step's bounds are on their way before the queries are looked at.
+    constexpr int kLoads = D / 64;  // 16-byte pieces of each bound that a lane reads
+    const int g = lane >> 2, c = lane & 3;
+    const int stride = size * kSelectWarps * kAtOnce;
+    struct Bounds {  // of the lane's rows g and g + 8 of a step
+        uint4 b[2][2][kLoads];  // [row][largest, smallest][piece]
+        int page[2], e[2];
+    } ahead;
+    int next[2], j0 = (rank * kSelectWarps + warp) * kAtOnce;
+    auto pages_at = [&](int j0) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) next[y] = j0 + 8 * y + g < pages ? table[j0 + 8 * y + g] : -1;
+    };
+    // the step at j0 (its pages are in `next`)
+    auto fetch = [&](int j0, Bounds &to) {
+        if (j0 >= pages) return;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            to.page[y] = (unsigned)next[y] < (unsigned)a.n_pages ? next[y] : -1;
+            const int64_t unit = (int64_t)max(to.page[y], 0) * a.n_kv_heads + head;
+            const int8_t *from = a.bounds + unit * 2 * D + 16 * c;
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) to.b[y][z][i] = __ldg(reinterpret_cast<const uint4 *>(from + z * D + 64 * i));
+            to.e[y] = a.bound_scales[unit] - 127;
+        }
+        pages_at(j0 + stride);
+    };
+    pages_at(j0);
+    fetch(j0, ahead);
+
     // the group's query heads as bytes
     for (int h = warp; h < group; h += kSelectWarps) {
-        constexpr int kEach = D / 32;
-        float v[4] = {};
-        if (live) {
-            const uint16_t *q = (const uint16_t *)a.q + (int64_t)t * a.q_stride + (int64_t)(head * group + h) * D + lane * kEach;
-#pragma unroll
-            for (int i = 0; i < kEach; i += 2) {
-                const float2 x = Pair<TYPE>::unpack(*reinterpret_cast<const uint32_t *>(q + i));
-                v[i] = x.x, v[i + 1] = x.y;
-            }
-        }
+        if (h != warp) query(h);
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) top = fmaxf(top, fabsf(v[i]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));  // (not negative: its bits are in its order)
         const int e = bound_exponent(top);
         const float f0 = power_of_two(-e / 2), f1 = power_of_two(-e - -e / 2);
+        uint32_t over = 0, under = 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) v[i] = fminf(fmaxf(rintf(v[i] * f0 * f1), -127.0f), 127.0f);
-        uint32_t over = bytes4(fmaxf(v[0], 0.0f), fmaxf(v[1], 0.0f), fmaxf(v[2], 0.0f), fmaxf(v[3], 0.0f));
-        uint32_t under = bytes4(fminf(v[0], 0.0f), fminf(v[1], 0.0f), fminf(v[2], 0.0f), fminf(v[3], 0.0f));
+        for (int i = 0; i < kEach; ++i) {
+            const int x = (int)fminf(fmaxf(rintf(v[i] * f0 * f1), -127.0f), 127.0f);
+            over |= (uint32_t)(max(x, 0) & 0xFF) << (8 * i);
+            under |= (uint32_t)(min(x, 0) & 0xFF) << (8 * i);
+        }
         if (kEach == 4) {
             s_q[0][h][lane] = over, s_q[1][h][lane] = under;
         } else {  // two dims a lane
-            over |= __shfl_down_sync(0xFFFFFFFFu, over, 1) << 16, under = (under & 0xFFFFu) | __shfl_down_sync(0xFFFFFFFFu, under, 1) << 16;
-            if (lane % 2 == 0) s_q[0][h][lane / 2] = over, s_q[1][h][lane / 2] = under;
+            reinterpret_cast<uint16_t *>(s_q[0][h])[lane] = (uint16_t)over, reinterpret_cast<uint16_t *>(s_q[1][h])[lane] = (uint16_t)under;
         }
         if (lane == 0) s_eq[h] = e;
     }
@@ -284,36 +324,12 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
 
     // scores of this CTA's pages
     {
-        constexpr int kLoads = D / 64;  // 16-byte pieces of each bound that a lane reads
-        const int g = lane >> 2, c = lane & 3;
-        const int stride = size * kSelectWarps * kAtOnce;
-        // the lane's rows g and g + 8 of the step at j0: pages, and of these those of the table
-        auto pages_at = [&](int j0, int *page) {
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int j = j0 + 8 * y + g;
-                page[y] = j < pages ? table[j] : -1;
-            }
-        };
-        int page[2], next[2];
-        int j0 = (rank * kSelectWarps + warp) * kAtOnce;
-        pages_at(j0, next);
         for (; j0 < pages; j0 += stride) {
-            uint4 b[2][2][kLoads];  // [row][largest, smallest][piece]
-            int e[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                page[y] = (unsigned)next[y] < (unsigned)a.n_pages ? next[y] : -1;
-                e[y] = 0;
-                const int64_t unit = (int64_t)max(page[y], 0) * a.n_kv_heads + head;
-                const int8_t *from = a.bounds + unit * 2 * D + 16 * c;
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-#pragma unroll
-                    for (int i = 0; i < kLoads; ++i) b[y][z][i] = __ldg(reinterpret_cast<const uint4 *>(from + z * D + 64 * i));
-                e[y] = a.bound_scales[unit] - 127;
-            }
-            pages_at(j0 + stride, next);
+            Bounds now = ahead;
+            if (FEW) fetch(j0 + stride, ahead);
+            const auto &b = now.b;
+            const auto &page = now.page;
+            const auto &e = now.e;
             float best[2] = {-INFINITY, -INFINITY};
             for (int h0 = 0; h0 < group; h0 += 8) {
                 int sum[4] = {};
@@ -349,6 +365,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
                     if (QDQ_CHECK(&g_pages_status, j >= 0 && j < a.max_pages)) store_to_rank0(smem_u32(keys + j), key);
                 }
             }
+            if (!FEW) fetch(j0 + stride, ahead);
         }
     }
     cluster_sync();
@@ -357,55 +374,68 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
     // ---- the first CTA selects -------------------------------------------------------------------
     // a thread has a run of consecutive pages (an odd number, which are in other banks than its neighbours')
     const int tid = threadIdx.x, per = ((pages + kSelectThreads - 1) / kSelectThreads) | 1;
-    const int j0 = min(tid * per, pages), j1 = min(j0 + per, pages);
-    uint32_t valid = 0, forced = 0, least_key = 0xFFFFFFFFu, most_key = 0;
+    const int i0 = min(tid * per, pages), i1 = min(i0 + per, pages);
+    uint32_t valid = 0, forced = 0, own = 0, small = 0xFFFFFFFFu;  // this thread's largest and smallest score
     for (int j = tid; j < pages; j += kSelectThreads) {
         const uint32_t k = keys[j];
         if (k == 0) continue;
         ++valid;
         if (k == kForced) ++forced;
-        else least_key = min(least_key, k), most_key = max(most_key, k);
+        else own = max(own, k), small = min(small, k);
     }
     uint32_t all;
-    scan(valid | forced << 16, s_room, all);
+    scan<kSelectWarps>(valid | forced << 16, s_room, all);
     forced = all >> 16, all &= 0xFFFFu;
     uint32_t threshold = 1, equals = 0xFFFFFFFFu;  // taken: above the threshold, and of its equals the first so many
     if (all > (uint32_t)a.select) {
-        least_key = __reduce_min_sync(0xFFFFFFFFu, least_key);
-        most_key = __reduce_max_sync(0xFFFFFFFFu, most_key);
-        if (lane == 0) s_range[0][warp] = least_key, s_range[1][warp] = most_key;
-        __syncthreads();
+        // (of the threads' largest scores the smallest, and of all scores)
+        const uint32_t low = __reduce_min_sync(0xFFFFFFFFu, own ? own : 0xFFFFFFFFu), top = __reduce_max_sync(0xFFFFFFFFu, own);
+        small = __reduce_min_sync(0xFFFFFFFFu, small);
+        if (lane == 0) s_range[0][warp] = low, s_range[1][warp] = top, s_range[2][warp] = small;
+        const uint32_t some = __syncthreads_count(own != 0);
+        uint32_t low_own = 0xFFFFFFFFu, most_key = 0, from = 0xFFFFFFFFu;
 #pragma unroll
-        for (int w = 0; w < kSelectWarps; ++w) least_key = min(least_key, s_range[0][w]), most_key = max(most_key, s_range[1][w]);
-        // the want-th largest of the scores lies in from .. from + width
-        uint32_t want = a.select - forced, from = least_key, width = most_key - least_key;
+        for (int w = 0; w < kSelectWarps; ++w)
+            low_own = min(low_own, s_range[0][w]), most_key = max(most_key, s_range[1][w]), from = min(from, s_range[2][w]);
+        // The want-th largest of the scores lies in from .. from + width. It is no less than the want-th largest
+        // of the threads' largest, where there are so many, and with many scores that is looked for first, so
+        // that few are left to be counted (8188 scores: 5100 clocks and not 7200).
+        uint32_t want = a.select - forced;
         if (want == 0) threshold = kForced;
+        bool firsts = some >= want && pages > 4 * kSelectThreads;
+        if (firsts) from = low_own;
+        uint32_t width = most_key - from;
         while (want) {
-            const int bits = 32 - __clz(width), shift = max(bits - 11, 0);
-            for (int i = tid; i < kBins; i += kSelectThreads) s_bins[i] = 0;
+            constexpr int kBits = FEW ? 9 : 8;  // of kSelectThreads
+            const int bits = 32 - __clz(width), shift = max(bits - kBits, 0);
+            s_bins[tid] = 0;
             __syncthreads();
-            for (int j = tid; j < pages; j += kSelectThreads) {
-                const uint32_t k = keys[j];
-                if (k >= from && k - from <= width) atomicAdd(&s_bins[(k - from) >> shift], 1u);
+            if (firsts) {
+                if (own) atomicAdd(&s_bins[(own - from) >> shift], 1u);
+            } else {
+                for (int j = tid; j < pages; j += kSelectThreads) {
+                    const uint32_t k = keys[j];
+                    if (k >= from && k - from <= width) atomicAdd(&s_bins[(k - from) >> shift], 1u);
+                }
             }
             __syncthreads();
-            // from the top: thread i has bins kBins - 8 i - 8 .. kBins - 8 i - 1
-            constexpr int kEach = kBins / kSelectThreads;
-            uint32_t mine = 0, total;
-            for (int i = 0; i < kEach; ++i) mine += s_bins[kBins - 1 - kEach * tid - i];
-            uint32_t above = scan(mine, s_room, total);
-            if (above < want && want <= above + mine) {
-                int bin = kBins - 1 - kEach * tid;
-                while (above + s_bins[bin] < want) above += s_bins[bin--];
-                s_pick[0] = bin, s_pick[1] = want - above, s_pick[2] = s_bins[bin];
-            }
+            // from the top: thread i has bin kSelectThreads - 1 - i
+            uint32_t total;
+            const uint32_t mine = s_bins[kSelectThreads - 1 - tid], above = scan<kSelectWarps>(mine, s_room, total);
+            if (above < want && want <= above + mine) s_pick[0] = kSelectThreads - 1 - tid, s_pick[1] = want - above, s_pick[2] = mine;
             __syncthreads();
-            const uint32_t bin = s_pick[0], here = s_pick[2];
-            want = s_pick[1];
+            const uint32_t bin = s_pick[0], here = s_pick[2], next_want = s_pick[1];
+            __syncthreads();
+            if (firsts) {  // (all of what lies above the bin's lower end)
+                firsts = false;
+                from += bin << shift;
+                width = most_key - from;
+                continue;
+            }
+            want = next_want;
             from += bin << shift;
             // (the last bin may reach past the range)
             width = min((1u << shift) - 1, width - (bin << shift));
-            __syncthreads();
             if (shift == 0 || here == want) {  // one value, or the whole bin
                 threshold = from;
                 if (shift == 0) equals = want;
@@ -415,18 +445,18 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
     }
     const bool exact = equals != 0xFFFFFFFFu;
     uint32_t over = 0, same = 0;
-    for (int j = j0; j < j1; ++j) {
+    for (int j = i0; j < i1; ++j) {
         const uint32_t k = keys[j];
         if (exact ? k > threshold : k >= threshold) ++over;
         else if (exact && k == threshold) ++same;
     }
     uint32_t total;
-    uint32_t rank_same = scan(same, s_room, total);
+    uint32_t rank_same = scan<kSelectWarps>(same, s_room, total);
     // entries before this thread's: those over, and of the equals the first `equals`
     const uint32_t taken_same = exact ? (rank_same >= equals ? 0 : min(same, equals - rank_same)) : 0;
-    uint32_t to = scan(over + taken_same, s_room, total);
+    uint32_t to = scan<kSelectWarps>(over + taken_same, s_room, total);
     int32_t *out = a.lists + ((int64_t)t * a.n_kv_heads + head) * a.select;
-    for (int j = j0; j < j1; ++j) {
+    for (int j = i0; j < i1; ++j) {
         const uint32_t k = keys[j];
         const bool is_same = exact && k == threshold;
         const bool take = is_same ? rank_same < equals : k >= threshold && k != 0;
@@ -438,7 +468,14 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const PagesArgs 
 
 using Kernel = void (*)(PagesArgs);
 #define QDQ_BY_TYPE(NAME, D) (type == QDQ_E4M3 ? NAME<QDQ_E4M3, D> : type == QDQ_BF16 ? NAME<QDQ_BF16, D> : NAME<QDQ_F16, D>)
-Kernel select_of(int type, int head_dim) { return head_dim == 64 ? QDQ_BY_TYPE(select_kernel, 64) : QDQ_BY_TYPE(select_kernel, 128); }
+template <int D, bool FEW>
+Kernel select_of(int type) {
+    return type == QDQ_E4M3 ? select_kernel<QDQ_E4M3, D, FEW> : type == QDQ_BF16 ? select_kernel<QDQ_BF16, D, FEW> : select_kernel<QDQ_F16, D, FEW>;
+}
+Kernel select_of(int type, int head_dim, bool few) {
+    if (head_dim == 64) return few ? select_of<64, true>(type) : select_of<64, false>(type);
+    return few ? select_of<128, true>(type) : select_of<128, false>(type);
+}
 
 }  // namespace
 
@@ -452,13 +489,14 @@ int launch_bounds(PagesArgs a, int type, int head_dim, cudaStream_t stream, int 
 }
 
 int launch_select(const PagesArgs &a, int type, int head_dim, cudaStream_t stream, int sm_count) {
-    // CTAs of a cluster: as many as the SMs have room for beside the other items, up to 8, with 64 pages
+    // CTAs of a cluster: as many as the SMs have room for beside the other items, up to 8, with 256 pages
     // each at least.
     const int64_t items = (int64_t)a.n_tokens * a.n_kv_heads;
     unsigned size = 1;
-    while (size < 8 && items * size * 2 <= (int64_t)sm_count * 2 && a.max_pages >= 128 * (int)size) size *= 2;
+    while (size < 8 && items * size * 2 <= sm_count && a.max_pages >= 256 * (int)size) size *= 2;
     if (items * size > 0x7FFFFFFF) return QDQ_ERR_LIMIT;
-    return launch_following(select_of(type, head_dim), (unsigned)(items * size), kSelectThreads, (size_t)a.max_pages * 4, size,
+    const bool few = items * size <= sm_count;
+    return launch_following(select_of(type, head_dim, few), (unsigned)(items * size), few ? 512 : 256, (size_t)a.max_pages * 4, size,
                             stream, a);
 }
 
@@ -466,10 +504,11 @@ int launch_select(const PagesArgs &a, int type, int head_dim, cudaStream_t strea
 int pages_setup() {
     for (int type : {QDQ_F16, QDQ_BF16, QDQ_E4M3})
         for (int dim : {64, 128})
-            if (cudaFuncSetAttribute(select_of(type, dim), cudaFuncAttributeMaxDynamicSharedMemorySize, kMostPages * 4) != cudaSuccess) {
-                cudaGetLastError();
-                return QDQ_ERR_CUDA;
-            }
+            for (bool few : {false, true})
+                if (cudaFuncSetAttribute(select_of(type, dim, few), cudaFuncAttributeMaxDynamicSharedMemorySize, kMostPages * 4) != cudaSuccess) {
+                    cudaGetLastError();
+                    return QDQ_ERR_CUDA;
+                }
     return QDQ_OK;
 }
 
