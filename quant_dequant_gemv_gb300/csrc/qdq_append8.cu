@@ -17,7 +17,8 @@ namespace {
 __device__ int g_append8_status;
 #endif
 
-constexpr int kThreads = 256, kMostWindow = 16;
+constexpr int kThreads = 256, kMostWindow = 17;
+static_assert(kMostWindow + kScaleBlock - 1 <= 32, "a lane a token");
 constexpr int kSpan = kMostWindow + kScaleBlock - 1;  // tokens that a window's blocks reach
 
 // Two values as fp16; beyond its range they become its largest, what is no number stays none.
@@ -263,13 +264,23 @@ int launch_typed(const Append8Args &a, bool interleaved, unsigned grid, cudaStre
 }  // namespace
 
 int launch_append8(Append8Args a, int in_type, bool interleaved, int head_dim, cudaStream_t stream, int sm_count) {
-    a.window = a.n_tokens >= 2048 ? kMostWindow : 1;
+    // Many tokens: the window that ends soonest, at three CTAs an SM in turn and three tokens' time for each CTA's
+    // start (7436 tokens: 17 of them, one wave; at 16 a second one of nine CTAs, 64.7 and not 51.8 us).
+    const int warps = kThreads / 32, slots = 3 * sm_count;
+    a.window = 1;
+    if (a.n_tokens >= 2048) {
+        int64_t least = INT64_MAX;
+        for (int w = 8; w <= kMostWindow; ++w) {
+            const int64_t time = (((int64_t)a.n_tokens + w - 1) / w + slots - 1) / slots * (w + 3);
+            if (time <= least) least = time, a.window = w;
+        }
+    }
     const int64_t windows = ((int64_t)a.n_tokens + a.window - 1) / a.window;
-    const int rw = 256 / head_dim, warps = kThreads / 32;
+    const int rw = 256 / head_dim;
     // with few tokens their rows are shared by CTAs, until about 16 warps per SM have work
     const int tasks = a.window == 1 ? 2 * a.n_kv_heads + (a.n_heads + 4 * rw - 1) / (4 * rw) : 16 * warps;
     const int64_t want = std::max<int64_t>(1, ((int64_t)sm_count * 2 + windows - 1) / windows);
-    a.parts = (int)std::min<int64_t>(want, (tasks + warps - 1) / warps);
+    a.parts = a.window > 1 ? 1 : (int)std::min<int64_t>(want, (tasks + warps - 1) / warps);
     const int64_t grid = windows * a.parts;
     if (grid > 0x7FFFFFFF) return QDQ_ERR_LIMIT;
     const unsigned g = (unsigned)grid;
