@@ -219,15 +219,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int run = position & ~((1 << run_shift) - 1);
             if (run < f.hi && run + (1 << run_shift) > f.lo && QDQ_CHECK(status, at >= 0 && at < a.max_pages)) page = w.pages[at];
         };
-        auto scale = [&](const Walk &w, int position, int &page, int &e) {
+        // (the bytes as they are: what is computed of them would wait for them, and with it the copies)
+        uint8_t k_scale = 127, v_scale = 127;
+        auto scale = [&](const Walk &w, int position, int &page) {
             if ((unsigned)page >= (unsigned)a.n_pages) page = -1;
             if (KIND != kE4m3 || page < 0) return;
             const int64_t at = (((int64_t)page * a.g.kv_heads + w.head) << blocks_shift) + ((position & ((1 << a.page_shift) - 1)) >> 4);
-            e = exponent_of(a.k_scales[at]) << 16 | (exponent_of(a.v_scales[at]) & 0xFFFF);
+            k_scale = a.k_scales[at], v_scale = a.v_scales[at];
         };
         Walk w(a, s0), ahead = w;
         Source f = source(w), f_ahead = f;
-        int position = -1, page = -1, e = 0, next_position = -1, next_page = -1, first_position = -1, first_page = -1;
+        int position = -1, page = -1, next_position = -1, next_page = -1, first_position = -1, first_page = -1;
         if (w.more()) {
             entry(w, f, 0, position, page);
             entry(w, f, 4, next_position, next_page);
@@ -257,12 +259,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < w.b.i1 - w.b.i0 && QDQ_CHECK(status, f.token0 + lane < a.n_tokens && (lane + 1) * q_bytes <= L::kQSize))
                 bulk_g2s(sb + L::kQ + at * L::kQSize + lane * q_bytes,
                          a.q + (int64_t)(f.token0 + lane) * a.q_stride + (int64_t)w.head * a.g.group * HD, q_bytes, piece_full(at));
-            scale(w, position, page, e);
+            scale(w, position, page);
             for (int j = 0; j < w.n; ++j, ++stage_no) {
                 const int y = j & 3;
                 if (y == 0 && j) {
                     position = next_position, page = next_page;
-                    scale(w, position, page, e);
+                    scale(w, position, page);
                     entry(w, f, j + 4, next_position, next_page);
                 }
                 // lane r issues the copies of the tile's run r
@@ -290,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane >> 3 == y) {
                     Meta *m = reinterpret_cast<Meta *>(smem + L::kMeta + stage * 64);
                     m->base[lane & 7] = page < 0 ? -1 : position;
-                    m->ek[lane & 7] = (int8_t)(e >> 16);
-                    m->ev[lane & 7] = (int8_t)e;
+                    m->ek[lane & 7] = (int8_t)exponent_of(k_scale);
+                    m->ev[lane & 7] = (int8_t)exponent_of(v_scale);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(full(stage), bytes);
