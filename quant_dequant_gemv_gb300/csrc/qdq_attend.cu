@@ -152,10 +152,10 @@ struct Shape {
     static constexpr bool kApart = HD == 64;
     static constexpr int kColOne = kApart ? kColO + 2 * HD : 0, kPitchOne = kApart ? 64 : 128;
     static constexpr int kColRest = 64;  // of the second term, from the first one's
-    static constexpr uint32_t kPieces = kStart + 64;
+    static constexpr uint32_t kPieces = kStart + 80;
     static constexpr uint32_t kNote = (kPieces + 192 + 15) / 16 * 16;
     static constexpr uint32_t kTotal = kNote + (KV8 ? kNotes * sizeof(Note) : 0);
-    static_assert(kTotal <= 232448, "shared memory");
+    static_assert(kTotal <= 232448 && sizeof(Start) + 8 <= 80 && kSlots * kSlot >= 20 * kMaxSeqs, "shared memory, Start, find_start's room");
 };
 
 // barriers (8 bytes each) at kBars

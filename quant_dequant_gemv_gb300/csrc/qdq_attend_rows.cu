@@ -32,6 +32,7 @@
 #include <cmath>
 #include <cuda.h>
 #include <new>
+#include <type_traits>
 
 #include "qdq_attend_walk.cuh"
 #include "qdq_internal.h"
@@ -101,10 +102,10 @@ struct Shape {
     static constexpr uint32_t kMeta = kQ + kPieces * kQSize;              // [stage] Meta
     static constexpr uint32_t kBars = kMeta + kStages * 64;
     static constexpr uint32_t kStart = kBars + (2 * kStages + 2 * kPieces + 4) * 8;
-    static constexpr uint32_t kPiece = kStart + 64;
+    static constexpr uint32_t kPiece = kStart + 80;
     static constexpr uint32_t kTotal = kPiece + kPieces * sizeof(RowsPiece);
     static_assert(kQ % 16 == 0 && kMeta % 16 == 0 && kBars % 8 == 0 && kStart % 8 == 0 && kTotal <= 232448, "shared memory");
-    static_assert(kStages * kStage >= 16 * kMaxSeqs && sizeof(Start) <= 64, "find_start's room, Shape::kPiece");
+    static_assert(kStages * kStage >= 20 * kMaxSeqs && sizeof(Start) <= 80, "find_start's room, Shape::kPiece");
 };
 
 // Of each block of 16 positions of a stage: its first position (-1: absent) and its scales' exponents.
@@ -235,30 +236,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             entry(w, f, 4, next_position, next_page);
         }
         for (;; ++items) {
-            const int at = piece_at(items);
-            RowsPiece &piece = pieces[at];
-            mbar_wait(piece_free(at), piece_phase(items) ^ 1, status);
-            if (lane == 0) {
-                piece.n = w.n;
-                if (w.n) {
-                    piece.t0 = f.t0;
-                    piece.lo = f.lo, piece.hi = f.hi;
-                    piece.tokens = w.b.i1 - w.b.i0, piece.token0 = f.token0, piece.p0 = f.p0;
-                    piece.head = w.head;
-                    piece.whole = w.whole();
-                    if (!w.whole()) {
-                        piece.c_first = range_owner(s0.total, s0.ctas, w.item + a.g.item);
-                        piece.c_last = range_owner(s0.total, s0.ctas, w.item + item_units(w.b, a.g.item) - 1);
+            // (after the first tile's copies have been issued: all of it is needed at once)
+            auto publish = [&] {
+                const int at = piece_at(items);
+                RowsPiece &piece = pieces[at];
+                mbar_wait(piece_free(at), piece_phase(items) ^ 1, status);
+                if (lane == 0) {
+                    piece.n = w.n;
+                    if (w.n) {
+                        piece.t0 = f.t0;
+                        piece.lo = f.lo, piece.hi = f.hi;
+                        piece.tokens = w.b.i1 - w.b.i0, piece.token0 = f.token0, piece.p0 = f.p0;
+                        piece.head = w.head;
+                        piece.whole = w.whole();
+                        if (!w.whole()) {
+                            piece.c_first = range_owner(s0.total, s0.ctas, w.item + a.g.item);
+                            piece.c_last = range_owner(s0.total, s0.ctas, w.item + item_units(w.b, a.g.item) - 1);
+                        }
                     }
+                    // (the group's heads of a token lie one behind the other)
+                    mbar_arrive_expect_tx(piece_full(at), w.n ? piece.tokens * q_bytes : 0u);
                 }
-                // (the group's heads of a token lie one behind the other)
-                mbar_arrive_expect_tx(piece_full(at), w.n ? piece.tokens * q_bytes : 0u);
+                __syncwarp();
+                if (w.more() && lane < w.b.i1 - w.b.i0 && QDQ_CHECK(status, f.token0 + lane < a.n_tokens && (lane + 1) * q_bytes <= L::kQSize))
+                    bulk_g2s(sb + L::kQ + at * L::kQSize + lane * q_bytes,
+                             a.q + (int64_t)(f.token0 + lane) * a.q_stride + (int64_t)w.head * a.g.group * HD, q_bytes, piece_full(at));
+            };
+            if (!w.more()) {
+                publish();
+                break;
             }
-            __syncwarp();
-            if (!w.more()) break;
-            if (lane < w.b.i1 - w.b.i0 && QDQ_CHECK(status, f.token0 + lane < a.n_tokens && (lane + 1) * q_bytes <= L::kQSize))
-                bulk_g2s(sb + L::kQ + at * L::kQSize + lane * q_bytes,
-                         a.q + (int64_t)(f.token0 + lane) * a.q_stride + (int64_t)w.head * a.g.group * HD, q_bytes, piece_full(at));
             scale(w, position, page);
             for (int j = 0; j < w.n; ++j, ++stage_no) {
                 const int y = j & 3;
@@ -289,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                if (j == 0) publish();
                 if (lane >> 3 == y) {
                     Meta *m = reinterpret_cast<Meta *>(smem + L::kMeta + stage * 64);
                     m->base[lane & 7] = page < 0 ? -1 : position;
@@ -625,34 +633,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool last = *flag != 0;
         named_bar_sync(1, kJoin);
         if (!last) continue;
-        for (int x = tid; x < rows * (HD / 4); x += kJoin) {
-            const int row = x / (HD / 4), dim = x % (HD / 4) * 4;
-            float top = -INFINITY, sum = 0.0f;
-            float4 acc = make_float4(0, 0, 0, 0);
-            constexpr int kAtOnce = 8;
-            for (int cta = w.c_first; cta <= w.c_last; cta += kAtOnce) {
-                float2 ml[kAtOnce];
-                float4 v[kAtOnce];
-#pragma unroll
-                for (int y = 0; y < kAtOnce; ++y) {
-                    const int at = min(cta + y, w.c_last), pt = 2 * at + (at == w.c_first ? 1 : 0);
-                    ml[y] = __ldcg(a.part_ml + pt * kMostRows + row);
-                    v[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + ((int64_t)pt * kMostRows + row) * HD + dim));
+        // (as many loads in flight as there may be parts)
+        auto join = [&](auto at_once) {
+            constexpr int kAtOnce = decltype(at_once)::value;
+            for (int x = tid; x < rows * (HD / 4); x += kJoin) {
+                const int row = x / (HD / 4), dim = x % (HD / 4) * 4;
+                float top = -INFINITY, sum = 0.0f;
+                float4 acc = make_float4(0, 0, 0, 0);
+                for (int cta = w.c_first; cta <= w.c_last; cta += kAtOnce) {
+                    float2 ml[kAtOnce];
+                    float4 v[kAtOnce];
+    #pragma unroll
+                    for (int y = 0; y < kAtOnce; ++y) {
+                        const int at = min(cta + y, w.c_last), pt = 2 * at + (at == w.c_first ? 1 : 0);
+                        ml[y] = __ldcg(a.part_ml + pt * kMostRows + row);
+                        v[y] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + ((int64_t)pt * kMostRows + row) * HD + dim));
+                    }
+    #pragma unroll
+                    for (int y = 0; y < kAtOnce; ++y) {
+                        if (cta + y > w.c_last || ml[y].y == 0.0f) continue;
+                        const float to = fmaxf(top, ml[y].x), h = sum != 0.0f ? ex2(top - to) : 0.0f, f = ex2(ml[y].x - to);
+                        top = to;
+                        sum = fmaf(sum, h, ml[y].y * f);
+                        acc.x = fmaf(v[y].x, f, acc.x * h), acc.y = fmaf(v[y].y, f, acc.y * h);
+                        acc.z = fmaf(v[y].z, f, acc.z * h), acc.w = fmaf(v[y].w, f, acc.w * h);
+                    }
                 }
-#pragma unroll
-                for (int y = 0; y < kAtOnce; ++y) {
-                    if (cta + y > w.c_last || ml[y].y == 0.0f) continue;
-                    const float to = fmaxf(top, ml[y].x), h = sum != 0.0f ? ex2(top - to) : 0.0f, f = ex2(ml[y].x - to);
-                    top = to;
-                    sum = fmaf(sum, h, ml[y].y * f);
-                    acc.x = fmaf(v[y].x, f, acc.x * h), acc.y = fmaf(v[y].y, f, acc.y * h);
-                    acc.z = fmaf(v[y].z, f, acc.z * h), acc.w = fmaf(v[y].w, f, acc.w * h);
-                }
+                const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+                store(row, dim, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                if (dim == 0) store_lse(row, top, sum);
             }
-            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-            store(row, dim, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-            if (dim == 0) store_lse(row, top, sum);
-        }
+        };
+        if (w.c_last - w.c_first < 6) join(std::integral_constant<int, 6>());
+        else join(std::integral_constant<int, 16>());
     }
 }
 

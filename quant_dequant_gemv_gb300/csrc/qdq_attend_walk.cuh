@@ -10,6 +10,7 @@ namespace qdq {
 struct Start {
     long long total, item, pos, end;  // units: of all items, where the first one begins, the CTA's range
     int seq, block, head, ctas, live;
+    int first, count, kv;  // of the sequence: its first row, its rows, its positions
 };
 
 // A walk over the pieces of a CTA's range, by the copying warp.
@@ -28,8 +29,9 @@ struct Walk {
     }
     template <typename A>
     QDQ_DEV Walk(const A &a, const Start &s)
-        : item(s.item), pos(s.pos), end(s.end), seq(s.seq), block(s.block), head(s.head) {
-        load_seq(a);
+        : item(s.item), pos(s.pos), end(s.end), seq(s.seq), block(s.block), head(s.head), first(s.first), count(s.count), kv(s.kv) {
+        blocks = seq_blocks(a.g, count);
+        pages = a.page_table + (int64_t)seq * a.max_pages;
         b = block_of(a.g, count, kv, block);
         int last;
         piece_of(b, item, pos, end, off, last, a.g.item);
@@ -63,11 +65,12 @@ struct Walk {
 };
 
 // Where the CTA's range starts: sums of key tiles per sequence, a scan, and a search.
-// `room`: 16 * kMaxSeqs bytes of shared memory; every one of the CTA's kThreads threads comes here.
+// `room`: 20 * kMaxSeqs bytes of shared memory; every one of the CTA's kThreads threads comes here.
 template <int kThreads, typename A>
 QDQ_DEV void find_start(const A &a, char *room, Start *start) {
     int *cnt = reinterpret_cast<int *>(room), *kvs = cnt + kMaxSeqs;
     long long *pre = reinterpret_cast<long long *>(room + 8 * kMaxSeqs);  // [n_seqs]
+    int *rows = reinterpret_cast<int *>(room + 16 * kMaxSeqs);
     constexpr int kAlone = 8;  // blocks that one thread sums; longer sequences are summed by a warp
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool longer = false;
@@ -76,6 +79,7 @@ QDQ_DEV void find_start(const A &a, char *room, Start *start) {
         seq_tokens(a.q_start, s, a.n_tokens, first, count);
         const int kv = max(a.kv_len[s], 0), nb = seq_blocks(a.g, count);
         cnt[s] = count;
+        rows[s] = first;
         kvs[s] = kv;
         int sum = 0;
         if (nb <= kAlone) {
@@ -148,6 +152,7 @@ QDQ_DEV void find_start(const A &a, char *room, Start *start) {
                     if (lane == l) {
                         const int r = (int)(rem - (run - own));
                         start->seq = s;
+                        start->first = rows[s], start->count = cnt[s], start->kv = kvs[s];
                         start->block = b0 + l;
                         start->head = r / n;
                         start->item = x - r % n;
