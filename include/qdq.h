@@ -331,8 +331,8 @@ void qdq_llama_destroy(qdq_llama *model);
  * page holds which positions is the caller's to decide: position j of a
  * sequence lives in row j % page_size of page page_table[seq][j / page_size].
  * A handle keeps the geometry, the rotation's frequency table and the attention's
- * workspace (all device memory it needs, 1024 bytes x SMs x head_dim x 2 and a little:
- * 40 MB at 128 dims; the calls allocate nothing).
+ * workspace (all device memory it needs, 1152 bytes x SMs x head_dim x 2 and a little:
+ * 45 MB at 128 dims; the calls allocate nothing).
  *
  * A step's batch (all arrays int32 on the device, 4-byte aligned, read when the
  * kernels run, so a captured graph replays with their new contents):
@@ -459,7 +459,8 @@ int qdq_paged_attention(qdq_paged *cache, int layer, const qdq_paged_batch *batc
  * qdq_paged_attention_pages: as qdq_paged_attention without a window, over the positions up to
  * the token's own that lie in the listed pages: pages as above. An entry counts if it is not
  * negative and larger than the one before it. A token with nothing to attend to gets a zero row
- * and lse = -inf. The weights meet the values in two terms. Uses the handle's workspace.
+ * and lse = -inf. The weights meet the values in two terms. An attention call of its handle: it uses
+ * the workspace, and must not overlap with another.
  * ------------------------------------------------------------------------- */
 int qdq_paged_key_bounds(qdq_paged *cache, int layer, const qdq_paged_batch *batch, int8_t *bounds, uint8_t *scales,
                          qdq_stream_t stream);

@@ -452,6 +452,25 @@ def test_select_one_token_over_many_pages(qdq):
     check_select(qdq, b, 1, 0, 0)
 
 
+@pytest.mark.parametrize("dtype,dim,heads", [("e4m3", 128, 8), ("bf16", 64, 36), ("f16", 128, 4)])
+def test_select_many_items(qdq, dtype, dim, heads):
+    """More tokens and heads than SMs: several share one."""
+    lens = [(1, int(x)) for x in np.random.default_rng(5).integers(0, 900, 60)]
+    b = make(qdq, lens, heads, 4, dim, 16, dtype, seed=4)
+    for n in (1, 20):
+        check_select(qdq, b, n, 0, 1)
+
+
+def test_select_as_many_pages_as_there_may_be(qdq):
+    """32768 entries of a table over a few pages: thousands of equal scores."""
+    b = make(qdq, [(1, 200), (1, 40)], 2, 1, 64, 16, seed=1)
+    b["table"] = b["rng"].integers(-1, b["n_pages"], (2, 32768)).astype(np.int32)
+    b["kv_len"] = np.array([32768 * 16, 20000 * 16 - 3], np.int32)
+    b["batch"] = batch_of(qdq, b)
+    for n in (7, 5000):
+        check_select(qdq, b, n, 1, 2)
+
+
 def test_select_ties_and_absent_pages(qdq):
     """Equal scores take the lowest pages; absent pages and negative positions none."""
     b = make(qdq, [(1, 4000), (1, 900), (9, 0), (2, 500), (1, 100)], 4, 2, 64, 16, seed=2)
