@@ -61,7 +61,7 @@
 // goes into the scores' factor, and with the values' 2^e the weight that meets them is 2^(t + e - m),
 // m the maximum of t + e, l the sum of those weights times 2^-e. (Block by block in the softmax, as in
 // qdq_attend_rows.cu, which takes the batches of few rows, the 8191 tokens took 530 us with two
-// widening warps; so 522 with four.) Shared memory bounds it: a tile of both sets reads 192 KB of
+// widening warps; so 522 with four.) By count shared memory bounds it: a tile of both sets reads 192 KB of
 // operands and moves 128 KB to be widened, about 100 bytes a clock at 522 us, 1.05 PFLOP/s; ragged
 // pieces of 11 to 642 tokens take 104 us.
 #include <cmath>
