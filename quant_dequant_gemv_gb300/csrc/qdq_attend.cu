@@ -61,9 +61,9 @@
 // goes into the scores' factor, and with the values' 2^e the weight that meets them is 2^(t + e - m),
 // m the maximum of t + e, l the sum of those weights times 2^-e. (Block by block in the softmax, as in
 // qdq_attend_rows.cu, which takes the batches of few rows, the 8191 tokens took 530 us with two
-// widening warps; so 522 with four.) By count shared memory bounds it: a tile of both sets reads 192 KB of
-// operands and moves 128 KB to be widened, about 100 bytes a clock at 522 us, 1.05 PFLOP/s; ragged
-// pieces of 11 to 642 tokens take 104 us.
+// widening warps; so 490 with four, 1.12 PFLOP/s; ragged pieces of 11 to 642 tokens 104.) The widening
+// bounds it (with a quarter of it done 425 us): its instructions, and shared memory, of which a tile of
+// both sets reads 192 KB of operands and moves 128 KB to be widened.
 #include <cmath>
 #include <cuda.h>
 #include <limits>
@@ -200,18 +200,20 @@ QDQ_DEV float max3(float a, float b, float c) {
 }
 
 // KV8, bytes to fp16: the warp's kTileN / kWiden positions of each tile. A lane takes 16 bytes of a row, which
-// are two 16-byte pieces of the widened row; 8 lanes store to 8 different places of the swizzle at once
-// (of 128 dims, the upper half's lanes store their second piece first).
+// are two 16-byte pieces of the widened row. Eight lanes that go to shared memory together have four
+// pieces of each of two neighbouring rows (of 128 dims, the other half of the second one): they read 128
+// bytes of different banks, and store to the eight places of the swizzle.
 template <int HD>
 QDQ_DEV void widen(char *smem, const Piece *pieces, int mine, int *status) {
     using L = Shape<HD, true>;
     constexpr int kChunks = HD / 16, kRows = 32 / kChunks;  // lanes of a row, rows at once
-    constexpr int kDeep = 2;                                 // loads in flight
+    constexpr int kDeep = HD == 128 ? 4 : 2;                 // loads in flight
     const uint32_t sb = smem_u32(smem);
     auto bar = [&](int i) { return sb + L::kBars + 8u * i; };
-    const int lane = threadIdx.x & 31, chunk = lane % kChunks, sub = lane / kChunks;
-    const bool swap = HD == 128 && chunk >= 4;
-    const uint32_t c = (2 * chunk) & 7, c_first = c + (swap ? 1 : 0), c_second = c + (swap ? 0 : 1);
+    const int lane = threadIdx.x & 31;
+    const int sub = HD == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane / kChunks;
+    const int chunk = HD == 128 ? (lane & 3) | (((lane >> 2) ^ (lane >> 3)) & 1) << 2 : lane % kChunks;
+    const uint32_t piece = (2 * chunk) & 7;
     uint32_t seq_no = 0;
     for (uint32_t items = 0;; ++items) {
         mbar_wait(bar(kBarPiece + (items & 1)), (items >> 1) & 1, status);
@@ -233,21 +235,25 @@ QDQ_DEV void widen(char *smem, const Piece *pieces, int mine, int *status) {
 #pragma unroll
                 for (int y = 0; y < kDeep; ++y) v[y] = lds128(from + (r0 + y * kRows + sub) * HD);
                 const __half2 by = __half2half2(__ushort_as_half(times[r0 / 16]));
-                const uint32_t live = note.rows[r0 / 16] >> (r0 % 16);
+                const uint32_t rows = note.rows[r0 / 16];
+                if (rows != 0xFFFFu) {
+#pragma unroll
+                    for (int y = 0; y < kDeep; ++y)
+                        if (!((rows >> (r0 % 16 + y * kRows + sub)) & 1)) v[y] = make_uint4(0, 0, 0, 0);
+                }
                 static_assert(16 % (kDeep * kRows) == 0, "one block at a time");
 #pragma unroll
                 for (int y = 0; y < kDeep; ++y) {
                     const int r = r0 + y * kRows + sub;
-                    if (!((live >> (y * kRows + sub)) & 1)) v[y] = make_uint4(0, 0, 0, 0);
                     uint4 f, g;
-                    e4m3x4_to_f16(swap ? v[y].z : v[y].x, f.x, f.y);
-                    e4m3x4_to_f16(swap ? v[y].w : v[y].y, f.z, f.w);
-                    e4m3x4_to_f16(swap ? v[y].x : v[y].z, g.x, g.y);
-                    e4m3x4_to_f16(swap ? v[y].y : v[y].w, g.z, g.w);
+                    e4m3x4_to_f16(v[y].x, f.x, f.y);
+                    e4m3x4_to_f16(v[y].y, f.z, f.w);
+                    e4m3x4_to_f16(v[y].z, g.x, g.y);
+                    e4m3x4_to_f16(v[y].w, g.z, g.w);
                     auto scaled = [&](uint32_t &u) { *reinterpret_cast<__half2 *>(&u) = __hmul2(*reinterpret_cast<__half2 *>(&u), by); };
                     scaled(f.x), scaled(f.y), scaled(f.z), scaled(f.w), scaled(g.x), scaled(g.y), scaled(g.z), scaled(g.w);
                     const uint32_t row = to + (r >> 3) * L::kGroup8 + (r & 7) * 128;
-                    const uint32_t first = row + ((c_first ^ (r & 7)) << 4), second = row + ((c_second ^ (r & 7)) << 4);
+                    const uint32_t first = row + ((piece ^ (r & 7)) << 4), second = first ^ 16;
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(first), "r"(f.x), "r"(f.y), "r"(f.z), "r"(f.w) : "memory");
                     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(second), "r"(g.x), "r"(g.y), "r"(g.z), "r"(g.w) : "memory");
                 }
