@@ -283,19 +283,20 @@ __global__ void __launch_bounds__(FEW ? 512 : 256, FEW ? 1 : 3) select_kernel(co
     };
     // the step at j0 (its pages are in `next`)
     auto fetch = [&](int j0, Bounds &to) {
-        if (j0 >= pages) return;
+        if (j0 < pages) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            to.page[y] = (unsigned)next[y] < (unsigned)a.n_pages ? next[y] : -1;
-            const int64_t unit = (int64_t)max(to.page[y], 0) * a.n_kv_heads + head;
-            const int8_t *from = a.bounds + unit * 2 * D + 16 * c;
+            for (int y = 0; y < 2; ++y) {
+                to.page[y] = (unsigned)next[y] < (unsigned)a.n_pages ? next[y] : -1;
+                const int64_t unit = (int64_t)max(to.page[y], 0) * a.n_kv_heads + head;
+                const int8_t *from = a.bounds + unit * 2 * D + 16 * c;
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
+                for (int z = 0; z < 2; ++z)
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) to.b[y][z][i] = __ldg(reinterpret_cast<const uint4 *>(from + z * D + 64 * i));
-            to.e[y] = a.bound_scales[unit] - 127;
+                    for (int i = 0; i < kLoads; ++i) to.b[y][z][i] = __ldg(reinterpret_cast<const uint4 *>(from + z * D + 64 * i));
+                to.e[y] = a.bound_scales[unit] - 127;
+            }
+            pages_at(j0 + stride);
         }
-        pages_at(j0 + stride);
     };
     pages_at(j0);
     fetch(j0, ahead);
