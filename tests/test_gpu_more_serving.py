@@ -675,3 +675,51 @@ def test_refusals_on_the_device(qdq):
         c.select_pages(0, wide, q, bounds, scales, lists)
     torch.cuda.synchronize()
     assert qdq.get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16"])
+def test_pages_past_four_gigabytes(qdq, dtype):
+    """The same batch in a small cache and in the last pages of a pool of over 4 GB: the same bits."""
+    H, G, D, page = 8, 8, 128, 64
+    lens = [(1, 700), (40, 100), (1, 0)]
+    b = make(qdq, lens, H, G, D, page, dtype, seed=2)
+    fill_held(b)
+    far = 33000 if dtype == "bf16" else 66000
+    assert far * page * G * D * b["pools"].element_size() > 1 << 32
+    pools = torch.zeros(2, 2, far, *b["pools"].shape[3:], dtype=b["pools"].dtype, device="cuda")
+    pools[:, 1, far - b["n_pages"]:] = b["pools"][:, 0]
+    more = {}
+    if dtype == "e4m3":
+        scales = torch.zeros(2, 2, far, G, page // 16, dtype=torch.uint8, device="cuda")
+        scales[:, 1, far - b["n_pages"]:] = b["scales"][:, 0]
+        more = dict(k_scales=scales[0], v_scales=scales[1])
+    big = qdq.PagedCache(*(pools.view(torch.float8_e4m3fn) if more else pools), H, **more)
+    table = b["batch"]._keep[2]
+    there = qdq.PagedBatch(*b["batch"]._keep[:2], torch.where(table >= 0, table + (far - b["n_pages"]), table), b["tokens"])
+    T = b["tokens"]
+    x = torch.from_numpy(b["rng"].standard_normal((T, (H + 2 * G) * D))).float().cuda()
+    q, k, v = x.split([H * D, G * D, G * D], dim=1)
+    got = []
+    for cache, batch, layer, n in ((b["cache"], b["batch"], 0, b["n_pages"]), (big, there, 1, far)):
+        q16 = torch.zeros(T, H * D, dtype=DT[b["q_dtype"]], device="cuda")
+        bounds = torch.zeros(layer + 1, n, G, 2, D, dtype=torch.int8, device="cuda")
+        bound_scales = torch.zeros(layer + 1, n, G, dtype=torch.uint8, device="cuda")
+        lists = torch.zeros(T, G, 4, dtype=torch.int32, device="cuda")
+        outs = [torch.zeros(T, H * D, device="cuda") for _ in range(2)]
+        cache.append(layer, batch, q, k, v, q16)
+        cache.key_bounds(layer, batch, bounds, bound_scales)
+        cache.select_pages(layer, batch, q16, bounds, bound_scales, lists)
+        cache.attention(layer, batch, q16, outs[0])
+        cache.attention_pages(layer, batch, q16, lists, outs[1])
+        got.append((q16, bounds[layer, -b["n_pages"]:], lists, *outs))
+    assert qdq.get_device_status() == 0
+    assert all(torch.equal(a, c) for a, c in zip(*got))
+    assert torch.equal(pools[:, 1, far - b["n_pages"]:].view(torch.uint8), b["pools"][:, 0].view(torch.uint8))
+
+
+def test_attention_pages_of_a_prompt_piece(qdq):
+    """Hundreds of tokens, each with a list of its own."""
+    for dtype in ("e4m3", "f16"):
+        b = make(qdq, [(150, 60), (1, 300), (0, 5), (33, 0)], 8, 2, 64, 16, dtype, seed=5, extra_tokens=3)
+        fill_held(b)
+        check_attention(qdq, b, lists=random_lists(b, 7, b["rng"]))
